@@ -35,6 +35,8 @@
  *     contents are a precondition (check them with rmoe_validate_contract).
  *     A device fault shows at the caller's next synchronisation.
  *   - fp16 is IEEE binary16 (passed as void*), fp32 is float, tables int32.
+ *   - MXFP4 (the rmoe_*_mxfp4 entries) is the microscaled 4-bit format
+ *     described at rmoe_quantize_mxfp4.
  */
 #ifndef ROUTED_MOE_H
 #define ROUTED_MOE_H
@@ -420,6 +422,120 @@ RMOE_API int rmoe_build_contract_device_noalloc(const int32_t *topk_ids, int64_t
 RMOE_API int rmoe_router_f16(const void *x, const void *router_w, int64_t num_tokens,
                              int64_t hidden, int32_t num_experts, int32_t top_k,
                              int32_t *topk_ids, float *topk_weights, void *stream);
+
+/*
+ * MXFP4: microscaled 4-bit floating point.  A row of `cols` elements is cut
+ * into blocks of 32; a block shares the scale 2^(b - 127), held as its
+ * exponent byte b, and each element is an E2M1 code (sign bit, then the
+ * magnitudes 0 0.5 1 1.5 2 3 4 6): 4.25 bits per element.
+ *   b = max(0, floor(log2(amax)) - 2 + 127), amax the block's largest
+ *   magnitude; an element's code is element / 2^(b - 127) rounded to the
+ *   nearest, ties to the even code, magnitudes above 6 to 6 (amax lands in
+ *   [4, 8)).  A block of zeros has b = 0.  A block that holds an infinity or
+ *   a NaN has b = 255, the format's NaN, and codes 0: every product with it
+ *   is NaN.
+ * Layout of [batch, rows, cols]:
+ *   codes  [batch, rows, row bytes]: row bytes = rmoe_mxfp4_row_bytes(cols)
+ *          = 128 * ceil(cols / 256), two codes per byte, the even element in
+ *          the low nibble; elements past cols are zero codes;
+ *   scales [batch, chunks, rows, 8]: chunks = ceil(cols / 256); the 8 bytes
+ *          of a (chunk, row) belong to the chunk's blocks in the order
+ *          0 2 4 6 1 3 5 7 (blocks past cols: 0).  A matrix of scale bytes
+ *          [rows, chunks * 8] in plain block order becomes this layout by
+ *          viewing it as [rows, chunks, 4, 2], swapping the last two axes and
+ *          moving chunks first.
+ */
+#define RMOE_TYPE_F16 0
+#define RMOE_TYPE_BF16 1
+#define RMOE_TYPE_F32 2
+
+/* Chunks of a row; bytes of its codes; of a matrix's codes; of its scales.  0
+ * for sizes that are not positive. */
+RMOE_API int64_t rmoe_mxfp4_chunks(int64_t cols);
+RMOE_API int64_t rmoe_mxfp4_row_bytes(int64_t cols);
+RMOE_API size_t rmoe_mxfp4_code_bytes(int64_t rows, int64_t cols);
+RMOE_API size_t rmoe_mxfp4_scale_bytes(int64_t rows, int64_t cols);
+
+/*
+ * Quantise x [batch, rows, cols] of element type RMOE_TYPE_* to MXFP4: expert
+ * matrices [E, N, K] once when a model is loaded (batch E: each expert's
+ * scales are laid out by themselves), or token rows (batch 1).
+ * cols a positive multiple of 8 (a last block shorter than 32 is allowed);
+ * batch * rows * chunks at most 2^31 - 1 (RMOE_ERR_UNSUPPORTED_SHAPE).  x and
+ * codes 16-byte, scales 8-byte aligned (RMOE_ERR_MISALIGNED); the three must
+ * not overlap.  One launch on `stream`.
+ */
+RMOE_API int rmoe_quantize_mxfp4(const void *x, int32_t type, int64_t batch, int64_t rows, int64_t cols,
+                                 void *codes, void *scales, void *stream);
+
+/*
+ * The inverse: y [batch, rows, cols] of element type RMOE_TYPE_* = the values
+ * the codes stand for, rounded once to the type (exact in fp32; in fp16 a
+ * value above 65504 becomes an infinity).  Blocks with scale byte 255 give
+ * NaN.  Sizes, alignment (y as x) and errors as rmoe_quantize_mxfp4.
+ */
+RMOE_API int rmoe_dequantize_mxfp4(const void *codes, const void *scales, int32_t type, int64_t batch,
+                                   int64_t rows, int64_t cols, void *y, void *stream);
+
+/*
+ * rmoe_pack_f16 that quantises on the way: token t's row of x [num_tokens,
+ * hidden] fp16 is read and quantised once (as rmoe_quantize_mxfp4) and
+ * written to its top_k padded rows of codes [Tp, row bytes] and scales
+ * [chunks, Tp, 8], Tp = total_padded_tokens; w_compact as in rmoe_pack_f16.
+ * Pairs with table entries out of range move nothing; other rows are not
+ * written.  hidden a multiple of 8; num_tokens * chunks at most 2^31 - 1.
+ */
+RMOE_API int rmoe_pack_mxfp4_f16(const void *x, const float *topk_weights,
+                                 const int32_t *padded_row_of_pair, const int32_t *compact_pos_of_pair,
+                                 int64_t num_tokens, int32_t top_k, int64_t hidden, void *codes,
+                                 void *scales, float *w_compact, int64_t total_padded_tokens,
+                                 void *stream);
+
+/*
+ * The routed expert FFN on MXFP4 tokens and weights, fp32 accumulation:
+ *   gate = x . gate_w[e]^T, up = x . up_w[e]^T on the values the codes stand
+ *   for; hidden = mxfp4( silu(gate) * up ), quantised from fp32 without an
+ *   fp16 rounding between; out = fp16( (hidden . down_w[e]^T) * w ).
+ * Tokens: codes [Tp, row bytes(H)] and scales [chunks(H), Tp, 8]
+ * (rmoe_pack_mxfp4_f16); gate_w, up_w: [E, I, H], down_w: [E, H, I], each as
+ * codes and scales of a batch of E matrices (rmoe_quantize_mxfp4); tables,
+ * routed weights, out and sizes as rmoe_forward_f16_variant.  workspace:
+ * rmoe_mxfp4_workspace_bytes(Tp, I) bytes, the hidden rows' codes [Tp, row
+ * bytes(I)] followed by their scales [chunks(I), Tp, 8]; contents irrelevant
+ * on entry.  Only valid rows of out and of the workspace are written.
+ * variant: RMOE_VARIANT_STREAM or _TILE, or _AUTO for the choice of
+ * rmoe_pick_variant_mxfp4.  Codes, scales and workspace 16-byte aligned.  Two
+ * launches on `stream`.
+ */
+RMOE_API size_t rmoe_mxfp4_workspace_bytes(int64_t total_padded_tokens, int64_t intermediate);
+RMOE_API int rmoe_pick_variant_mxfp4(int32_t variant, int64_t num_pairs, int32_t num_experts);
+RMOE_API int rmoe_forward_mxfp4(const void *token_codes, const void *token_scales,
+                                const void *gate_codes, const void *gate_scales, const void *up_codes,
+                                const void *up_scales, const void *down_codes, const void *down_scales,
+                                const float *routed_expert_weights, const int32_t *group_sizes,
+                                const int32_t *group_offsets, const int32_t *group_padded_offsets,
+                                const int32_t *group_idx_for_bx, void *workspace, void *out,
+                                int64_t hidden, int64_t intermediate, int32_t num_experts,
+                                int64_t total_padded_tokens, int64_t total_valid_tokens,
+                                int32_t num_blocks_m, int32_t variant, void *stream);
+
+/* Its stages alone.  rmoe_gate_up_mxfp4 writes the hidden rows' codes and
+ * scales, rmoe_down_mxfp4 reads them. */
+RMOE_API int rmoe_gate_up_mxfp4(const void *token_codes, const void *token_scales,
+                                const void *gate_codes, const void *gate_scales, const void *up_codes,
+                                const void *up_scales, const int32_t *group_sizes,
+                                const int32_t *group_padded_offsets, const int32_t *group_idx_for_bx,
+                                void *hidden_codes, void *hidden_scales, int64_t hidden,
+                                int64_t intermediate, int32_t num_experts, int64_t total_padded_tokens,
+                                int64_t total_valid_tokens, int32_t num_blocks_m, int32_t variant,
+                                void *stream);
+RMOE_API int rmoe_down_mxfp4(const void *hidden_codes, const void *hidden_scales, const void *down_codes,
+                             const void *down_scales, const float *routed_expert_weights,
+                             const int32_t *group_sizes, const int32_t *group_offsets,
+                             const int32_t *group_padded_offsets, const int32_t *group_idx_for_bx,
+                             void *out, int64_t hidden, int64_t intermediate, int32_t num_experts,
+                             int64_t total_padded_tokens, int64_t total_valid_tokens,
+                             int32_t num_blocks_m, int32_t variant, void *stream);
 
 #ifdef __cplusplus
 }

@@ -62,6 +62,18 @@ _SIGS = {
     "rmoe_router_f16": ([_P, _P, _I64, _I64, _I32, _I32, _P, _P, _P], ctypes.c_int),
     "rmoe_build_contract_device": ([_P, _I64, _I32, _I32, _P, _P, _P, _P, _I64, _P, _P, _P, _P, _P,
                                     _P, ctypes.c_size_t, _P], ctypes.c_int),
+    "rmoe_mxfp4_chunks": ([_I64], _I64),
+    "rmoe_mxfp4_row_bytes": ([_I64], _I64),
+    "rmoe_mxfp4_code_bytes": ([_I64, _I64], ctypes.c_size_t),
+    "rmoe_mxfp4_scale_bytes": ([_I64, _I64], ctypes.c_size_t),
+    "rmoe_mxfp4_workspace_bytes": ([_I64, _I64], ctypes.c_size_t),
+    "rmoe_quantize_mxfp4": ([_P, _I32, _I64, _I64, _I64, _P, _P, _P], ctypes.c_int),
+    "rmoe_dequantize_mxfp4": ([_P, _P, _I32, _I64, _I64, _I64, _P, _P], ctypes.c_int),
+    "rmoe_pack_mxfp4_f16": ([_P] * 4 + [_I64, _I32, _I64, _P, _P, _P, _I64, _P], ctypes.c_int),
+    "rmoe_pick_variant_mxfp4": ([_I32, _I64, _I32], ctypes.c_int),
+    "rmoe_forward_mxfp4": ([_P] * 15 + [_I64, _I64, _I32, _I64, _I64, _I32, _I32, _P], ctypes.c_int),
+    "rmoe_gate_up_mxfp4": ([_P] * 11 + [_I64, _I64, _I32, _I64, _I64, _I32, _I32, _P], ctypes.c_int),
+    "rmoe_down_mxfp4": ([_P] * 10 + [_I64, _I64, _I32, _I64, _I64, _I32, _I32, _P], ctypes.c_int),
     "rmoe_contract_noalloc_max_words": ([], ctypes.c_size_t),
     "rmoe_build_contract_device_noalloc": ([_P, _I64, _I32, _I32, _P, _P, _P, _P, _I64, _P, _P, _P,
                                             _P, _P, _P], ctypes.c_int),
@@ -517,6 +529,259 @@ def build_contract_device_noalloc(topk_ids, num_experts: int, out: dict, stream=
     _check(st, "rmoe_build_contract_device_noalloc")
     out["num_blocks_m"] = nb.value
     return out
+
+
+# ------------------------------------------------------------- MXFP4
+def _same_device(first, **tensors):
+    """The tensors live on ``first``'s device; returns a context in which
+    that device is current (a launch goes to the current device)."""
+    torch = _torch()
+    for name, t in tensors.items():
+        if isinstance(t, torch.Tensor) and t.is_cuda and t.device != first.device:
+            raise ValueError(f"{name} is on {t.device}, not on {first.device}")
+    return torch.cuda.device(first.device)
+
+
+def _shape(t, shape, name):
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+
+
+def _empty(shape, dtype, device, stream):
+    """An uninitialised tensor that belongs to ``stream`` (default: the
+    current one), so its memory is not handed out again before that stream
+    is done with it."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _mx_type(dtype):
+    torch = _torch()
+    types = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
+    if dtype not in types:
+        raise TypeError(f"MXFP4 converts float16, bfloat16 and float32, not {dtype}")
+    return types[dtype]
+
+
+def mxfp4_row_bytes(cols: int) -> int:
+    """Bytes of one row of MXFP4 codes, whole chunks of 256 elements."""
+    return int(lib().rmoe_mxfp4_row_bytes(int(cols)))
+
+
+def mxfp4_shapes(shape) -> tuple[tuple, tuple]:
+    """Shapes of the uint8 ``codes`` and ``scales`` of a matrix [rows, cols]
+    or a batch of them [batch, rows, cols] (layout: rmoe_quantize_mxfp4)."""
+    if len(shape) not in (2, 3):
+        raise ValueError("MXFP4 tensors are [rows, cols] or [batch, rows, cols]")
+    *batch, rows, cols = (int(n) for n in shape)
+    return (*batch, rows, mxfp4_row_bytes(cols)), (*batch, int(lib().rmoe_mxfp4_chunks(cols)), rows, 8)
+
+
+def quantize_mxfp4(x, codes=None, scales=None, stream=None):
+    """MXFP4 of ``x`` [rows, cols] or [batch, rows, cols] (fp16, bf16 or fp32;
+    cols a multiple of 8): returns ``(codes, scales)``, uint8 tensors of
+    ``mxfp4_shapes(x.shape)`` (allocated unless given)."""
+    torch = _torch()
+    px, ty = _dev(x, x.dtype, "x"), _mx_type(x.dtype)
+    cs, ss = mxfp4_shapes(x.shape)
+    if codes is None:
+        codes = _empty(cs, torch.uint8, x.device, stream)
+    if scales is None:
+        scales = _empty(ss, torch.uint8, x.device, stream)
+    _shape(codes, cs, "codes")
+    _shape(scales, ss, "scales")
+    batch = x.shape[0] if x.dim() == 3 else 1
+    with _same_device(x, codes=codes, scales=scales):
+        st = lib().rmoe_quantize_mxfp4(px, ty, batch, x.shape[-2], x.shape[-1],
+                                       _dev(codes, torch.uint8, "codes"),
+                                       _dev(scales, torch.uint8, "scales"), _stream(x, stream))
+    _check(st, "rmoe_quantize_mxfp4")
+    return codes, scales
+
+
+def dequantize_mxfp4(codes, scales, cols: int, dtype=None, out=None, stream=None):
+    """The values of MXFP4 ``codes`` and ``scales`` of rows of ``cols``
+    elements, as ``dtype`` (default fp16), in ``out`` if given."""
+    torch = _torch()
+    if out is not None and dtype is not None and out.dtype != dtype:
+        raise TypeError(f"out must be {dtype}, got {out.dtype}")
+    dtype = out.dtype if out is not None else torch.float16 if dtype is None else dtype
+    ty = _mx_type(dtype)
+    shape = (*codes.shape[:-1], int(cols))
+    cs, ss = mxfp4_shapes(shape)
+    _shape(codes, cs, "codes")
+    _shape(scales, ss, "scales")
+    pc, ps = _dev(codes, torch.uint8, "codes"), _dev(scales, torch.uint8, "scales")
+    if out is None:
+        out = _empty(shape, dtype, codes.device, stream)
+    _shape(out, shape, "out")
+    batch = shape[0] if len(shape) == 3 else 1
+    with _same_device(codes, scales=scales, out=out):
+        st = lib().rmoe_dequantize_mxfp4(pc, ps, ty, batch, shape[-2], shape[-1], _dev(out, dtype, "out"),
+                                         _stream(codes, stream))
+    _check(st, "rmoe_dequantize_mxfp4")
+    return out
+
+
+def pack_mxfp4(x, topk_weights, padded_row_of_pair, compact_pos_of_pair, codes, scales, w_compact,
+               stream=None):
+    """``pack`` that quantises: each fp16 token row is quantised once and its
+    codes and scales are written to its padded rows of ``codes`` [Tp, row
+    bytes] and ``scales`` [chunks, Tp, 8]."""
+    torch = _torch()
+    T, H = x.shape
+    pairs = topk_weights.numel()
+    k = pairs // T if T else 0
+    if k * T != pairs or padded_row_of_pair.numel() != pairs or compact_pos_of_pair.numel() != pairs or \
+            w_compact.numel() != pairs:
+        raise ValueError("topk_weights, the pair tables and w_compact must have num_tokens * top_k entries")
+    Tp = codes.shape[0]
+    cs, ss = mxfp4_shapes((Tp, H))
+    _shape(codes, cs, "codes")
+    _shape(scales, ss, "scales")
+    with _same_device(x, topk_weights=topk_weights, padded_row_of_pair=padded_row_of_pair,
+                      compact_pos_of_pair=compact_pos_of_pair, codes=codes, scales=scales,
+                      w_compact=w_compact):
+        st = lib().rmoe_pack_mxfp4_f16(
+            _dev(x, torch.float16, "x"), _dev(topk_weights, torch.float32, "topk_weights"),
+            _dev(padded_row_of_pair, torch.int32, "padded_row_of_pair"),
+            _dev(compact_pos_of_pair, torch.int32, "compact_pos_of_pair"), T, k, H,
+            _dev(codes, torch.uint8, "codes"), _dev(scales, torch.uint8, "scales"),
+            _dev(w_compact, torch.float32, "w_compact"), Tp, _stream(x, stream))
+    _check(st, "rmoe_pack_mxfp4_f16")
+
+
+def mxfp4_workspace_bytes(total_padded_tokens: int, intermediate: int) -> int:
+    """Bytes of ``forward_mxfp4``'s workspace (the hidden rows' codes, then
+    their scales)."""
+    return int(lib().rmoe_mxfp4_workspace_bytes(int(total_padded_tokens), int(intermediate)))
+
+
+def pick_variant_mxfp4(num_pairs: int, num_experts: int, variant="auto") -> str:
+    """The kernel family of the MXFP4 forward for a batch."""
+    v = int(lib().rmoe_pick_variant_mxfp4(_VARIANTS[variant], int(num_pairs), int(num_experts)))
+    _check(min(v, 0), "rmoe_pick_variant_mxfp4")
+    return _VARIANT_NAMES[v]
+
+
+def _tables(E, M, group_sizes, group_padded_offsets, group_idx_for_bx, group_offsets=None):
+    """Device pointers of the contract's tables after their sizes' check."""
+    i32 = _torch().int32
+    if group_sizes.numel() != E or group_padded_offsets.numel() != E + 1 or \
+            (group_offsets is not None and group_offsets.numel() != E + 1):
+        raise ValueError("group tables must have E, E+1, E+1 entries")
+    out = [_dev(group_sizes, i32, "group_sizes")]
+    if group_offsets is not None:
+        out.append(_dev(group_offsets, i32, "group_offsets"))
+    return out + [_dev(group_padded_offsets, i32, "group_padded_offsets"),
+                  _dev(group_idx_for_bx, i32, "group_idx_for_bx")]
+
+
+def forward_mxfp4(token_codes, token_scales, gate_codes, gate_scales, up_codes, up_scales, down_codes,
+                  down_scales, routed_expert_weights, group_sizes, group_offsets,
+                  group_padded_offsets, group_idx_for_bx, workspace, out, variant="auto", stream=None):
+    """The routed expert FFN on MXFP4 tokens (``pack_mxfp4``) and weights
+    (``quantize_mxfp4`` of [E, I, H], [E, I, H] and [E, H, I]); the hidden
+    rows between the two products are MXFP4 too.  ``workspace``: uint8, at
+    least ``mxfp4_workspace_bytes(Tp, I)``; ``out`` [Tp, H] fp16, valid rows
+    written.  Asynchronous on ``stream``."""
+    torch = _torch()
+    u8 = torch.uint8
+    Tp, H = out.shape
+    E, I = gate_codes.shape[:2]
+    for name, c, s, shape in (("token", token_codes, token_scales, (Tp, H)),
+                              ("gate", gate_codes, gate_scales, (E, I, H)),
+                              ("up", up_codes, up_scales, (E, I, H)),
+                              ("down", down_codes, down_scales, (E, H, I))):
+        cs, ss = mxfp4_shapes(shape)
+        _shape(c, cs, f"{name}_codes")
+        _shape(s, ss, f"{name}_scales")
+    if workspace.numel() < mxfp4_workspace_bytes(Tp, I):
+        raise ValueError("workspace too small")
+    M = group_idx_for_bx.numel()
+    with _same_device(out, token_codes=token_codes, token_scales=token_scales, gate_codes=gate_codes,
+                      gate_scales=gate_scales, up_codes=up_codes, up_scales=up_scales,
+                      down_codes=down_codes, down_scales=down_scales, workspace=workspace,
+                      routed_expert_weights=routed_expert_weights, group_sizes=group_sizes,
+                      group_offsets=group_offsets, group_padded_offsets=group_padded_offsets,
+                      group_idx_for_bx=group_idx_for_bx):
+        st = lib().rmoe_forward_mxfp4(
+            _dev(token_codes, u8, "token_codes"), _dev(token_scales, u8, "token_scales"),
+            _dev(gate_codes, u8, "gate_codes"), _dev(gate_scales, u8, "gate_scales"),
+            _dev(up_codes, u8, "up_codes"), _dev(up_scales, u8, "up_scales"),
+            _dev(down_codes, u8, "down_codes"), _dev(down_scales, u8, "down_scales"),
+            _dev(routed_expert_weights, torch.float32, "routed_expert_weights"),
+            *_tables(E, M, group_sizes, group_padded_offsets, group_idx_for_bx, group_offsets),
+            _dev(workspace, u8, "workspace"), _dev(out, torch.float16, "out"), H, I, E, Tp,
+            routed_expert_weights.numel(), M, _VARIANTS[variant], _stream(out, stream))
+    _check(st, "rmoe_forward_mxfp4")
+
+
+def gate_up_mxfp4(token_codes, token_scales, gate_codes, gate_scales, up_codes, up_scales, group_sizes,
+                  group_padded_offsets, group_idx_for_bx, hidden_codes, hidden_scales, hidden: int,
+                  num_pairs: int, variant="auto", stream=None):
+    """Stage 1 of ``forward_mxfp4`` alone: the hidden rows' codes [Tp, row
+    bytes(I)] and scales [chunks(I), Tp, 8].  ``hidden`` is H, the tokens'
+    row length; ``num_pairs`` feeds the family choice."""
+    torch = _torch()
+    u8 = torch.uint8
+    Tp, H = token_codes.shape[0], int(hidden)
+    E, I = gate_codes.shape[:2]
+    for name, c, s, shape in (("token", token_codes, token_scales, (Tp, H)),
+                              ("gate", gate_codes, gate_scales, (E, I, H)),
+                              ("up", up_codes, up_scales, (E, I, H)),
+                              ("hidden", hidden_codes, hidden_scales, (Tp, I))):
+        cs, ss = mxfp4_shapes(shape)
+        _shape(c, cs, f"{name}_codes")
+        _shape(s, ss, f"{name}_scales")
+    M = group_idx_for_bx.numel()
+    with _same_device(token_codes, token_scales=token_scales, gate_codes=gate_codes,
+                      gate_scales=gate_scales, up_codes=up_codes, up_scales=up_scales,
+                      group_sizes=group_sizes, group_padded_offsets=group_padded_offsets,
+                      group_idx_for_bx=group_idx_for_bx, hidden_codes=hidden_codes,
+                      hidden_scales=hidden_scales):
+        st = lib().rmoe_gate_up_mxfp4(
+            _dev(token_codes, u8, "token_codes"), _dev(token_scales, u8, "token_scales"),
+            _dev(gate_codes, u8, "gate_codes"), _dev(gate_scales, u8, "gate_scales"),
+            _dev(up_codes, u8, "up_codes"), _dev(up_scales, u8, "up_scales"),
+            *_tables(E, M, group_sizes, group_padded_offsets, group_idx_for_bx),
+            _dev(hidden_codes, u8, "hidden_codes"), _dev(hidden_scales, u8, "hidden_scales"),
+            H, I, E, Tp, int(num_pairs), M, _VARIANTS[variant], _stream(token_codes, stream))
+    _check(st, "rmoe_gate_up_mxfp4")
+
+
+def down_mxfp4(hidden_codes, hidden_scales, down_codes, down_scales, routed_expert_weights, group_sizes,
+               group_offsets, group_padded_offsets, group_idx_for_bx, out, intermediate: int,
+               variant="auto", stream=None):
+    """Stage 2 of ``forward_mxfp4`` alone: out = fp16((hidden Wd^T) * w) on
+    valid rows; ``intermediate`` is I, the hidden rows' length."""
+    torch = _torch()
+    u8 = torch.uint8
+    (Tp, H), I = out.shape, int(intermediate)
+    E = down_codes.shape[0]
+    for name, c, s, shape in (("hidden", hidden_codes, hidden_scales, (Tp, I)),
+                              ("down", down_codes, down_scales, (E, H, I))):
+        cs, ss = mxfp4_shapes(shape)
+        _shape(c, cs, f"{name}_codes")
+        _shape(s, ss, f"{name}_scales")
+    M = group_idx_for_bx.numel()
+    with _same_device(out, hidden_codes=hidden_codes, hidden_scales=hidden_scales, down_codes=down_codes,
+                      down_scales=down_scales, routed_expert_weights=routed_expert_weights,
+                      group_sizes=group_sizes, group_offsets=group_offsets,
+                      group_padded_offsets=group_padded_offsets, group_idx_for_bx=group_idx_for_bx):
+        st = lib().rmoe_down_mxfp4(
+            _dev(hidden_codes, u8, "hidden_codes"), _dev(hidden_scales, u8, "hidden_scales"),
+            _dev(down_codes, u8, "down_codes"), _dev(down_scales, u8, "down_scales"),
+            _dev(routed_expert_weights, torch.float32, "routed_expert_weights"),
+            *_tables(E, M, group_sizes, group_padded_offsets, group_idx_for_bx, group_offsets),
+            _dev(out, torch.float16, "out"), H, I, E, Tp, routed_expert_weights.numel(), M,
+            _VARIANTS[variant], _stream(out, stream))
+    _check(st, "rmoe_down_mxfp4")
 
 
 _WORKSPACE = {}

@@ -562,3 +562,203 @@ int rmoe_router_f16(const void *x, const void *router_w, int64_t num_tokens, int
 }
 
 }  // extern "C"
+
+// ---- MXFP4 -----------------------------------------------------------------
+
+namespace {
+
+bool aligned8(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
+int64_t mx_chunks(int64_t cols) { return ceil_div(cols, 256); }
+bool bad_type(int32_t t) { return t != RMOE_TYPE_F16 && t != RMOE_TYPE_BF16 && t != RMOE_TYPE_F32; }
+rmoe::MxType mx_type(int32_t t) {
+    return t == RMOE_TYPE_F16 ? rmoe::MxType::f16 : t == RMOE_TYPE_BF16 ? rmoe::MxType::bf16 : rmoe::MxType::f32;
+}
+
+// Sizes of a quantisation: RMOE_OK with *empty set where there is nothing to do.
+int check_mx_sizes(int32_t type, int64_t batch, int64_t rows, int64_t cols, bool *empty) {
+    if (bad_type(type) || batch < 0 || rows < 0 || cols <= 0) return RMOE_ERR_INVALID_ARGUMENT;
+    if (cols % 8 != 0) return RMOE_ERR_UNSUPPORTED_SHAPE;
+    *empty = batch == 0 || rows == 0;
+    int64_t n = 0, u = 0;
+    if (__builtin_mul_overflow(batch, rows, &n) || __builtin_mul_overflow(n, mx_chunks(cols), &u) || u > INT32_MAX)
+        return RMOE_ERR_UNSUPPORTED_SHAPE;
+    return RMOE_OK;
+}
+
+// Streaming reads an expert's weights once per 64 rows of each of its blocks.
+int pick_variant_mx(int32_t variant, int64_t pairs, int32_t num_experts) {
+    if (variant == RMOE_VARIANT_STREAM || variant == RMOE_VARIANT_TILE) return variant;
+    return pairs <= 48 * (int64_t)num_experts ? RMOE_VARIANT_STREAM : RMOE_VARIANT_TILE;
+}
+
+int mx_gate_up_impl(rmoe::MxArgs a, int32_t variant, int64_t pairs, void *stream) {
+    if (a.M == 0) return RMOE_OK;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (pick_variant_mx(variant, pairs, a.E) == RMOE_VARIANT_STREAM)
+        return to_status(rmoe::launch_mx_stream_gate_up(a, s));
+    return to_status(rmoe::launch_mx_tile_gate_up(a, s));
+}
+
+int mx_down_impl(rmoe::MxArgs a, int32_t variant, int64_t pairs, void *stream) {
+    if (a.M == 0) return RMOE_OK;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (pick_variant_mx(variant, pairs, a.E) == RMOE_VARIANT_STREAM)
+        return to_status(rmoe::launch_mx_stream_down(a, s));
+    return to_status(rmoe::launch_mx_tile_down(a, s));
+}
+
+const unsigned char *bytes(const void *p) { return static_cast<const unsigned char *>(p); }
+unsigned char *bytes(void *p) { return static_cast<unsigned char *>(p); }
+
+// The two stages' checked arguments.
+int mx_gate_up_args(rmoe::MxArgs *a, const void *xc, const void *xs, const void *gc, const void *gsc, const void *uc,
+                    const void *us, const int32_t *gs, const int32_t *gpo, const int32_t *gidx, void *hc, void *hs,
+                    int64_t hidden, int64_t intermediate, int32_t E, int64_t Tp, int32_t M) {
+    if (!xc || !xs || !gc || !gsc || !uc || !us || !gs || !gpo || (M > 0 && !gidx) || !hc || !hs)
+        return RMOE_ERR_INVALID_ARGUMENT;
+    if (!aligned16(xc) || !aligned16(gc) || !aligned16(uc) || !aligned16(hc) || !aligned16(xs) || !aligned16(gsc) ||
+        !aligned16(us) || !aligned16(hs) || !aligned4(gs) || !aligned4(gpo) || !aligned4(gidx))
+        return RMOE_ERR_MISALIGNED;
+    a->x = bytes(xc), a->xs = bytes(xs);
+    a->w0 = bytes(gc), a->w0s = bytes(gsc), a->w1 = bytes(uc), a->w1s = bytes(us);
+    a->gs = gs, a->gpo = gpo, a->gidx = gidx;
+    a->yc = bytes(hc), a->ys = bytes(hs);
+    a->N = intermediate, a->Tp = Tp, a->kc = (int32_t)mx_chunks(hidden), a->E = E, a->M = M;
+    return RMOE_OK;
+}
+
+int mx_down_args(rmoe::MxArgs *a, const void *hc, const void *hs, const void *dc, const void *ds, const float *rw,
+                 const int32_t *gs, const int32_t *go, const int32_t *gpo, const int32_t *gidx, void *out,
+                 int64_t hidden, int64_t intermediate, int32_t E, int64_t Tp, int64_t pairs, int32_t M) {
+    if (!hc || !hs || !dc || !ds || !gs || !go || !gpo || (M > 0 && !gidx) || !out || (pairs > 0 && !rw))
+        return RMOE_ERR_INVALID_ARGUMENT;
+    if (!aligned16(hc) || !aligned16(hs) || !aligned16(dc) || !aligned16(ds) || !aligned16(out) || !aligned4(rw) ||
+        !aligned4(gs) || !aligned4(go) || !aligned4(gpo) || !aligned4(gidx))
+        return RMOE_ERR_MISALIGNED;
+    a->x = bytes(hc), a->xs = bytes(hs), a->w0 = bytes(dc), a->w0s = bytes(ds), a->rw = rw;
+    a->gs = gs, a->go = go, a->gpo = gpo, a->gidx = gidx;
+    a->y = static_cast<_Float16 *>(out);
+    a->N = hidden, a->Tp = Tp, a->kc = (int32_t)mx_chunks(intermediate), a->E = E, a->M = M;
+    return RMOE_OK;
+}
+
+int check_mx_dims(int64_t hidden, int64_t intermediate, int32_t E, int64_t Tp, int64_t pairs, int32_t M,
+                  int32_t variant) {
+    const int st = check_dims(hidden, intermediate, E, Tp, M);
+    if (st != RMOE_OK) return st;
+    return bad_variant(variant) || pairs < 0 ? RMOE_ERR_INVALID_ARGUMENT : RMOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t rmoe_mxfp4_chunks(int64_t cols) { return cols <= 0 ? 0 : mx_chunks(cols); }
+int64_t rmoe_mxfp4_row_bytes(int64_t cols) { return cols <= 0 ? 0 : 128 * mx_chunks(cols); }
+size_t rmoe_mxfp4_code_bytes(int64_t rows, int64_t cols) {
+    return rows <= 0 || cols <= 0 ? 0 : (size_t)rows * 128u * (size_t)mx_chunks(cols);
+}
+size_t rmoe_mxfp4_scale_bytes(int64_t rows, int64_t cols) {
+    return rows <= 0 || cols <= 0 ? 0 : (size_t)rows * 8u * (size_t)mx_chunks(cols);
+}
+
+int rmoe_quantize_mxfp4(const void *x, int32_t type, int64_t batch, int64_t rows, int64_t cols, void *codes,
+                        void *scales, void *stream) {
+    bool empty = false;
+    const int st = check_mx_sizes(type, batch, rows, cols, &empty);
+    if (st != RMOE_OK) return st;
+    if (empty) return RMOE_OK;
+    if (!x || !codes || !scales) return RMOE_ERR_INVALID_ARGUMENT;
+    if (!aligned16(x) || !aligned16(codes) || !aligned8(scales)) return RMOE_ERR_MISALIGNED;
+    return to_status(rmoe::launch_quantize(x, mx_type(type), batch, rows, cols, bytes(codes), bytes(scales),
+                                           static_cast<hipStream_t>(stream)));
+}
+
+int rmoe_dequantize_mxfp4(const void *codes, const void *scales, int32_t type, int64_t batch, int64_t rows,
+                          int64_t cols, void *y, void *stream) {
+    bool empty = false;
+    const int st = check_mx_sizes(type, batch, rows, cols, &empty);
+    if (st != RMOE_OK) return st;
+    if (empty) return RMOE_OK;
+    if (!codes || !scales || !y) return RMOE_ERR_INVALID_ARGUMENT;
+    if (!aligned16(y) || !aligned16(codes) || !aligned8(scales)) return RMOE_ERR_MISALIGNED;
+    return to_status(rmoe::launch_dequantize(bytes(codes), bytes(scales), mx_type(type), batch, rows, cols, y,
+                                             static_cast<hipStream_t>(stream)));
+}
+
+int rmoe_pack_mxfp4_f16(const void *x, const float *topk_weights, const int32_t *prow, const int32_t *cpos,
+                        int64_t num_tokens, int32_t top_k, int64_t hidden, void *codes, void *scales,
+                        float *w_compact, int64_t total_padded_tokens, void *stream) {
+    if (top_k < 0 || total_padded_tokens < 0) return RMOE_ERR_INVALID_ARGUMENT;
+    bool empty = false;
+    const int st = check_mx_sizes(RMOE_TYPE_F16, 1, num_tokens, hidden, &empty);
+    if (st != RMOE_OK) return st;
+    if (empty || top_k == 0) return RMOE_OK;
+    if (!x || !topk_weights || !prow || !cpos || !codes || !scales || !w_compact) return RMOE_ERR_INVALID_ARGUMENT;
+    if (!aligned16(x) || !aligned16(codes) || !aligned8(scales) || !aligned4(topk_weights) || !aligned4(prow) ||
+        !aligned4(cpos) || !aligned4(w_compact))
+        return RMOE_ERR_MISALIGNED;
+    return to_status(rmoe::launch_pack_mx(static_cast<const _Float16 *>(x), topk_weights, prow, cpos, num_tokens,
+                                          top_k, hidden, total_padded_tokens, bytes(codes), bytes(scales), w_compact,
+                                          static_cast<hipStream_t>(stream)));
+}
+
+size_t rmoe_mxfp4_workspace_bytes(int64_t total_padded_tokens, int64_t intermediate) {
+    return rmoe_mxfp4_code_bytes(total_padded_tokens, intermediate) +
+           rmoe_mxfp4_scale_bytes(total_padded_tokens, intermediate);
+}
+
+int rmoe_pick_variant_mxfp4(int32_t variant, int64_t num_pairs, int32_t num_experts) {
+    if (bad_variant(variant) || num_pairs < 0 || num_experts < 1) return RMOE_ERR_INVALID_ARGUMENT;
+    return pick_variant_mx(variant, num_pairs, num_experts);
+}
+
+int rmoe_gate_up_mxfp4(const void *xc, const void *xs, const void *gc, const void *gsc, const void *uc,
+                       const void *us, const int32_t *gs, const int32_t *gpo, const int32_t *gidx, void *hc, void *hs,
+                       int64_t hidden, int64_t intermediate, int32_t num_experts, int64_t total_padded_tokens,
+                       int64_t total_valid_tokens, int32_t num_blocks_m, int32_t variant, void *stream) {
+    int st = check_mx_dims(hidden, intermediate, num_experts, total_padded_tokens, total_valid_tokens, num_blocks_m,
+                           variant);
+    if (st != RMOE_OK) return st;
+    rmoe::MxArgs a{};
+    st = mx_gate_up_args(&a, xc, xs, gc, gsc, uc, us, gs, gpo, gidx, hc, hs, hidden, intermediate, num_experts,
+                         total_padded_tokens, num_blocks_m);
+    return st != RMOE_OK ? st : mx_gate_up_impl(a, variant, total_valid_tokens, stream);
+}
+
+int rmoe_down_mxfp4(const void *hc, const void *hs, const void *dc, const void *ds, const float *rw,
+                    const int32_t *gs, const int32_t *go, const int32_t *gpo, const int32_t *gidx, void *out,
+                    int64_t hidden, int64_t intermediate, int32_t num_experts, int64_t total_padded_tokens,
+                    int64_t total_valid_tokens, int32_t num_blocks_m, int32_t variant, void *stream) {
+    int st = check_mx_dims(hidden, intermediate, num_experts, total_padded_tokens, total_valid_tokens, num_blocks_m,
+                           variant);
+    if (st != RMOE_OK) return st;
+    rmoe::MxArgs a{};
+    st = mx_down_args(&a, hc, hs, dc, ds, rw, gs, go, gpo, gidx, out, hidden, intermediate, num_experts,
+                      total_padded_tokens, total_valid_tokens, num_blocks_m);
+    return st != RMOE_OK ? st : mx_down_impl(a, variant, total_valid_tokens, stream);
+}
+
+int rmoe_forward_mxfp4(const void *xc, const void *xs, const void *gc, const void *gsc, const void *uc,
+                       const void *us, const void *dc, const void *ds, const float *rw, const int32_t *gs,
+                       const int32_t *go, const int32_t *gpo, const int32_t *gidx, void *workspace, void *out,
+                       int64_t hidden, int64_t intermediate, int32_t num_experts, int64_t total_padded_tokens,
+                       int64_t total_valid_tokens, int32_t num_blocks_m, int32_t variant, void *stream) {
+    int st = check_mx_dims(hidden, intermediate, num_experts, total_padded_tokens, total_valid_tokens, num_blocks_m,
+                           variant);
+    if (st != RMOE_OK) return st;
+    if (!workspace) return RMOE_ERR_INVALID_ARGUMENT;
+    // the codes' bytes are a multiple of 128, so the scales keep the workspace's alignment
+    void *hs = bytes(workspace) + rmoe_mxfp4_code_bytes(total_padded_tokens, intermediate);
+    rmoe::MxArgs gu{}, dn{};
+    st = mx_gate_up_args(&gu, xc, xs, gc, gsc, uc, us, gs, gpo, gidx, workspace, hs, hidden, intermediate, num_experts,
+                         total_padded_tokens, num_blocks_m);
+    if (st != RMOE_OK) return st;
+    st = mx_down_args(&dn, workspace, hs, dc, ds, rw, gs, go, gpo, gidx, out, hidden, intermediate, num_experts,
+                      total_padded_tokens, total_valid_tokens, num_blocks_m);
+    if (st != RMOE_OK) return st;
+    st = mx_gate_up_impl(gu, variant, total_valid_tokens, stream);
+    return st != RMOE_OK ? st : mx_down_impl(dn, variant, total_valid_tokens, stream);
+}
+
+}  // extern "C"

@@ -23,6 +23,27 @@ inline hipError_t lds_opt_in_once(const void *fn, int bytes, std::atomic<uint64_
     return e;
 }
 
+constexpr int kXcd = 8;  // MI355X: workgroups go round-robin over 8 XCDs
+
+// Workgroup slots of the persistent kernel on the current device: its CU
+// count rounded down to a multiple of 8 (cached per device).
+inline hipError_t persistent_grid(unsigned &grid) {
+    static std::atomic<int> cached[64];
+    int dev = 0;
+    hipError_t e = hipGetDevice(&dev);
+    if (e != hipSuccess) return e;
+    int n = dev < 64 ? cached[dev].load(std::memory_order_relaxed) : 0;
+    if (n == 0) {
+        e = hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev);
+        if (e != hipSuccess) return e;
+        n = n / kXcd * kXcd;
+        if (n < kXcd) n = kXcd;
+        if (dev < 64) cached[dev].store(n, std::memory_order_relaxed);
+    }
+    grid = (unsigned)n;
+    return hipSuccess;
+}
+
 // One stage of the routed expert FFN as the kernels see it: a grouped GEMM
 // Y[r, n] = epilogue( sum_k X[r, k] * W[e(r), n, k] ) over the valid rows r
 // of every 128-row block.  For the gate/up stage W0 = gate_w, W1 = up_w and
@@ -72,6 +93,37 @@ hipError_t launch_router(const _Float16 *x, const _Float16 *w, int64_t T, int64_
 hipError_t launch_validate(const int32_t *gs, const int32_t *go, const int32_t *gpo,
                            const int32_t *gidx, int32_t E, int32_t M, int64_t pairs,
                            int32_t *violations, hipStream_t s);
+
+// ---- MXFP4 (rmoe_mx.h)
+
+enum class MxType { f16, bf16, f32 };
+
+// x [batch, rows, cols] -> codes [batch, rows, 128 ceil(cols / 256)], scales
+// [batch, ceil(cols / 256), rows, 8]; and back.
+hipError_t launch_quantize(const void *x, MxType type, int64_t batch, int64_t rows, int64_t cols,
+                           unsigned char *codes, unsigned char *scales, hipStream_t s);
+hipError_t launch_dequantize(const unsigned char *codes, const unsigned char *scales, MxType type, int64_t batch,
+                             int64_t rows, int64_t cols, void *y, hipStream_t s);
+hipError_t launch_pack_mx(const _Float16 *x, const float *topk_w, const int32_t *prow, const int32_t *cpos,
+                          int64_t T, int32_t k, int64_t H, int64_t Tp, unsigned char *codes, unsigned char *scales,
+                          float *w_compact, hipStream_t s);
+
+// One stage of the routed FFN on MXFP4 operands, as StageArgs.
+struct MxArgs {
+    const unsigned char *x, *xs;               // token codes [Tp, 128 kc], scales [kc, Tp, 8]
+    const unsigned char *w0, *w0s, *w1, *w1s;  // weight codes [E, N, 128 kc], scales [E, kc, N, 8]; w1 gate/up only
+    const float *rw;                           // [pairs] compact order (down only)
+    const int32_t *gs, *go, *gpo, *gidx;
+    unsigned char *yc, *ys;                    // gate/up: hidden codes [Tp, 128 ceil(N / 256)], scales
+    _Float16 *y;                               // down: out [Tp, N]
+    int64_t N, Tp;
+    int32_t kc;                                // chunks of 256 along K
+    int32_t E, M;
+};
+hipError_t launch_mx_tile_gate_up(const MxArgs &a, hipStream_t s);
+hipError_t launch_mx_tile_down(const MxArgs &a, hipStream_t s);
+hipError_t launch_mx_stream_gate_up(const MxArgs &a, hipStream_t s);
+hipError_t launch_mx_stream_down(const MxArgs &a, hipStream_t s);
 
 // Words of the static scratch the allocation-free contract build uses
 // (1 MiB per GPU): contract_chunks(pairs) * (E + 1) must not exceed it.

@@ -1,0 +1,50 @@
+// MXFP4 format shared by the quantisation and product kernels.
+//
+// A block of 32 consecutive elements of a row shares one scale 2^(b - 127),
+// held as the exponent byte b; an element is a 4-bit E2M1 code (sign, then
+// the magnitudes 0 0.5 1 1.5 2 3 4 6), two per byte, the even element in the
+// low nibble.  Codes are row-major, a row padded to whole chunks of 256
+// elements (128 bytes: one LDS row of the product kernels, 8 blocks).  Scale
+// bytes are stored chunk by chunk, [chunks][rows][8], so that the bytes of
+// 32 rows of a chunk are 256 contiguous bytes: one DMA.  The 8 bytes of a
+// (chunk, row) hold blocks 0 2 4 6 1 3 5 7: v_mfma_scale_f32_32x32x64 takes
+// K = 64 per instruction, lanes 0-31 the first block of it and lanes 32-63
+// the second, so one dword per lane holds its scales of a chunk's four
+// instructions, picked by the instruction's byte select.
+#pragma once
+
+#include "rmoe_device.h"
+
+namespace rmoe {
+
+constexpr int kMxChunk = 256;     // elements per chunk
+constexpr int kMxChunkBytes = 128;
+
+// Byte of block j (0..7) of a chunk within its 8 scale bytes.
+__device__ __forceinline__ int mx_pos(int j) { return ((j & 1) << 2) | (j >> 1); }
+
+// Scale byte of a block whose largest magnitude has these fp32 bits:
+// floor(log2(amax)) - 2 + 127, so that the largest element lands in [4, 8);
+// at least 0 (amax < 2^-125, zero included).  Infinities and NaN (their bits
+// order above every number) give 255, the format's NaN.
+__device__ __forceinline__ unsigned mx_scale_byte(unsigned amax_bits) {
+    const int ex = (int)(amax_bits >> 23);
+    return ex == 255 ? 255u : ex > 2 ? (unsigned)(ex - 2) : 0u;
+}
+
+// E2M1 codes of 4 values over 2^(byte - 127), rounded to nearest even and
+// clamped at 6 by the conversion instruction, in the low 16 bits.  Small
+// scales are moved up by 2^64 together with the values (exact), away from
+// the subnormal scales; `up` is mx_up(byte), `scale` mx_scale(byte).
+__device__ __forceinline__ float mx_up(unsigned byte) { return byte < 64 ? 0x1p64f : 1.0f; }
+__device__ __forceinline__ float mx_scale(unsigned byte) {
+    return __builtin_bit_cast(float, (byte < 64 ? byte + 64 : byte) << 23);
+}
+__device__ __forceinline__ unsigned mx_codes4(float a, float b, float c, float d, float up, float scale) {
+    unsigned r = 0;
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, a * up, b * up, scale, 0);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, c * up, d * up, scale, 1);
+    return r;
+}
+
+}  // namespace rmoe
