@@ -537,6 +537,88 @@ RMOE_API int rmoe_down_mxfp4(const void *hidden_codes, const void *hidden_scales
                              int64_t total_padded_tokens, int64_t total_valid_tokens,
                              int32_t num_blocks_m, int32_t variant, void *stream);
 
+/*
+ * ---- Training: the forward that keeps its pre-activations, and the backward
+ * pass.  fp16 tensors, fp32 in between; E = 1 is the dense gated block.
+ *
+ * rmoe_gate_up_train_f16 is rmoe_gate_up_f16 that also writes gate = x.Wg^T
+ * and up = x.Wu^T, each [Tp, I] fp16, on valid rows; hidden as there, bit for
+ * bit as the tiled family.  rmoe_down_f16 completes the forward.
+ */
+RMOE_API int rmoe_gate_up_train_f16(const void *stacked_expert_tokens, const void *gate_w,
+                                    const void *up_w, const int32_t *group_sizes,
+                                    const int32_t *group_padded_offsets,
+                                    const int32_t *group_idx_for_bx, void *gate, void *up,
+                                    void *hidden_rows, int64_t hidden, int64_t intermediate,
+                                    int32_t num_experts, int64_t total_padded_tokens,
+                                    int64_t total_valid_tokens, int32_t num_blocks_m, void *stream);
+
+/*
+ * Backward of the routed FFN out = (hidden . Wd[e]^T) * w.  dout [Tp, H] is
+ * the gradient of out in the padded layout (of a combined output: rmoe_pack_
+ * f16 of its gradient).  For a valid row with compact index c, w = routed
+ * weight c, s = 1/(1 + e^-gate):
+ *   b = dout . Wd[e] (fp32);  drw[c] = sum_i b silu(gate) up   (fp32)
+ *   dgate = fp16( w b up (s + gate s (1 - s)) ), dup = fp16( w b silu(gate) ),
+ *   whidden = fp16( w silu(gate) up )                    each [Tp, I]
+ *   dx = fp16( dgate . Wg[e] + dup . Wu[e] )             [Tp, H]
+ *   dgate_w[e] = fp16( sum_rows dgate^T x ), dup_w[e] = fp16( sum_rows dup^T
+ *   x ) [E, I, H]; ddown_w[e] = fp16( sum_rows dout^T whidden ) [E, H, I];
+ *   zeros for an expert without rows.
+ * Products accumulate in fp32, in an order fixed by the shapes and tables
+ * (no atomics): equal calls give equal bits.
+ * x [Tp, H]: the stacked token rows of the forward; gate, up: what
+ * rmoe_gate_up_train_f16 kept.  dgate may be gate's own memory and dup up's;
+ * other overlaps are not allowed.  scratch: rmoe_backward_scratch_bytes(
+ * pairs, I) bytes, contents irrelevant on entry.  Padding rows of dgate, dup,
+ * whidden and dx are not written, padding rows of the inputs may hold
+ * anything; drw holds one value per valid pair.  The gradient of the routed
+ * weights reaches the router through topk_weights; a token's gradient is
+ * rmoe_combine_f16 of dx.
+ * H, I multiples of 128; fp16 pointers 16-byte, others 4-byte aligned; at
+ * most 2^23 weight-gradient tiles, 3 E ceil(H/256) ceil(I/256)
+ * (RMOE_ERR_UNSUPPORTED_SHAPE).  rmoe_backward_f16 runs the three stages
+ * below in this order, four launches on `stream`.
+ */
+RMOE_API size_t rmoe_backward_scratch_bytes(int64_t num_pairs, int64_t intermediate);
+RMOE_API int rmoe_backward_f16(const void *x, const void *dout, const void *gate_w, const void *up_w,
+                               const void *down_w, const float *routed_expert_weights,
+                               const void *gate, const void *up, const int32_t *group_sizes,
+                               const int32_t *group_offsets, const int32_t *group_padded_offsets,
+                               const int32_t *group_idx_for_bx, void *dgate, void *dup,
+                               void *whidden, void *scratch, void *dx, void *dgate_w, void *dup_w,
+                               void *ddown_w, float *drw, int64_t hidden, int64_t intermediate,
+                               int32_t num_experts, int64_t total_padded_tokens,
+                               int64_t total_valid_tokens, int32_t num_blocks_m, void *stream);
+
+/* dgate, dup, whidden and drw. */
+RMOE_API int rmoe_down_backward_f16(const void *dout, const void *down_w,
+                                    const float *routed_expert_weights, const void *gate,
+                                    const void *up, const int32_t *group_sizes,
+                                    const int32_t *group_offsets, const int32_t *group_padded_offsets,
+                                    const int32_t *group_idx_for_bx, void *dgate, void *dup,
+                                    void *whidden, void *scratch, float *drw, int64_t hidden,
+                                    int64_t intermediate, int32_t num_experts,
+                                    int64_t total_padded_tokens, int64_t total_valid_tokens,
+                                    int32_t num_blocks_m, void *stream);
+
+/* dx from dgate and dup. */
+RMOE_API int rmoe_gate_up_backward_f16(const void *dgate, const void *dup, const void *gate_w,
+                                       const void *up_w, const int32_t *group_sizes,
+                                       const int32_t *group_padded_offsets,
+                                       const int32_t *group_idx_for_bx, void *dx, int64_t hidden,
+                                       int64_t intermediate, int32_t num_experts,
+                                       int64_t total_padded_tokens, int64_t total_valid_tokens,
+                                       int32_t num_blocks_m, void *stream);
+
+/* The three weight gradients.  Writes every element of them, whatever the
+ * routing; a group whose table entries point outside [0, Tp) is left out. */
+RMOE_API int rmoe_weight_grad_f16(const void *x, const void *dout, const void *dgate, const void *dup,
+                                  const void *whidden, const int32_t *group_sizes,
+                                  const int32_t *group_padded_offsets, void *dgate_w, void *dup_w,
+                                  void *ddown_w, int64_t hidden, int64_t intermediate,
+                                  int32_t num_experts, int64_t total_padded_tokens, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

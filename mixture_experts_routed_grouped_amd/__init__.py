@@ -74,6 +74,12 @@ _SIGS = {
     "rmoe_forward_mxfp4": ([_P] * 15 + [_I64, _I64, _I32, _I64, _I64, _I32, _I32, _P], ctypes.c_int),
     "rmoe_gate_up_mxfp4": ([_P] * 11 + [_I64, _I64, _I32, _I64, _I64, _I32, _I32, _P], ctypes.c_int),
     "rmoe_down_mxfp4": ([_P] * 10 + [_I64, _I64, _I32, _I64, _I64, _I32, _I32, _P], ctypes.c_int),
+    "rmoe_gate_up_train_f16": ([_P] * 9 + [_I64, _I64, _I32, _I64, _I64, _I32, _P], ctypes.c_int),
+    "rmoe_backward_scratch_bytes": ([_I64, _I64], ctypes.c_size_t),
+    "rmoe_backward_f16": ([_P] * 21 + [_I64, _I64, _I32, _I64, _I64, _I32, _P], ctypes.c_int),
+    "rmoe_down_backward_f16": ([_P] * 14 + [_I64, _I64, _I32, _I64, _I64, _I32, _P], ctypes.c_int),
+    "rmoe_gate_up_backward_f16": ([_P] * 8 + [_I64, _I64, _I32, _I64, _I64, _I32, _P], ctypes.c_int),
+    "rmoe_weight_grad_f16": ([_P] * 10 + [_I64, _I64, _I32, _I64, _P], ctypes.c_int),
     "rmoe_contract_noalloc_max_words": ([], ctypes.c_size_t),
     "rmoe_build_contract_device_noalloc": ([_P, _I64, _I32, _I32, _P, _P, _P, _P, _I64, _P, _P, _P,
                                             _P, _P, _P], ctypes.c_int),
@@ -782,6 +788,153 @@ def down_mxfp4(hidden_codes, hidden_scales, down_codes, down_scales, routed_expe
             _dev(out, torch.float16, "out"), H, I, E, Tp, routed_expert_weights.numel(), M,
             _VARIANTS[variant], _stream(out, stream))
     _check(st, "rmoe_down_mxfp4")
+
+
+# ------------------------------------------------------------- training
+def gate_up_train(x, gate_w, up_w, group_sizes, group_padded_offsets, group_idx_for_bx, gate, up, hidden,
+                  stream=None):
+    """Stage 1 of the training forward: ``gate_up`` that also keeps the
+    pre-activations.  On valid rows of the padded layout: gate = fp16(x Wg^T),
+    up = fp16(x Wu^T), hidden = fp16(silu(x Wg^T) * (x Wu^T)), each [Tp, I];
+    ``down`` completes the forward."""
+    torch = _torch()
+    f16 = torch.float16
+    E, I, H = gate_w.shape
+    Tp, M = x.shape[0], group_idx_for_bx.numel()
+    for name, t, shape in (("x", x, (Tp, H)), ("up_w", up_w, (E, I, H)), ("gate", gate, (Tp, I)),
+                           ("up", up, (Tp, I)), ("hidden", hidden, (Tp, I))):
+        _shape(t, shape, name)
+    with _same_device(x, gate_w=gate_w, up_w=up_w, group_sizes=group_sizes,
+                      group_padded_offsets=group_padded_offsets, group_idx_for_bx=group_idx_for_bx,
+                      gate=gate, up=up, hidden=hidden):
+        st = lib().rmoe_gate_up_train_f16(
+            _dev(x, f16, "x"), _dev(gate_w, f16, "gate_w"), _dev(up_w, f16, "up_w"),
+            *_tables(E, M, group_sizes, group_padded_offsets, group_idx_for_bx), _dev(gate, f16, "gate"),
+            _dev(up, f16, "up"), _dev(hidden, f16, "hidden"), H, I, E, Tp, 0, M, _stream(x, stream))
+    _check(st, "rmoe_gate_up_train_f16")
+
+
+def backward_scratch_bytes(num_pairs: int, intermediate: int) -> int:
+    """Bytes of the scratch that ``backward`` and ``down_backward`` need."""
+    return int(lib().rmoe_backward_scratch_bytes(int(num_pairs), int(intermediate)))
+
+
+def _scratch(scratch, num_pairs, intermediate):
+    """Pointer of a scratch tensor of any type that holds enough bytes."""
+    if not scratch.is_cuda or not scratch.is_contiguous():
+        raise ValueError("scratch must be contiguous GPU memory")
+    if scratch.numel() * scratch.element_size() < backward_scratch_bytes(num_pairs, intermediate):
+        raise ValueError("scratch too small")
+    return ctypes.c_void_p(scratch.data_ptr())
+
+
+def backward(x, dout, gate_w, up_w, down_w, routed_expert_weights, gate, up, group_sizes, group_offsets,
+             group_padded_offsets, group_idx_for_bx, dgate, dup, whidden, scratch, dx, dgate_w, dup_w,
+             ddown_w, drw, stream=None):
+    """Backward pass of the routed expert FFN (rmoe_backward_f16).  Inputs:
+    the stacked token rows ``x`` and the output's gradient ``dout`` [Tp, H],
+    the weights, the kept ``gate`` and ``up`` [Tp, I] and the tables.  Writes
+    ``dgate``, ``dup`` (they may be ``gate`` and ``up`` themselves) and
+    ``whidden`` [Tp, I], then the results: ``dx`` [Tp, H], ``dgate_w``,
+    ``dup_w`` [E, I, H], ``ddown_w`` [E, H, I] and ``drw`` (fp32, one per
+    pair, compact order).  ``scratch``: ``backward_scratch_bytes(pairs, I)``."""
+    torch = _torch()
+    f16, f32 = torch.float16, torch.float32
+    E, I, H = gate_w.shape
+    Tp, M, pairs = x.shape[0], group_idx_for_bx.numel(), routed_expert_weights.numel()
+    rows_h, rows_i, w_ih = (Tp, H), (Tp, I), (E, I, H)
+    for name, t, shape in (("x", x, rows_h), ("dout", dout, rows_h), ("up_w", up_w, w_ih),
+                           ("down_w", down_w, (E, H, I)), ("gate", gate, rows_i), ("up", up, rows_i),
+                           ("dgate", dgate, rows_i), ("dup", dup, rows_i), ("whidden", whidden, rows_i),
+                           ("dx", dx, rows_h), ("dgate_w", dgate_w, w_ih), ("dup_w", dup_w, w_ih),
+                           ("ddown_w", ddown_w, (E, H, I))):
+        _shape(t, shape, name)
+    if drw.numel() != pairs:
+        raise ValueError("drw must have one entry per routed weight")
+    with _same_device(x, dout=dout, gate_w=gate_w, up_w=up_w, down_w=down_w, gate=gate, up=up,
+                      routed_expert_weights=routed_expert_weights, group_sizes=group_sizes,
+                      group_offsets=group_offsets, group_padded_offsets=group_padded_offsets,
+                      group_idx_for_bx=group_idx_for_bx, dgate=dgate, dup=dup, whidden=whidden,
+                      scratch=scratch, dx=dx, dgate_w=dgate_w, dup_w=dup_w, ddown_w=ddown_w, drw=drw):
+        st = lib().rmoe_backward_f16(
+            _dev(x, f16, "x"), _dev(dout, f16, "dout"), _dev(gate_w, f16, "gate_w"), _dev(up_w, f16, "up_w"),
+            _dev(down_w, f16, "down_w"), _dev(routed_expert_weights, f32, "routed_expert_weights"),
+            _dev(gate, f16, "gate"), _dev(up, f16, "up"),
+            *_tables(E, M, group_sizes, group_padded_offsets, group_idx_for_bx, group_offsets),
+            _dev(dgate, f16, "dgate"), _dev(dup, f16, "dup"), _dev(whidden, f16, "whidden"),
+            _scratch(scratch, pairs, I), _dev(dx, f16, "dx"), _dev(dgate_w, f16, "dgate_w"),
+            _dev(dup_w, f16, "dup_w"), _dev(ddown_w, f16, "ddown_w"), _dev(drw, f32, "drw"), H, I, E, Tp,
+            pairs, M, _stream(x, stream))
+    _check(st, "rmoe_backward_f16")
+
+
+def down_backward(dout, down_w, routed_expert_weights, gate, up, group_sizes, group_offsets,
+                  group_padded_offsets, group_idx_for_bx, dgate, dup, whidden, scratch, drw, stream=None):
+    """The first stage of ``backward``: dgate, dup, whidden and drw."""
+    torch = _torch()
+    f16, f32 = torch.float16, torch.float32
+    E, H, I = down_w.shape
+    Tp, M, pairs = dout.shape[0], group_idx_for_bx.numel(), routed_expert_weights.numel()
+    for name, t, shape in (("dout", dout, (Tp, H)), ("gate", gate, (Tp, I)), ("up", up, (Tp, I)),
+                           ("dgate", dgate, (Tp, I)), ("dup", dup, (Tp, I)), ("whidden", whidden, (Tp, I))):
+        _shape(t, shape, name)
+    if drw.numel() != pairs:
+        raise ValueError("drw must have one entry per routed weight")
+    with _same_device(dout, down_w=down_w, gate=gate, up=up, routed_expert_weights=routed_expert_weights,
+                      group_sizes=group_sizes, group_offsets=group_offsets,
+                      group_padded_offsets=group_padded_offsets, group_idx_for_bx=group_idx_for_bx,
+                      dgate=dgate, dup=dup, whidden=whidden, scratch=scratch, drw=drw):
+        st = lib().rmoe_down_backward_f16(
+            _dev(dout, f16, "dout"), _dev(down_w, f16, "down_w"),
+            _dev(routed_expert_weights, f32, "routed_expert_weights"), _dev(gate, f16, "gate"),
+            _dev(up, f16, "up"),
+            *_tables(E, M, group_sizes, group_padded_offsets, group_idx_for_bx, group_offsets),
+            _dev(dgate, f16, "dgate"), _dev(dup, f16, "dup"), _dev(whidden, f16, "whidden"),
+            _scratch(scratch, pairs, I), _dev(drw, f32, "drw"), H, I, E, Tp, pairs, M, _stream(dout, stream))
+    _check(st, "rmoe_down_backward_f16")
+
+
+def gate_up_backward(dgate, dup, gate_w, up_w, group_sizes, group_padded_offsets, group_idx_for_bx, dx,
+                     stream=None):
+    """The second stage of ``backward``: dx = fp16(dgate Wg + dup Wu) on valid rows."""
+    torch = _torch()
+    f16 = torch.float16
+    E, I, H = gate_w.shape
+    Tp, M = dgate.shape[0], group_idx_for_bx.numel()
+    for name, t, shape in (("dgate", dgate, (Tp, I)), ("dup", dup, (Tp, I)), ("up_w", up_w, (E, I, H)),
+                           ("dx", dx, (Tp, H))):
+        _shape(t, shape, name)
+    with _same_device(dgate, dup=dup, gate_w=gate_w, up_w=up_w, group_sizes=group_sizes,
+                      group_padded_offsets=group_padded_offsets, group_idx_for_bx=group_idx_for_bx, dx=dx):
+        st = lib().rmoe_gate_up_backward_f16(
+            _dev(dgate, f16, "dgate"), _dev(dup, f16, "dup"), _dev(gate_w, f16, "gate_w"),
+            _dev(up_w, f16, "up_w"), *_tables(E, M, group_sizes, group_padded_offsets, group_idx_for_bx),
+            _dev(dx, f16, "dx"), H, I, E, Tp, 0, M, _stream(dgate, stream))
+    _check(st, "rmoe_gate_up_backward_f16")
+
+
+def weight_grad(x, dout, dgate, dup, whidden, group_sizes, group_padded_offsets, dgate_w, dup_w, ddown_w,
+                stream=None):
+    """The third stage of ``backward``: the gradients of the expert matrices,
+    zeros for experts without rows."""
+    torch = _torch()
+    f16, i32 = torch.float16, torch.int32
+    E, I, H = dgate_w.shape
+    Tp = x.shape[0]
+    for name, t, shape in (("x", x, (Tp, H)), ("dout", dout, (Tp, H)), ("dgate", dgate, (Tp, I)),
+                           ("dup", dup, (Tp, I)), ("whidden", whidden, (Tp, I)), ("dup_w", dup_w, (E, I, H)),
+                           ("ddown_w", ddown_w, (E, H, I)), ("group_sizes", group_sizes, (E,)),
+                           ("group_padded_offsets", group_padded_offsets, (E + 1,))):
+        _shape(t, shape, name)
+    with _same_device(x, dout=dout, dgate=dgate, dup=dup, whidden=whidden, group_sizes=group_sizes,
+                      group_padded_offsets=group_padded_offsets, dgate_w=dgate_w, dup_w=dup_w,
+                      ddown_w=ddown_w):
+        st = lib().rmoe_weight_grad_f16(
+            _dev(x, f16, "x"), _dev(dout, f16, "dout"), _dev(dgate, f16, "dgate"), _dev(dup, f16, "dup"),
+            _dev(whidden, f16, "whidden"), _dev(group_sizes, i32, "group_sizes"),
+            _dev(group_padded_offsets, i32, "group_padded_offsets"), _dev(dgate_w, f16, "dgate_w"),
+            _dev(dup_w, f16, "dup_w"), _dev(ddown_w, f16, "ddown_w"), H, I, E, Tp, _stream(x, stream))
+    _check(st, "rmoe_weight_grad_f16")
 
 
 _WORKSPACE = {}

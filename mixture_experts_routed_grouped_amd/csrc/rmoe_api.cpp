@@ -762,3 +762,167 @@ int rmoe_forward_mxfp4(const void *xc, const void *xs, const void *gc, const voi
 }
 
 }  // extern "C"
+
+// ---- training --------------------------------------------------------------
+
+namespace {
+
+const _Float16 *f16(const void *p) { return static_cast<const _Float16 *>(p); }
+_Float16 *f16(void *p) { return static_cast<_Float16 *>(p); }
+
+template <class... T>
+bool any_null(T... p) {
+    return (!p || ...);
+}
+template <class... T>
+bool all16(T... p) {
+    return (aligned16(p) && ...);
+}
+template <class... T>
+bool all4(T... p) {
+    return (aligned4(p) && ...);
+}
+
+constexpr int64_t kMaxGradTiles = (int64_t)1 << 23;  // one workgroup each, within the grid's limit
+
+int check_train_dims(rmoe::TrainArgs *a, int64_t hidden, int64_t intermediate, int32_t E, int64_t Tp, int64_t pairs,
+                     int32_t M) {
+    const int st = check_dims(hidden, intermediate, E, Tp, M);
+    if (st != RMOE_OK) return st;
+    if (pairs < 0) return RMOE_ERR_INVALID_ARGUMENT;
+    a->H = hidden, a->I = intermediate, a->E = E, a->Tp = Tp, a->pairs = pairs, a->M = M;
+    return RMOE_OK;
+}
+
+// Checked arguments of each stage.
+int down_backward_args(rmoe::TrainArgs *a, const void *dout, const void *down_w, const float *rw, const void *gate,
+                       const void *up, const int32_t *gs, const int32_t *go, const int32_t *gpo, const int32_t *gidx,
+                       void *dgate, void *dup, void *whidden, void *scratch, float *drw) {
+    if (any_null(dout, down_w, gate, up, gs, go, gpo, dgate, dup, whidden) || (a->M > 0 && !gidx) ||
+        (a->pairs > 0 && any_null(rw, scratch, drw)))
+        return RMOE_ERR_INVALID_ARGUMENT;
+    if (!all16(dout, down_w, gate, up, dgate, dup, whidden) || !all4(rw, gs, go, gpo, gidx, scratch, drw))
+        return RMOE_ERR_MISALIGNED;
+    a->dy = f16(dout), a->wd = f16(down_w), a->rw = rw, a->g = f16(gate), a->u = f16(up);
+    a->gs = gs, a->go = go, a->gpo = gpo, a->gidx = gidx;
+    a->dg = f16(dgate), a->du = f16(dup), a->hw = f16(whidden);
+    a->part = static_cast<float *>(scratch), a->drw = drw;
+    return RMOE_OK;
+}
+
+int gate_up_backward_args(rmoe::TrainArgs *a, const void *dgate, const void *dup, const void *gate_w,
+                          const void *up_w, const int32_t *gs, const int32_t *gpo, const int32_t *gidx, void *dx) {
+    if (any_null(dgate, dup, gate_w, up_w, gs, gpo, dx) || (a->M > 0 && !gidx)) return RMOE_ERR_INVALID_ARGUMENT;
+    if (!all16(dgate, dup, gate_w, up_w, dx) || !all4(gs, gpo, gidx)) return RMOE_ERR_MISALIGNED;
+    // the kernel only reads dgate and dup
+    a->dg = const_cast<_Float16 *>(f16(dgate)), a->du = const_cast<_Float16 *>(f16(dup));
+    a->wg = f16(gate_w), a->wu = f16(up_w), a->gs = gs, a->gpo = gpo, a->gidx = gidx, a->dx = f16(dx);
+    return RMOE_OK;
+}
+
+int weight_grad_args(rmoe::TrainArgs *a, const void *x, const void *dout, const void *dgate, const void *dup,
+                     const void *whidden, const int32_t *gs, const int32_t *gpo, void *dgate_w, void *dup_w,
+                     void *ddown_w) {
+    if (rmoe::weight_grad_tiles(a->H, a->I, a->E) > kMaxGradTiles) return RMOE_ERR_UNSUPPORTED_SHAPE;
+    if (any_null(x, dout, dgate, dup, whidden, gs, gpo, dgate_w, dup_w, ddown_w)) return RMOE_ERR_INVALID_ARGUMENT;
+    if (!all16(x, dout, dgate, dup, whidden, dgate_w, dup_w, ddown_w) || !all4(gs, gpo)) return RMOE_ERR_MISALIGNED;
+    a->x = f16(x), a->dy = f16(dout);
+    a->dg = const_cast<_Float16 *>(f16(dgate)), a->du = const_cast<_Float16 *>(f16(dup));
+    a->hw = const_cast<_Float16 *>(f16(whidden));
+    a->gs = gs, a->gpo = gpo, a->dwg = f16(dgate_w), a->dwu = f16(dup_w), a->dwd = f16(ddown_w);
+    return RMOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int rmoe_gate_up_train_f16(const void *x, const void *gate_w, const void *up_w, const int32_t *gs,
+                           const int32_t *gpo, const int32_t *gidx, void *gate, void *up, void *hidden_rows,
+                           int64_t hidden, int64_t intermediate, int32_t num_experts, int64_t total_padded_tokens,
+                           int64_t total_valid_tokens, int32_t num_blocks_m, void *stream) {
+    const int st = check_dims(hidden, intermediate, num_experts, total_padded_tokens, num_blocks_m);
+    if (st != RMOE_OK) return st;
+    if (total_valid_tokens < 0 || any_null(x, gate_w, up_w, gs, gpo, gate, up, hidden_rows) ||
+        (num_blocks_m > 0 && !gidx))
+        return RMOE_ERR_INVALID_ARGUMENT;
+    if (!all16(x, gate_w, up_w, gate, up, hidden_rows) || !all4(gs, gpo, gidx)) return RMOE_ERR_MISALIGNED;
+    if (num_blocks_m == 0) return RMOE_OK;
+    rmoe::StageArgs a{};
+    a.x = f16(x), a.w0 = f16(gate_w), a.w1 = f16(up_w);
+    a.gs = gs, a.gpo = gpo, a.gidx = gidx;
+    a.y = f16(hidden_rows), a.yg = f16(gate), a.yu = f16(up);
+    a.K = hidden, a.N = intermediate, a.E = num_experts, a.M = num_blocks_m, a.pairs = total_valid_tokens;
+    return to_status(rmoe::launch_tile_gate_up_train(a, static_cast<hipStream_t>(stream)));
+}
+
+size_t rmoe_backward_scratch_bytes(int64_t num_pairs, int64_t intermediate) {
+    return num_pairs <= 0 || intermediate <= 0 ? 0 : (size_t)num_pairs * (size_t)ceil_div(intermediate, 128) * 4u;
+}
+
+int rmoe_down_backward_f16(const void *dout, const void *down_w, const float *rw, const void *gate, const void *up,
+                           const int32_t *gs, const int32_t *go, const int32_t *gpo, const int32_t *gidx, void *dgate,
+                           void *dup, void *whidden, void *scratch, float *drw, int64_t hidden, int64_t intermediate,
+                           int32_t num_experts, int64_t total_padded_tokens, int64_t total_valid_tokens,
+                           int32_t num_blocks_m, void *stream) {
+    rmoe::TrainArgs a{};
+    int st = check_train_dims(&a, hidden, intermediate, num_experts, total_padded_tokens, total_valid_tokens,
+                              num_blocks_m);
+    if (st != RMOE_OK) return st;
+    st = down_backward_args(&a, dout, down_w, rw, gate, up, gs, go, gpo, gidx, dgate, dup, whidden, scratch, drw);
+    if (st != RMOE_OK || num_blocks_m == 0) return st;
+    return to_status(rmoe::launch_down_backward(a, static_cast<hipStream_t>(stream)));
+}
+
+int rmoe_gate_up_backward_f16(const void *dgate, const void *dup, const void *gate_w, const void *up_w,
+                              const int32_t *gs, const int32_t *gpo, const int32_t *gidx, void *dx, int64_t hidden,
+                              int64_t intermediate, int32_t num_experts, int64_t total_padded_tokens,
+                              int64_t total_valid_tokens, int32_t num_blocks_m, void *stream) {
+    rmoe::TrainArgs a{};
+    int st = check_train_dims(&a, hidden, intermediate, num_experts, total_padded_tokens, total_valid_tokens,
+                              num_blocks_m);
+    if (st != RMOE_OK) return st;
+    st = gate_up_backward_args(&a, dgate, dup, gate_w, up_w, gs, gpo, gidx, dx);
+    if (st != RMOE_OK || num_blocks_m == 0) return st;
+    return to_status(rmoe::launch_gate_up_backward(a, static_cast<hipStream_t>(stream)));
+}
+
+int rmoe_weight_grad_f16(const void *x, const void *dout, const void *dgate, const void *dup, const void *whidden,
+                         const int32_t *gs, const int32_t *gpo, void *dgate_w, void *dup_w, void *ddown_w,
+                         int64_t hidden, int64_t intermediate, int32_t num_experts, int64_t total_padded_tokens,
+                         void *stream) {
+    rmoe::TrainArgs a{};
+    int st = check_train_dims(&a, hidden, intermediate, num_experts, total_padded_tokens, 0, 0);
+    if (st != RMOE_OK) return st;
+    st = weight_grad_args(&a, x, dout, dgate, dup, whidden, gs, gpo, dgate_w, dup_w, ddown_w);
+    if (st != RMOE_OK) return st;
+    return to_status(rmoe::launch_weight_grad(a, static_cast<hipStream_t>(stream)));
+}
+
+int rmoe_backward_f16(const void *x, const void *dout, const void *gate_w, const void *up_w, const void *down_w,
+                      const float *rw, const void *gate, const void *up, const int32_t *gs, const int32_t *go,
+                      const int32_t *gpo, const int32_t *gidx, void *dgate, void *dup, void *whidden, void *scratch,
+                      void *dx, void *dgate_w, void *dup_w, void *ddown_w, float *drw, int64_t hidden,
+                      int64_t intermediate, int32_t num_experts, int64_t total_padded_tokens,
+                      int64_t total_valid_tokens, int32_t num_blocks_m, void *stream) {
+    rmoe::TrainArgs a{};
+    int st = check_train_dims(&a, hidden, intermediate, num_experts, total_padded_tokens, total_valid_tokens,
+                              num_blocks_m);
+    if (st != RMOE_OK) return st;
+    st = down_backward_args(&a, dout, down_w, rw, gate, up, gs, go, gpo, gidx, dgate, dup, whidden, scratch, drw);
+    if (st != RMOE_OK) return st;
+    st = gate_up_backward_args(&a, dgate, dup, gate_w, up_w, gs, gpo, gidx, dx);
+    if (st != RMOE_OK) return st;
+    st = weight_grad_args(&a, x, dout, dgate, dup, whidden, gs, gpo, dgate_w, dup_w, ddown_w);
+    if (st != RMOE_OK) return st;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (num_blocks_m > 0) {
+        st = to_status(rmoe::launch_down_backward(a, s));
+        if (st != RMOE_OK) return st;
+        st = to_status(rmoe::launch_gate_up_backward(a, s));
+        if (st != RMOE_OK) return st;
+    }
+    return to_status(rmoe::launch_weight_grad(a, s));
+}
+
+}  // extern "C"

@@ -1,0 +1,466 @@
+// Backward pass of the routed expert FFN.  For a row r of expert e with
+// routed weight w, token row x, kept pre-activations g, u and output gradient
+// dy (all rows of the padded layout):
+//
+//     b  = dy . Wd[e]              (a sum over H)
+//     dw = sum_i b silu(g) u       dh = w b
+//     dg = dh u silu'(g)           du = dh silu(g)       hw = w silu(g) u
+//     dx = dg . Wg[e] + du . Wu[e] (a sum over I, twice)
+//     dWg[e] = sum_r dg^T x        dWu[e] = sum_r du^T x  dWd[e] = sum_r dy^T hw
+//
+// with silu'(g) = s + g s (1 - s), s = 1 / (1 + e^-g).  Everything between
+// the fp16 inputs and outputs is fp32; dg, du and hw are rounded to fp16
+// once, as operands of the products that follow.
+//
+// All three products run on the 256 x 256 tiles of rmoe_kloop.h with fp16
+// MFMA (v_mfma_f32_32x32x16_f16), bound by the matrix cores and by operand
+// delivery as the forward's tiles are.  Their sums run along the row index of
+// a row-major matrix (Wd over H, Wg and Wu over I; for the weight gradients
+// both operands, over the tokens), so those operands lie k-major: an LDS slot
+// holds 64 k rows of 256 columns, and ds_read_b64_tr_b16 turns it into MFMA
+// operands: a group of 16 lanes reads 4 k rows of 16 columns and each lane
+// receives its column's 4 values.  DMA instructions move 8 k rows x 128
+// bytes, the pattern the L2 serves best.
+//
+// k-major slot: [4 column groups of 64][8 k groups of 8] blocks of 1 KB =
+// 8 rows x 128 bytes; 16-byte chunk c of row r sits at c ^ swz_k(r), which
+// spreads the 4 rows x 64 bytes that 32 lanes read over all 64 banks.
+#include <atomic>
+
+#include "rmoe_internal.h"
+#include "rmoe_kloop.h"
+#include "rmoe_sched.h"
+
+namespace rmoe {
+namespace {
+
+constexpr int BK = 64;               // K per step
+constexpr int SLOT = 256 * BK * 2;   // 32 KB
+constexpr int NAS = 3, NBS = 2;      // A (weight) and B (token) slots: A runs two steps ahead, B one
+constexpr int B_OFF = NAS * SLOT;
+constexpr int LDS_BYTES = (NAS + NBS) * SLOT;
+static_assert(LDS_BYTES <= 160 * 1024, "LDS");
+typedef short s4 __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ int swz_k(int r) { return ((r >> 1) & 1) * 4 | ((r >> 2) & 1) * 2; }
+
+// Lane offset in a k-major slot of read half h of a 32-column tile of parity
+// tp: rows 4h .. 4h+3 of k group lane / 32 (sub-step s: + 2048 s; column
+// group nb: + 8192 nb).
+__device__ __forceinline__ unsigned tr_off(int lane, int tp, int h) {
+    const int i = lane & 15, n16 = (lane >> 4) & 1, lh = lane >> 5;
+    const int r = 4 * h + (i >> 2), c = 4 * tp + 2 * n16 + ((i & 3) >> 1);
+    return lh * 1024 + r * 128 + ((c ^ swz_k(r)) << 4) + (i & 1) * 8;
+}
+__device__ __forceinline__ h4 tr_read(const unsigned char *p) {
+    return __builtin_bit_cast(
+        h4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4 *)p));
+}
+
+// DMA source of a k-major slot: wave w fills column group w, instruction j
+// k rows 8j .. 8j+7; byte offset of this lane from (first k row, the wave's
+// first column) in a matrix of N columns.
+__device__ __forceinline__ unsigned k_major_off(int lane, int j, int64_t N) {
+    const int r = lane >> 3, c = (lane & 7) ^ swz_k(r);
+    return (unsigned)(((int64_t)(8 * j + r) * N + 8 * c) * 2);
+}
+
+struct OpsBase {
+    typedef h8 Frag;
+    static constexpr int DMAS = 16, LATE = 8, PARTS = 4, PRE = 3;
+    __device__ __forceinline__ void step(int) {}
+    __device__ __forceinline__ void next() {}
+    template <int S>
+    __device__ __forceinline__ void mma(const Frag &x, const Frag &y, f16x &c, int, int) {
+        c = __builtin_amdgcn_mfma_f32_32x32x16_f16(x, y, c, 0, 0, 0);
+    }
+};
+
+// A: weight rows k-major [K, N]; B: token rows row-major [rows, K].  The sum
+// may run over two pairs of matrices of K = 64 n1 each, one after the other.
+struct RowOps : OpsBase {
+    static constexpr int AR = 2, BR = 1;
+    unsigned char *smem;
+    unsigned dwave;
+    const _Float16 *w[2], *t[2];  // uniform bases of the two pairs
+    unsigned woff[8], toff[8];
+    int64_t wstep;                // elements per K step: 64 N
+    int nk, n1;
+    unsigned la[2][2];            // tr_off of tile parity, half
+    int nb0;                      // first column group of this wave's A half
+    int trow0, lr, lh;
+
+    __device__ __forceinline__ void dma(int d, int j) {
+        if (d < 8) {
+            const int k = min(j + NBS, nk - 1), two = k >= n1;
+            dma16_sb((two ? t[1] : t[0]) + (int64_t)(two ? k - n1 : k) * BK, toff[d],
+                     dwave + B_OFF + ((j + NBS) % NBS) * SLOT + 1024 * d);
+        } else {
+            const int k = min(j + NAS, nk - 1), two = k >= n1;
+            dma16_sb((two ? w[1] : w[0]) + (int64_t)(two ? k - n1 : k) * wstep, woff[d - 8],
+                     dwave + ((j + NAS) % NAS) * SLOT + 1024 * (d - 8));
+        }
+    }
+    __device__ __forceinline__ void read(int k, int s, int i, Frag *a, Frag *b) {
+        if (i < 8) {
+            const int tt = i >> 1, h = i & 1;
+            const h4 v = tr_read(smem + (k % NAS) * SLOT + (nb0 + (tt >> 1)) * 8192 + 2048 * s + la[tt & 1][h]);
+            if (h) a[tt].hi = v; else a[tt].lo = v;
+        } else {
+            b[i - 8] = *(const h8 *)(smem + B_OFF + (k % NBS) * SLOT + lds_off(trow0 + 32 * (i - 8) + lr, 2 * s + lh));
+        }
+    }
+    __device__ __forceinline__ void publish(int) {}
+};
+
+// A and B k-major: the sum runs over token rows.
+struct ColOps : OpsBase {
+    static constexpr int AR = 2, BR = 2;
+    unsigned char *smem;
+    unsigned dwave;
+    const _Float16 *a, *b;
+    unsigned aoff[8], boff[8];
+    int64_t astep, bstep;
+    int nk, tail;                 // rows of the last step, 0: a whole one
+    unsigned la[2][2];
+    int na0, nb0;                 // first column groups of this wave's halves
+
+    __device__ __forceinline__ void dma(int d, int j) {
+        if (d < 8)
+            dma16_sb(b + (int64_t)min(j + NBS, nk - 1) * bstep, boff[d],
+                     dwave + B_OFF + ((j + NBS) % NBS) * SLOT + 1024 * d);
+        else
+            dma16_sb(a + (int64_t)min(j + NAS, nk - 1) * astep, aoff[d - 8],
+                     dwave + ((j + NAS) % NAS) * SLOT + 1024 * (d - 8));
+    }
+    __device__ __forceinline__ void read(int k, int s, int i, Frag *fa, Frag *fb) {
+        const int tt = (i & 7) >> 1, h = i & 1;
+        const unsigned char *slot = i < 8 ? smem + (k % NAS) * SLOT : smem + B_OFF + (k % NBS) * SLOT;
+        const h4 v = tr_read(slot + ((i < 8 ? na0 : nb0) + (tt >> 1)) * 8192 + 2048 * s + la[tt & 1][h]);
+        Frag *f = i < 8 ? fa : fb;
+        if (h) f[tt].hi = v; else f[tt].lo = v;
+    }
+    // the rows past the group's last one hold padding (anything): zero them
+    // in both operands before anyone reads the last step
+    __device__ __forceinline__ void publish(int k) {
+        if (k != nk - 1 || tail == 0) return;
+        unsigned char *sa = smem + (k % NAS) * SLOT, *sb = smem + B_OFF + (k % NBS) * SLOT;
+        const int i = threadIdx.x & 31;  // column group i / 8, chunk i % 8
+        const h8 z = {0, 0, 0, 0, 0, 0, 0, 0};
+        for (int r = tail + (threadIdx.x >> 5); r < BK; r += 8) {
+            const int o = (i >> 3) * 8192 + (r >> 3) * 1024 + (r & 7) * 128 + (i & 7) * 16;
+            *(h8 *)(sa + o) = z;
+            *(h8 *)(sb + o) = z;
+        }
+        __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+        bar();
+    }
+};
+
+// Piece of this wave's LDS for staging: 8 KB in each slot, which only its own
+// DMAs fill (all landed after the K loop), and no wave reads the ring after
+// the last barrier.  32 rows of 256 bytes per piece.
+__device__ __forceinline__ unsigned char *stage_row(unsigned char *smem, int wave, int row) {
+    return smem + (row / 32) * SLOT + wave * 8192 + (row % 32) * 256;
+}
+
+// The wave's 128 x 128 block as fp16 rows of 128 columns: B index (token or
+// output row) = row, A index = column.  Staged, then stored as whole lines.
+template <bool NT>
+__device__ __forceinline__ void store_block(const f16x (&acc)[4][4], unsigned char *smem, int wave, int lane, int ntt,
+                                            int rows, _Float16 *y, int64_t N) {
+    const int lr = lane & 31, lh = lane >> 5;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        if (u >= ntt) continue;
+        const int row = 32 * u + lr;
+        unsigned char *srow = stage_row(smem, wave, row);
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const f16x &o = acc[t][u];
+                const int c = (4 * t + q) ^ (row & 15);
+                *(h4 *)(srow + (c << 4) + 8 * lh) = to_h4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+            }
+    }
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): this wave's staging writes are done
+    const int c = lane & 15;
+#pragma unroll 4
+    for (int r0 = 0; r0 < 32 * ntt; r0 += 4) {
+        const int row = r0 + (lane >> 4);
+        if (row >= rows) continue;
+        const h8 v = *(const h8 *)(stage_row(smem, wave, row) + ((c ^ (row & 15)) << 4));
+        h8 *dst = (h8 *)(y + (int64_t)row * N + 8 * c);
+        if constexpr (NT)
+            __builtin_nontemporal_store(v, dst);
+        else
+            *dst = v;
+    }
+}
+
+// Sum over the 16 lanes of a row (DPP rotations: every lane gets it).
+template <int CTRL>
+__device__ __forceinline__ float rot(float x) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, x), CTRL, 0xf, 0xf, true));
+}
+__device__ __forceinline__ float sum16(float x) {
+    x += rot<0x128>(x);  // row_ror:8
+    x += rot<0x124>(x);
+    x += rot<0x122>(x);
+    x += rot<0x121>(x);
+    return x;
+}
+
+// One work item of a row product (rmoe_sched.h): blocks bx, bx + 1 of expert
+// e against 256 columns.  HID: the hidden stage (b = dy . Wd and everything
+// that follows from it element by element); otherwise dx.
+template <bool HID>
+__device__ __forceinline__ void run_rows(const TrainArgs &a, unsigned char *smem, const TileItem &it) {
+    const int rows0 = a.gidx[it.bx] == it.e ? it.rows0 : 0;
+    const int rows1 = (it.rows1 > 0 && a.gidx[it.bx + 1] == it.e) ? it.rows1 : 0;
+    if (rows0 == 0 && rows1 == 0) return;
+    const bool has1 = rows1 > 0;
+    const int64_t K = HID ? a.H : a.I, N = HID ? a.I : a.H;  // of one pair of matrices
+    int tid = threadIdx.x;
+    asm volatile("" : "+v"(tid));  // opaque per item: addresses are not hoisted out of the item loop
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int lane = tid & 63, lr = lane & 31, lh = lane >> 5;
+    const int ww = wave & 1, wt = wave >> 1;  // column half, token half
+    const int64_t n0 = (int64_t)it.nt * 256;
+
+    RowOps p;
+    p.smem = smem;
+    p.dwave = (unsigned)(uintptr_t)smem + 8192 * wave;
+    p.n1 = (int)(K / BK);
+    p.nk = HID ? p.n1 : 2 * p.n1;
+    p.wstep = BK * N;
+    int64_t col = n0 + 64 * wave;
+    col = col < N ? col : N - 64;  // a narrow last slice: idle columns read valid ones
+    const int64_t wofs = (int64_t)it.e * K * N + col, tofs = (int64_t)it.bx * kBlockM * K;
+    p.w[0] = (HID ? a.wd : a.wg) + wofs;
+    p.t[0] = (HID ? a.dy : a.dg) + tofs;
+    p.w[1] = HID ? p.w[0] : a.wu + wofs;
+    p.t[1] = HID ? p.t[0] : a.du + tofs;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        p.woff[j] = k_major_off(lane, j, N);
+        const int r = 64 * wave + 8 * j + (lane >> 3);
+        const int c = (lane & 7) ^ lds_swz(r);
+        int tr = r;
+        if (r >= kBlockM && !has1) tr -= kBlockM;  // absent second block: stay in bounds
+        p.toff[j] = (unsigned)((tr * K + 8 * c) * 2);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p.la[i >> 1][i & 1] = tr_off(lane, i >> 1, i & 1);
+    p.nb0 = 2 * ww;
+    p.trow0 = 128 * wt;
+    p.lr = lr;
+    p.lh = lh;
+
+    const int rows = wt ? rows1 : rows0;
+    const bool live = n0 + 128 * ww < N;
+    const int ntt = live ? (rows + 31) / 32 : 0;
+    f16x acc[4][4];
+    zero_acc(acc);
+    kloop_tiles(p, p.nk, ntt, acc);
+    if (ntt == 0) return;
+    const int64_t row0 = (int64_t)(it.bx + wt) * kBlockM, col0 = n0 + 128 * ww;
+    if constexpr (!HID) {
+        store_block<false>(acc, smem, wave, lane, ntt, rows, a.dx + row0 * N + col0, N);
+    } else {
+        // 32 tokens at a time: b staged in fp32 (512 bytes per row over two
+        // pieces: columns 0-63 and 64-127), read back 8 columns per lane, 16
+        // lanes per row, next to 16-byte loads of g and u
+        const int64_t c0 = a.go[it.e] + it.off + kBlockM * wt;  // compact index of the block's first row
+        const int r4 = lane >> 4, cl = lane & 15;
+        const int64_t np = N / 128;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            if (u >= ntt) continue;
+            h8 g[8], p8[8];
+            float w[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int row = 32 * u + 4 * i + r4;
+                if (row < rows) {
+                    const int64_t o = (row0 + row) * N + col0 + 8 * cl;
+                    g[i] = *(const h8 *)(a.g + o);
+                    p8[i] = *(const h8 *)(a.u + o);
+                    w[i] = a.rw[c0 + row];
+                }
+            }
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const f16x &o = acc[t][u];
+                    const int c = (8 * (t & 1) + 2 * q + lh) ^ (lr & 15);
+                    *(f4 *)(smem + (t >> 1) * SLOT + wave * 8192 + lr * 256 + (c << 4)) =
+                        f4{o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]};
+                }
+            __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int sr = 4 * i + r4, row = 32 * u + sr;
+                const unsigned char *src = smem + (cl >> 3) * SLOT + wave * 8192 + sr * 256;
+                const int c = 2 * (cl & 7);
+                const f4 b0 = *(const f4 *)(src + ((c ^ (sr & 15)) << 4));
+                const f4 b1 = *(const f4 *)(src + (((c + 1) ^ (sr & 15)) << 4));
+                float dw = 0.f;
+                h8 dg, du, hw;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float b = j < 4 ? b0[j & 3] : b1[j & 3];
+                    const float gf = (float)g[i][j], uf = (float)p8[i][j];
+                    const float s = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-gf * 1.4426950408889634f));
+                    const float sl = gf * s, h = sl * uf, dh = w[i] * b;
+                    dw += b * h;
+                    dg[j] = (_Float16)(dh * uf * (s + sl * (1.0f - s)));
+                    du[j] = (_Float16)(dh * sl);
+                    hw[j] = (_Float16)(w[i] * h);
+                }
+                dw = sum16(dw);
+                if (row < rows) {
+                    const int64_t o = (row0 + row) * N + col0 + 8 * cl;
+                    *(h8 *)(a.dg + o) = dg;
+                    *(h8 *)(a.du + o) = du;
+                    *(h8 *)(a.hw + o) = hw;
+                    if (cl == 0) a.part[(c0 + row) * np + col0 / 128] = dw;
+                }
+            }
+        }
+    }
+}
+
+// Persistent, one workgroup per CU, items in the order of rmoe_sched.h.
+template <bool HID>
+__global__ __launch_bounds__(256) void rows_kernel(TrainArgs a, int NT) {
+    extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
+    const TileSeq seq = tile_seq(a.gs, a.E, NT, blockIdx.x % kXcd, kXcd);
+    const int nl = gridDim.x / kXcd;
+    TileCursor cur;
+    for (int i = blockIdx.x / kXcd; i < seq.n; i += nl) run_rows<HID>(a, smem, tile_item(a.gs, a.gpo, seq, i, cur));
+}
+
+// drw[c] = the sum of c's partial sums in ascending order of their columns:
+// 16 lanes per c, then over the lanes
+__global__ __launch_bounds__(256) void drw_kernel(const float *part, const int32_t *go, int32_t E, int64_t pairs,
+                                                  int np, float *drw) {
+    const int64_t n = min((int64_t)go[E], pairs);
+    const int l = threadIdx.x & 15;
+    for (int64_t c0 = (int64_t)blockIdx.x * 16; c0 < n; c0 += (int64_t)gridDim.x * 16) {
+        const int64_t c = c0 + (threadIdx.x >> 4);
+        float s = 0.f;
+        if (c < n)
+            for (int j = l; j < np; j += 16) s += part[c * np + j];
+        s = sum16(s);
+        if (c < n && l == 0) drw[c] = s;
+    }
+}
+
+// Weight gradients: every 256 x 256 tile of the three matrices of every
+// expert, its sum over the expert's rows.  An expert without rows gets
+// zeros.  Workgroups are dealt to the XCDs in runs of 32 consecutive tiles
+// (4 rows of tiles x 8), which share operands in that XCD's L2; heavy
+// experts spread over all XCDs, and the hardware starts the next tile
+// wherever a CU is free.
+__global__ __launch_bounds__(256) void cols_kernel(TrainArgs a, int total) {
+    extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
+    const int xcd = blockIdx.x % kXcd, seq = blockIdx.x / kXcd;
+    const int item = ((seq / 32) * kXcd + xcd) * 32 + seq % 32;
+    if (item >= total) return;
+    const int nh = (int)((a.H + 255) / 256), ni = (int)((a.I + 255) / 256), per = nh * ni;
+    const int e = item / (3 * per), m = (item / per) % 3, q = item % per;
+    // matrix m: A columns (contiguous in the output), B columns (its rows)
+    const int64_t NA = m < 2 ? a.H : a.I, NB = m < 2 ? a.I : a.H;
+    const int nA = m < 2 ? nh : ni, nB = m < 2 ? ni : nh;
+    const int g = q / (8 * nB), width = min(8, nA - 8 * g), r = q - 8 * g * nB;
+    const int64_t a0 = (int64_t)(8 * g + r % width) * 256, b0 = (int64_t)(r / width) * 256;
+    const int n = a.gs[e];
+    const int64_t row0 = a.gpo[e];
+    const int nk = (n + BK - 1) / BK;
+    // tables that break the contract: nothing read out of bounds, tile left out
+    if (n < 0 || row0 < 0 || row0 + (int64_t)nk * BK > a.Tp) return;
+
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63;
+    const int ww = wave & 1, wt = wave >> 1;
+    const int ntt = a0 + 128 * ww < NA && b0 + 128 * wt < NB ? 4 : 0;
+    f16x acc[4][4];
+    zero_acc(acc);
+    if (nk > 0) {
+        ColOps p;
+        p.smem = smem;
+        p.dwave = (unsigned)(uintptr_t)smem + 8192 * wave;
+        p.nk = nk;
+        p.tail = n % BK;
+        p.astep = BK * NA;
+        p.bstep = BK * NB;
+        int64_t ca = a0 + 64 * wave, cb = b0 + 64 * wave;
+        ca = ca < NA ? ca : NA - 64;  // narrow last tiles: idle columns read valid ones
+        cb = cb < NB ? cb : NB - 64;
+        p.a = (m < 2 ? a.x : a.hw) + row0 * NA + ca;
+        p.b = (m == 0 ? a.dg : m == 1 ? a.du : a.dy) + row0 * NB + cb;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            p.aoff[j] = k_major_off(lane, j, NA);
+            p.boff[j] = k_major_off(lane, j, NB);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p.la[i >> 1][i & 1] = tr_off(lane, i >> 1, i & 1);
+        p.na0 = 2 * ww;
+        p.nb0 = 2 * wt;
+        if (ntt)
+            kloop<4>(p, nk, acc);
+        else
+            kloop<0>(p, nk, acc);
+    }
+    if (ntt == 0) return;
+    _Float16 *y = (m == 0 ? a.dwg : m == 1 ? a.dwu : a.dwd) + (int64_t)e * NA * NB;
+    store_block<true>(acc, smem, wave, lane, 4, 128, y + (b0 + 128 * wt) * NA + a0 + 128 * ww, NA);
+}
+
+template <bool HID>
+hipError_t launch_rows(const TrainArgs &a, hipStream_t s) {
+    unsigned grid = 0;
+    hipError_t e = persistent_grid(grid);
+    if (e != hipSuccess) return e;
+    static std::atomic<uint64_t> lds_set{0};
+    e = lds_opt_in_once((const void *)rows_kernel<HID>, LDS_BYTES, lds_set);
+    if (e != hipSuccess) return e;
+    const int64_t N = HID ? a.I : a.H;
+    hipLaunchKernelGGL(rows_kernel<HID>, dim3(grid), dim3(256), LDS_BYTES, s, a, (int)((N + 255) / 256));
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_down_backward(const TrainArgs &a, hipStream_t s) {
+    const hipError_t e = launch_rows<true>(a, s);
+    if (e != hipSuccess) return e;
+    int64_t g = (a.pairs + 15) / 16;
+    if (g > 256 * 16) g = 256 * 16;  // strides beyond
+    if (g == 0) return hipSuccess;
+    hipLaunchKernelGGL(drw_kernel, dim3((unsigned)g), dim3(256), 0, s, a.part, a.go, a.E, a.pairs, (int)(a.I / 128),
+                       a.drw);
+    return hipGetLastError();
+}
+
+hipError_t launch_gate_up_backward(const TrainArgs &a, hipStream_t s) { return launch_rows<false>(a, s); }
+
+int64_t weight_grad_tiles(int64_t H, int64_t I, int32_t E) {
+    return 3 * (int64_t)E * ((H + 255) / 256) * ((I + 255) / 256);
+}
+
+hipError_t launch_weight_grad(const TrainArgs &a, hipStream_t s) {
+    static std::atomic<uint64_t> lds_set{0};
+    hipError_t e = lds_opt_in_once((const void *)cols_kernel, LDS_BYTES, lds_set);
+    if (e != hipSuccess) return e;
+    const int64_t total = weight_grad_tiles(a.H, a.I, a.E);
+    const int64_t grid = (total + 255) / 256 * 256;  // whole runs of 32 on each of 8 XCDs
+    hipLaunchKernelGGL(cols_kernel, dim3((unsigned)grid), dim3(256), LDS_BYTES, s, a, (int)total);
+    return hipGetLastError();
+}
+
+}  // namespace rmoe
