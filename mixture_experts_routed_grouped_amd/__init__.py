@@ -14,6 +14,7 @@ the fp16 hidden workspace per (device, rows, intermediate).
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import numpy as np
@@ -236,9 +237,16 @@ def pick_variant(num_pairs: int, num_experts: int, variant="auto", max_group_row
 
 
 # ------------------------------------------------------------- device calls
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    """torch, imported by the first device call."""
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _dev(t, dtype, name):
@@ -538,40 +546,73 @@ def build_contract_device_noalloc(topk_ids, num_experts: int, out: dict, stream=
 
 
 # ------------------------------------------------------------- MXFP4
-def _same_device(first, **tensors):
-    """The tensors live on ``first``'s device; returns a context in which
-    that device is current (a launch goes to the current device)."""
-    torch = _torch()
-    for name, t in tensors.items():
-        if isinstance(t, torch.Tensor) and t.is_cuda and t.device != first.device:
-            raise ValueError(f"{name} is on {t.device}, not on {first.device}")
-    return torch.cuda.device(first.device)
+# The entries below check every argument in one pass over plain attributes:
+# a call on a decode batch takes about as long on the host as its kernels on
+# the GPU.
+def _gpu(t, name):
+    """Index of the GPU that ``t`` lives on."""
+    if not isinstance(t, _torch().Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must live in GPU memory")
+    return t.get_device()
 
 
-def _shape(t, shape, name):
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+def _arg(dev, name, t, dtype, *shape):
+    """Address of a contiguous tensor of this type (and shape, if given) on
+    GPU ``dev``; anything else is refused by name."""
+    try:
+        if t.dtype is dtype and t.get_device() == dev and t.is_contiguous() and (not shape or t.shape == shape):
+            return t.data_ptr()
+    except AttributeError:
+        raise TypeError(f"{name} must be a torch tensor") from None
+    _dev(t, dtype, name)
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on GPU {t.get_device()}, not on GPU {dev}")
+    raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
 
 
-def _empty(shape, dtype, device, stream):
-    """An uninitialised tensor that belongs to ``stream`` (default: the
-    current one), so its memory is not handed out again before that stream
-    is done with it."""
+def _call(fn, dev, stream, *args):
+    """Call a library entry with GPU ``dev`` current (a launch goes to the
+    current one) and ``stream``, or that GPU's current stream, as its last
+    argument."""
     torch = _torch()
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        # the handle alone: building a Stream object costs as much as a launch
+        handle = torch._C._cuda_getCurrentRawStream(dev)
+    else:
+        handle = int(getattr(stream, "cuda_stream", stream))
+    if torch.cuda.current_device() == dev:
+        st = getattr(lib(), fn)(*args, handle)
+    else:
+        with torch.cuda.device(dev):
+            st = getattr(lib(), fn)(*args, handle)
+    if st:
+        _check(st, fn)
+
+
+def _empty(shape, dtype, dev, stream):
+    """An uninitialised tensor on GPU ``dev`` that belongs to ``stream``
+    (default: the current one), so its memory is not handed out again before
+    that stream is done with it."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
     if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream), device=device)
+        stream = torch.cuda.ExternalStream(int(stream), device=dev)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=dtype, device=dev)
 
 
 def _mx_type(dtype):
     torch = _torch()
-    types = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
-    if dtype not in types:
-        raise TypeError(f"MXFP4 converts float16, bfloat16 and float32, not {dtype}")
-    return types[dtype]
+    if dtype is torch.float16:
+        return 0
+    if dtype is torch.bfloat16:
+        return 1
+    if dtype is torch.float32:
+        return 2
+    raise TypeError(f"MXFP4 converts float16, bfloat16 and float32, not {dtype}")
 
 
 def mxfp4_row_bytes(cols: int) -> int:
@@ -579,34 +620,37 @@ def mxfp4_row_bytes(cols: int) -> int:
     return int(lib().rmoe_mxfp4_row_bytes(int(cols)))
 
 
+@functools.lru_cache(maxsize=1024)
+def _mx_row(cols):
+    """(code bytes, chunks) of a row."""
+    return mxfp4_row_bytes(cols), int(lib().rmoe_mxfp4_chunks(cols))
+
+
 def mxfp4_shapes(shape) -> tuple[tuple, tuple]:
     """Shapes of the uint8 ``codes`` and ``scales`` of a matrix [rows, cols]
     or a batch of them [batch, rows, cols] (layout: rmoe_quantize_mxfp4)."""
     if len(shape) not in (2, 3):
         raise ValueError("MXFP4 tensors are [rows, cols] or [batch, rows, cols]")
-    *batch, rows, cols = (int(n) for n in shape)
-    return (*batch, rows, mxfp4_row_bytes(cols)), (*batch, int(lib().rmoe_mxfp4_chunks(cols)), rows, 8)
+    *batch, rows, cols = shape
+    row, chunks = _mx_row(int(cols))
+    return (*batch, rows, row), (*batch, chunks, rows, 8)
 
 
 def quantize_mxfp4(x, codes=None, scales=None, stream=None):
     """MXFP4 of ``x`` [rows, cols] or [batch, rows, cols] (fp16, bf16 or fp32;
     cols a multiple of 8): returns ``(codes, scales)``, uint8 tensors of
     ``mxfp4_shapes(x.shape)`` (allocated unless given)."""
-    torch = _torch()
-    px, ty = _dev(x, x.dtype, "x"), _mx_type(x.dtype)
-    cs, ss = mxfp4_shapes(x.shape)
+    u8 = _torch().uint8
+    dev = _gpu(x, "x")
+    ty, px = _mx_type(x.dtype), _arg(dev, "x", x, x.dtype)
+    shape = x.shape
+    cs, ss = mxfp4_shapes(shape)
     if codes is None:
-        codes = _empty(cs, torch.uint8, x.device, stream)
+        codes = _empty(cs, u8, dev, stream)
     if scales is None:
-        scales = _empty(ss, torch.uint8, x.device, stream)
-    _shape(codes, cs, "codes")
-    _shape(scales, ss, "scales")
-    batch = x.shape[0] if x.dim() == 3 else 1
-    with _same_device(x, codes=codes, scales=scales):
-        st = lib().rmoe_quantize_mxfp4(px, ty, batch, x.shape[-2], x.shape[-1],
-                                       _dev(codes, torch.uint8, "codes"),
-                                       _dev(scales, torch.uint8, "scales"), _stream(x, stream))
-    _check(st, "rmoe_quantize_mxfp4")
+        scales = _empty(ss, u8, dev, stream)
+    _call("rmoe_quantize_mxfp4", dev, stream, px, ty, shape[0] if len(shape) == 3 else 1, shape[-2], shape[-1],
+          _arg(dev, "codes", codes, u8, *cs), _arg(dev, "scales", scales, u8, *ss))
     return codes, scales
 
 
@@ -614,23 +658,17 @@ def dequantize_mxfp4(codes, scales, cols: int, dtype=None, out=None, stream=None
     """The values of MXFP4 ``codes`` and ``scales`` of rows of ``cols``
     elements, as ``dtype`` (default fp16), in ``out`` if given."""
     torch = _torch()
-    if out is not None and dtype is not None and out.dtype != dtype:
-        raise TypeError(f"out must be {dtype}, got {out.dtype}")
-    dtype = out.dtype if out is not None else torch.float16 if dtype is None else dtype
-    ty = _mx_type(dtype)
+    u8 = torch.uint8
+    if dtype is None:
+        dtype = torch.float16 if out is None else out.dtype
+    ty, dev = _mx_type(dtype), _gpu(codes, "codes")
     shape = (*codes.shape[:-1], int(cols))
     cs, ss = mxfp4_shapes(shape)
-    _shape(codes, cs, "codes")
-    _shape(scales, ss, "scales")
-    pc, ps = _dev(codes, torch.uint8, "codes"), _dev(scales, torch.uint8, "scales")
+    pc, ps = _arg(dev, "codes", codes, u8, *cs), _arg(dev, "scales", scales, u8, *ss)
     if out is None:
-        out = _empty(shape, dtype, codes.device, stream)
-    _shape(out, shape, "out")
-    batch = shape[0] if len(shape) == 3 else 1
-    with _same_device(codes, scales=scales, out=out):
-        st = lib().rmoe_dequantize_mxfp4(pc, ps, ty, batch, shape[-2], shape[-1], _dev(out, dtype, "out"),
-                                         _stream(codes, stream))
-    _check(st, "rmoe_dequantize_mxfp4")
+        out = _empty(shape, dtype, dev, stream)
+    _call("rmoe_dequantize_mxfp4", dev, stream, pc, ps, ty, shape[0] if len(shape) == 3 else 1, shape[-2], shape[-1],
+          _arg(dev, "out", out, dtype, *shape))
     return out
 
 
@@ -640,6 +678,8 @@ def pack_mxfp4(x, topk_weights, padded_row_of_pair, compact_pos_of_pair, codes, 
     codes and scales are written to its padded rows of ``codes`` [Tp, row
     bytes] and ``scales`` [chunks, Tp, 8]."""
     torch = _torch()
+    u8, i32, f32 = torch.uint8, torch.int32, torch.float32
+    dev = _gpu(x, "x")
     T, H = x.shape
     pairs = topk_weights.numel()
     k = pairs // T if T else 0
@@ -648,18 +688,11 @@ def pack_mxfp4(x, topk_weights, padded_row_of_pair, compact_pos_of_pair, codes, 
         raise ValueError("topk_weights, the pair tables and w_compact must have num_tokens * top_k entries")
     Tp = codes.shape[0]
     cs, ss = mxfp4_shapes((Tp, H))
-    _shape(codes, cs, "codes")
-    _shape(scales, ss, "scales")
-    with _same_device(x, topk_weights=topk_weights, padded_row_of_pair=padded_row_of_pair,
-                      compact_pos_of_pair=compact_pos_of_pair, codes=codes, scales=scales,
-                      w_compact=w_compact):
-        st = lib().rmoe_pack_mxfp4_f16(
-            _dev(x, torch.float16, "x"), _dev(topk_weights, torch.float32, "topk_weights"),
-            _dev(padded_row_of_pair, torch.int32, "padded_row_of_pair"),
-            _dev(compact_pos_of_pair, torch.int32, "compact_pos_of_pair"), T, k, H,
-            _dev(codes, torch.uint8, "codes"), _dev(scales, torch.uint8, "scales"),
-            _dev(w_compact, torch.float32, "w_compact"), Tp, _stream(x, stream))
-    _check(st, "rmoe_pack_mxfp4_f16")
+    _call("rmoe_pack_mxfp4_f16", dev, stream, _arg(dev, "x", x, torch.float16),
+          _arg(dev, "topk_weights", topk_weights, f32), _arg(dev, "padded_row_of_pair", padded_row_of_pair, i32),
+          _arg(dev, "compact_pos_of_pair", compact_pos_of_pair, i32), T, k, H,
+          _arg(dev, "codes", codes, u8, *cs), _arg(dev, "scales", scales, u8, *ss),
+          _arg(dev, "w_compact", w_compact, f32), Tp)
 
 
 def mxfp4_workspace_bytes(total_padded_tokens: int, intermediate: int) -> int:
@@ -675,17 +708,15 @@ def pick_variant_mxfp4(num_pairs: int, num_experts: int, variant="auto") -> str:
     return _VARIANT_NAMES[v]
 
 
-def _tables(E, M, group_sizes, group_padded_offsets, group_idx_for_bx, group_offsets=None):
-    """Device pointers of the contract's tables after their sizes' check."""
+def _tables(dev, E, M, group_sizes, group_padded_offsets, group_idx_for_bx, group_offsets=None):
+    """Addresses of the contract's tables, in the entries' order."""
     i32 = _torch().int32
-    if group_sizes.numel() != E or group_padded_offsets.numel() != E + 1 or \
-            (group_offsets is not None and group_offsets.numel() != E + 1):
-        raise ValueError("group tables must have E, E+1, E+1 entries")
-    out = [_dev(group_sizes, i32, "group_sizes")]
-    if group_offsets is not None:
-        out.append(_dev(group_offsets, i32, "group_offsets"))
-    return out + [_dev(group_padded_offsets, i32, "group_padded_offsets"),
-                  _dev(group_idx_for_bx, i32, "group_idx_for_bx")]
+    sizes = _arg(dev, "group_sizes", group_sizes, i32, E)
+    padded = _arg(dev, "group_padded_offsets", group_padded_offsets, i32, E + 1)
+    blocks = _arg(dev, "group_idx_for_bx", group_idx_for_bx, i32, M)
+    if group_offsets is None:
+        return sizes, padded, blocks
+    return sizes, _arg(dev, "group_offsets", group_offsets, i32, E + 1), padded, blocks
 
 
 def forward_mxfp4(token_codes, token_scales, gate_codes, gate_scales, up_codes, up_scales, down_codes,
@@ -698,34 +729,22 @@ def forward_mxfp4(token_codes, token_scales, gate_codes, gate_scales, up_codes, 
     written.  Asynchronous on ``stream``."""
     torch = _torch()
     u8 = torch.uint8
+    dev = _gpu(out, "out")
     Tp, H = out.shape
     E, I = gate_codes.shape[:2]
-    for name, c, s, shape in (("token", token_codes, token_scales, (Tp, H)),
-                              ("gate", gate_codes, gate_scales, (E, I, H)),
-                              ("up", up_codes, up_scales, (E, I, H)),
-                              ("down", down_codes, down_scales, (E, H, I))):
-        cs, ss = mxfp4_shapes(shape)
-        _shape(c, cs, f"{name}_codes")
-        _shape(s, ss, f"{name}_scales")
+    (rh, ch), (ri, ci) = _mx_row(H), _mx_row(I)
+    M, pairs = group_idx_for_bx.numel(), routed_expert_weights.numel()
     if workspace.numel() < mxfp4_workspace_bytes(Tp, I):
         raise ValueError("workspace too small")
-    M = group_idx_for_bx.numel()
-    with _same_device(out, token_codes=token_codes, token_scales=token_scales, gate_codes=gate_codes,
-                      gate_scales=gate_scales, up_codes=up_codes, up_scales=up_scales,
-                      down_codes=down_codes, down_scales=down_scales, workspace=workspace,
-                      routed_expert_weights=routed_expert_weights, group_sizes=group_sizes,
-                      group_offsets=group_offsets, group_padded_offsets=group_padded_offsets,
-                      group_idx_for_bx=group_idx_for_bx):
-        st = lib().rmoe_forward_mxfp4(
-            _dev(token_codes, u8, "token_codes"), _dev(token_scales, u8, "token_scales"),
-            _dev(gate_codes, u8, "gate_codes"), _dev(gate_scales, u8, "gate_scales"),
-            _dev(up_codes, u8, "up_codes"), _dev(up_scales, u8, "up_scales"),
-            _dev(down_codes, u8, "down_codes"), _dev(down_scales, u8, "down_scales"),
-            _dev(routed_expert_weights, torch.float32, "routed_expert_weights"),
-            *_tables(E, M, group_sizes, group_padded_offsets, group_idx_for_bx, group_offsets),
-            _dev(workspace, u8, "workspace"), _dev(out, torch.float16, "out"), H, I, E, Tp,
-            routed_expert_weights.numel(), M, _VARIANTS[variant], _stream(out, stream))
-    _check(st, "rmoe_forward_mxfp4")
+    _call("rmoe_forward_mxfp4", dev, stream,
+          _arg(dev, "token_codes", token_codes, u8, Tp, rh), _arg(dev, "token_scales", token_scales, u8, ch, Tp, 8),
+          _arg(dev, "gate_codes", gate_codes, u8, E, I, rh), _arg(dev, "gate_scales", gate_scales, u8, E, ch, I, 8),
+          _arg(dev, "up_codes", up_codes, u8, E, I, rh), _arg(dev, "up_scales", up_scales, u8, E, ch, I, 8),
+          _arg(dev, "down_codes", down_codes, u8, E, H, ri), _arg(dev, "down_scales", down_scales, u8, E, ci, H, 8),
+          _arg(dev, "routed_expert_weights", routed_expert_weights, torch.float32),
+          *_tables(dev, E, M, group_sizes, group_padded_offsets, group_idx_for_bx, group_offsets),
+          _arg(dev, "workspace", workspace, u8), _arg(dev, "out", out, torch.float16), H, I, E, Tp, pairs, M,
+          _VARIANTS[variant])
 
 
 def gate_up_mxfp4(token_codes, token_scales, gate_codes, gate_scales, up_codes, up_scales, group_sizes,
@@ -734,31 +753,19 @@ def gate_up_mxfp4(token_codes, token_scales, gate_codes, gate_scales, up_codes, 
     """Stage 1 of ``forward_mxfp4`` alone: the hidden rows' codes [Tp, row
     bytes(I)] and scales [chunks(I), Tp, 8].  ``hidden`` is H, the tokens'
     row length; ``num_pairs`` feeds the family choice."""
-    torch = _torch()
-    u8 = torch.uint8
+    u8 = _torch().uint8
+    dev = _gpu(token_codes, "token_codes")
     Tp, H = token_codes.shape[0], int(hidden)
     E, I = gate_codes.shape[:2]
-    for name, c, s, shape in (("token", token_codes, token_scales, (Tp, H)),
-                              ("gate", gate_codes, gate_scales, (E, I, H)),
-                              ("up", up_codes, up_scales, (E, I, H)),
-                              ("hidden", hidden_codes, hidden_scales, (Tp, I))):
-        cs, ss = mxfp4_shapes(shape)
-        _shape(c, cs, f"{name}_codes")
-        _shape(s, ss, f"{name}_scales")
+    (rh, ch), (ri, ci) = _mx_row(H), _mx_row(I)
     M = group_idx_for_bx.numel()
-    with _same_device(token_codes, token_scales=token_scales, gate_codes=gate_codes,
-                      gate_scales=gate_scales, up_codes=up_codes, up_scales=up_scales,
-                      group_sizes=group_sizes, group_padded_offsets=group_padded_offsets,
-                      group_idx_for_bx=group_idx_for_bx, hidden_codes=hidden_codes,
-                      hidden_scales=hidden_scales):
-        st = lib().rmoe_gate_up_mxfp4(
-            _dev(token_codes, u8, "token_codes"), _dev(token_scales, u8, "token_scales"),
-            _dev(gate_codes, u8, "gate_codes"), _dev(gate_scales, u8, "gate_scales"),
-            _dev(up_codes, u8, "up_codes"), _dev(up_scales, u8, "up_scales"),
-            *_tables(E, M, group_sizes, group_padded_offsets, group_idx_for_bx),
-            _dev(hidden_codes, u8, "hidden_codes"), _dev(hidden_scales, u8, "hidden_scales"),
-            H, I, E, Tp, int(num_pairs), M, _VARIANTS[variant], _stream(token_codes, stream))
-    _check(st, "rmoe_gate_up_mxfp4")
+    _call("rmoe_gate_up_mxfp4", dev, stream,
+          _arg(dev, "token_codes", token_codes, u8, Tp, rh), _arg(dev, "token_scales", token_scales, u8, ch, Tp, 8),
+          _arg(dev, "gate_codes", gate_codes, u8, E, I, rh), _arg(dev, "gate_scales", gate_scales, u8, E, ch, I, 8),
+          _arg(dev, "up_codes", up_codes, u8, E, I, rh), _arg(dev, "up_scales", up_scales, u8, E, ch, I, 8),
+          *_tables(dev, E, M, group_sizes, group_padded_offsets, group_idx_for_bx),
+          _arg(dev, "hidden_codes", hidden_codes, u8, Tp, ri), _arg(dev, "hidden_scales", hidden_scales, u8, ci, Tp, 8),
+          H, I, E, Tp, int(num_pairs), M, _VARIANTS[variant])
 
 
 def down_mxfp4(hidden_codes, hidden_scales, down_codes, down_scales, routed_expert_weights, group_sizes,
@@ -768,26 +775,16 @@ def down_mxfp4(hidden_codes, hidden_scales, down_codes, down_scales, routed_expe
     valid rows; ``intermediate`` is I, the hidden rows' length."""
     torch = _torch()
     u8 = torch.uint8
+    dev = _gpu(out, "out")
     (Tp, H), I = out.shape, int(intermediate)
-    E = down_codes.shape[0]
-    for name, c, s, shape in (("hidden", hidden_codes, hidden_scales, (Tp, I)),
-                              ("down", down_codes, down_scales, (E, H, I))):
-        cs, ss = mxfp4_shapes(shape)
-        _shape(c, cs, f"{name}_codes")
-        _shape(s, ss, f"{name}_scales")
-    M = group_idx_for_bx.numel()
-    with _same_device(out, hidden_codes=hidden_codes, hidden_scales=hidden_scales, down_codes=down_codes,
-                      down_scales=down_scales, routed_expert_weights=routed_expert_weights,
-                      group_sizes=group_sizes, group_offsets=group_offsets,
-                      group_padded_offsets=group_padded_offsets, group_idx_for_bx=group_idx_for_bx):
-        st = lib().rmoe_down_mxfp4(
-            _dev(hidden_codes, u8, "hidden_codes"), _dev(hidden_scales, u8, "hidden_scales"),
-            _dev(down_codes, u8, "down_codes"), _dev(down_scales, u8, "down_scales"),
-            _dev(routed_expert_weights, torch.float32, "routed_expert_weights"),
-            *_tables(E, M, group_sizes, group_padded_offsets, group_idx_for_bx, group_offsets),
-            _dev(out, torch.float16, "out"), H, I, E, Tp, routed_expert_weights.numel(), M,
-            _VARIANTS[variant], _stream(out, stream))
-    _check(st, "rmoe_down_mxfp4")
+    E, M, pairs = down_codes.shape[0], group_idx_for_bx.numel(), routed_expert_weights.numel()
+    ri, ci = _mx_row(I)
+    _call("rmoe_down_mxfp4", dev, stream,
+          _arg(dev, "hidden_codes", hidden_codes, u8, Tp, ri), _arg(dev, "hidden_scales", hidden_scales, u8, ci, Tp, 8),
+          _arg(dev, "down_codes", down_codes, u8, E, H, ri), _arg(dev, "down_scales", down_scales, u8, E, ci, H, 8),
+          _arg(dev, "routed_expert_weights", routed_expert_weights, torch.float32),
+          *_tables(dev, E, M, group_sizes, group_padded_offsets, group_idx_for_bx, group_offsets),
+          _arg(dev, "out", out, torch.float16), H, I, E, Tp, pairs, M, _VARIANTS[variant])
 
 
 # ------------------------------------------------------------- training
@@ -797,21 +794,15 @@ def gate_up_train(x, gate_w, up_w, group_sizes, group_padded_offsets, group_idx_
     pre-activations.  On valid rows of the padded layout: gate = fp16(x Wg^T),
     up = fp16(x Wu^T), hidden = fp16(silu(x Wg^T) * (x Wu^T)), each [Tp, I];
     ``down`` completes the forward."""
-    torch = _torch()
-    f16 = torch.float16
+    f16 = _torch().float16
+    dev = _gpu(x, "x")
     E, I, H = gate_w.shape
     Tp, M = x.shape[0], group_idx_for_bx.numel()
-    for name, t, shape in (("x", x, (Tp, H)), ("up_w", up_w, (E, I, H)), ("gate", gate, (Tp, I)),
-                           ("up", up, (Tp, I)), ("hidden", hidden, (Tp, I))):
-        _shape(t, shape, name)
-    with _same_device(x, gate_w=gate_w, up_w=up_w, group_sizes=group_sizes,
-                      group_padded_offsets=group_padded_offsets, group_idx_for_bx=group_idx_for_bx,
-                      gate=gate, up=up, hidden=hidden):
-        st = lib().rmoe_gate_up_train_f16(
-            _dev(x, f16, "x"), _dev(gate_w, f16, "gate_w"), _dev(up_w, f16, "up_w"),
-            *_tables(E, M, group_sizes, group_padded_offsets, group_idx_for_bx), _dev(gate, f16, "gate"),
-            _dev(up, f16, "up"), _dev(hidden, f16, "hidden"), H, I, E, Tp, 0, M, _stream(x, stream))
-    _check(st, "rmoe_gate_up_train_f16")
+    _call("rmoe_gate_up_train_f16", dev, stream,
+          _arg(dev, "x", x, f16, Tp, H), _arg(dev, "gate_w", gate_w, f16), _arg(dev, "up_w", up_w, f16, E, I, H),
+          *_tables(dev, E, M, group_sizes, group_padded_offsets, group_idx_for_bx),
+          _arg(dev, "gate", gate, f16, Tp, I), _arg(dev, "up", up, f16, Tp, I),
+          _arg(dev, "hidden", hidden, f16, Tp, I), H, I, E, Tp, 0, M)
 
 
 def backward_scratch_bytes(num_pairs: int, intermediate: int) -> int:
@@ -819,13 +810,12 @@ def backward_scratch_bytes(num_pairs: int, intermediate: int) -> int:
     return int(lib().rmoe_backward_scratch_bytes(int(num_pairs), int(intermediate)))
 
 
-def _scratch(scratch, num_pairs, intermediate):
-    """Pointer of a scratch tensor of any type that holds enough bytes."""
-    if not scratch.is_cuda or not scratch.is_contiguous():
-        raise ValueError("scratch must be contiguous GPU memory")
+def _scratch(dev, scratch, num_pairs, intermediate):
+    """Address of a scratch tensor of any type that holds enough bytes."""
+    address = _arg(dev, "scratch", scratch, scratch.dtype)
     if scratch.numel() * scratch.element_size() < backward_scratch_bytes(num_pairs, intermediate):
         raise ValueError("scratch too small")
-    return ctypes.c_void_p(scratch.data_ptr())
+    return address
 
 
 def backward(x, dout, gate_w, up_w, down_w, routed_expert_weights, gate, up, group_sizes, group_offsets,
@@ -840,32 +830,20 @@ def backward(x, dout, gate_w, up_w, down_w, routed_expert_weights, gate, up, gro
     pair, compact order).  ``scratch``: ``backward_scratch_bytes(pairs, I)``."""
     torch = _torch()
     f16, f32 = torch.float16, torch.float32
+    dev = _gpu(x, "x")
     E, I, H = gate_w.shape
     Tp, M, pairs = x.shape[0], group_idx_for_bx.numel(), routed_expert_weights.numel()
-    rows_h, rows_i, w_ih = (Tp, H), (Tp, I), (E, I, H)
-    for name, t, shape in (("x", x, rows_h), ("dout", dout, rows_h), ("up_w", up_w, w_ih),
-                           ("down_w", down_w, (E, H, I)), ("gate", gate, rows_i), ("up", up, rows_i),
-                           ("dgate", dgate, rows_i), ("dup", dup, rows_i), ("whidden", whidden, rows_i),
-                           ("dx", dx, rows_h), ("dgate_w", dgate_w, w_ih), ("dup_w", dup_w, w_ih),
-                           ("ddown_w", ddown_w, (E, H, I))):
-        _shape(t, shape, name)
-    if drw.numel() != pairs:
-        raise ValueError("drw must have one entry per routed weight")
-    with _same_device(x, dout=dout, gate_w=gate_w, up_w=up_w, down_w=down_w, gate=gate, up=up,
-                      routed_expert_weights=routed_expert_weights, group_sizes=group_sizes,
-                      group_offsets=group_offsets, group_padded_offsets=group_padded_offsets,
-                      group_idx_for_bx=group_idx_for_bx, dgate=dgate, dup=dup, whidden=whidden,
-                      scratch=scratch, dx=dx, dgate_w=dgate_w, dup_w=dup_w, ddown_w=ddown_w, drw=drw):
-        st = lib().rmoe_backward_f16(
-            _dev(x, f16, "x"), _dev(dout, f16, "dout"), _dev(gate_w, f16, "gate_w"), _dev(up_w, f16, "up_w"),
-            _dev(down_w, f16, "down_w"), _dev(routed_expert_weights, f32, "routed_expert_weights"),
-            _dev(gate, f16, "gate"), _dev(up, f16, "up"),
-            *_tables(E, M, group_sizes, group_padded_offsets, group_idx_for_bx, group_offsets),
-            _dev(dgate, f16, "dgate"), _dev(dup, f16, "dup"), _dev(whidden, f16, "whidden"),
-            _scratch(scratch, pairs, I), _dev(dx, f16, "dx"), _dev(dgate_w, f16, "dgate_w"),
-            _dev(dup_w, f16, "dup_w"), _dev(ddown_w, f16, "ddown_w"), _dev(drw, f32, "drw"), H, I, E, Tp,
-            pairs, M, _stream(x, stream))
-    _check(st, "rmoe_backward_f16")
+    _call("rmoe_backward_f16", dev, stream,
+          _arg(dev, "x", x, f16, Tp, H), _arg(dev, "dout", dout, f16, Tp, H), _arg(dev, "gate_w", gate_w, f16),
+          _arg(dev, "up_w", up_w, f16, E, I, H), _arg(dev, "down_w", down_w, f16, E, H, I),
+          _arg(dev, "routed_expert_weights", routed_expert_weights, f32), _arg(dev, "gate", gate, f16, Tp, I),
+          _arg(dev, "up", up, f16, Tp, I),
+          *_tables(dev, E, M, group_sizes, group_padded_offsets, group_idx_for_bx, group_offsets),
+          _arg(dev, "dgate", dgate, f16, Tp, I), _arg(dev, "dup", dup, f16, Tp, I),
+          _arg(dev, "whidden", whidden, f16, Tp, I), _scratch(dev, scratch, pairs, I),
+          _arg(dev, "dx", dx, f16, Tp, H), _arg(dev, "dgate_w", dgate_w, f16, E, I, H),
+          _arg(dev, "dup_w", dup_w, f16, E, I, H), _arg(dev, "ddown_w", ddown_w, f16, E, H, I),
+          _arg(dev, "drw", drw, f32, pairs), H, I, E, Tp, pairs, M)
 
 
 def down_backward(dout, down_w, routed_expert_weights, gate, up, group_sizes, group_offsets,
@@ -873,44 +851,31 @@ def down_backward(dout, down_w, routed_expert_weights, gate, up, group_sizes, gr
     """The first stage of ``backward``: dgate, dup, whidden and drw."""
     torch = _torch()
     f16, f32 = torch.float16, torch.float32
+    dev = _gpu(dout, "dout")
     E, H, I = down_w.shape
     Tp, M, pairs = dout.shape[0], group_idx_for_bx.numel(), routed_expert_weights.numel()
-    for name, t, shape in (("dout", dout, (Tp, H)), ("gate", gate, (Tp, I)), ("up", up, (Tp, I)),
-                           ("dgate", dgate, (Tp, I)), ("dup", dup, (Tp, I)), ("whidden", whidden, (Tp, I))):
-        _shape(t, shape, name)
-    if drw.numel() != pairs:
-        raise ValueError("drw must have one entry per routed weight")
-    with _same_device(dout, down_w=down_w, gate=gate, up=up, routed_expert_weights=routed_expert_weights,
-                      group_sizes=group_sizes, group_offsets=group_offsets,
-                      group_padded_offsets=group_padded_offsets, group_idx_for_bx=group_idx_for_bx,
-                      dgate=dgate, dup=dup, whidden=whidden, scratch=scratch, drw=drw):
-        st = lib().rmoe_down_backward_f16(
-            _dev(dout, f16, "dout"), _dev(down_w, f16, "down_w"),
-            _dev(routed_expert_weights, f32, "routed_expert_weights"), _dev(gate, f16, "gate"),
-            _dev(up, f16, "up"),
-            *_tables(E, M, group_sizes, group_padded_offsets, group_idx_for_bx, group_offsets),
-            _dev(dgate, f16, "dgate"), _dev(dup, f16, "dup"), _dev(whidden, f16, "whidden"),
-            _scratch(scratch, pairs, I), _dev(drw, f32, "drw"), H, I, E, Tp, pairs, M, _stream(dout, stream))
-    _check(st, "rmoe_down_backward_f16")
+    _call("rmoe_down_backward_f16", dev, stream,
+          _arg(dev, "dout", dout, f16, Tp, H), _arg(dev, "down_w", down_w, f16),
+          _arg(dev, "routed_expert_weights", routed_expert_weights, f32), _arg(dev, "gate", gate, f16, Tp, I),
+          _arg(dev, "up", up, f16, Tp, I),
+          *_tables(dev, E, M, group_sizes, group_padded_offsets, group_idx_for_bx, group_offsets),
+          _arg(dev, "dgate", dgate, f16, Tp, I), _arg(dev, "dup", dup, f16, Tp, I),
+          _arg(dev, "whidden", whidden, f16, Tp, I), _scratch(dev, scratch, pairs, I),
+          _arg(dev, "drw", drw, f32, pairs), H, I, E, Tp, pairs, M)
 
 
 def gate_up_backward(dgate, dup, gate_w, up_w, group_sizes, group_padded_offsets, group_idx_for_bx, dx,
                      stream=None):
     """The second stage of ``backward``: dx = fp16(dgate Wg + dup Wu) on valid rows."""
-    torch = _torch()
-    f16 = torch.float16
+    f16 = _torch().float16
+    dev = _gpu(dgate, "dgate")
     E, I, H = gate_w.shape
     Tp, M = dgate.shape[0], group_idx_for_bx.numel()
-    for name, t, shape in (("dgate", dgate, (Tp, I)), ("dup", dup, (Tp, I)), ("up_w", up_w, (E, I, H)),
-                           ("dx", dx, (Tp, H))):
-        _shape(t, shape, name)
-    with _same_device(dgate, dup=dup, gate_w=gate_w, up_w=up_w, group_sizes=group_sizes,
-                      group_padded_offsets=group_padded_offsets, group_idx_for_bx=group_idx_for_bx, dx=dx):
-        st = lib().rmoe_gate_up_backward_f16(
-            _dev(dgate, f16, "dgate"), _dev(dup, f16, "dup"), _dev(gate_w, f16, "gate_w"),
-            _dev(up_w, f16, "up_w"), *_tables(E, M, group_sizes, group_padded_offsets, group_idx_for_bx),
-            _dev(dx, f16, "dx"), H, I, E, Tp, 0, M, _stream(dgate, stream))
-    _check(st, "rmoe_gate_up_backward_f16")
+    _call("rmoe_gate_up_backward_f16", dev, stream,
+          _arg(dev, "dgate", dgate, f16, Tp, I), _arg(dev, "dup", dup, f16, Tp, I),
+          _arg(dev, "gate_w", gate_w, f16), _arg(dev, "up_w", up_w, f16, E, I, H),
+          *_tables(dev, E, M, group_sizes, group_padded_offsets, group_idx_for_bx),
+          _arg(dev, "dx", dx, f16, Tp, H), H, I, E, Tp, 0, M)
 
 
 def weight_grad(x, dout, dgate, dup, whidden, group_sizes, group_padded_offsets, dgate_w, dup_w, ddown_w,
@@ -919,22 +884,16 @@ def weight_grad(x, dout, dgate, dup, whidden, group_sizes, group_padded_offsets,
     zeros for experts without rows."""
     torch = _torch()
     f16, i32 = torch.float16, torch.int32
+    dev = _gpu(x, "x")
     E, I, H = dgate_w.shape
     Tp = x.shape[0]
-    for name, t, shape in (("x", x, (Tp, H)), ("dout", dout, (Tp, H)), ("dgate", dgate, (Tp, I)),
-                           ("dup", dup, (Tp, I)), ("whidden", whidden, (Tp, I)), ("dup_w", dup_w, (E, I, H)),
-                           ("ddown_w", ddown_w, (E, H, I)), ("group_sizes", group_sizes, (E,)),
-                           ("group_padded_offsets", group_padded_offsets, (E + 1,))):
-        _shape(t, shape, name)
-    with _same_device(x, dout=dout, dgate=dgate, dup=dup, whidden=whidden, group_sizes=group_sizes,
-                      group_padded_offsets=group_padded_offsets, dgate_w=dgate_w, dup_w=dup_w,
-                      ddown_w=ddown_w):
-        st = lib().rmoe_weight_grad_f16(
-            _dev(x, f16, "x"), _dev(dout, f16, "dout"), _dev(dgate, f16, "dgate"), _dev(dup, f16, "dup"),
-            _dev(whidden, f16, "whidden"), _dev(group_sizes, i32, "group_sizes"),
-            _dev(group_padded_offsets, i32, "group_padded_offsets"), _dev(dgate_w, f16, "dgate_w"),
-            _dev(dup_w, f16, "dup_w"), _dev(ddown_w, f16, "ddown_w"), H, I, E, Tp, _stream(x, stream))
-    _check(st, "rmoe_weight_grad_f16")
+    _call("rmoe_weight_grad_f16", dev, stream,
+          _arg(dev, "x", x, f16, Tp, H), _arg(dev, "dout", dout, f16, Tp, H), _arg(dev, "dgate", dgate, f16, Tp, I),
+          _arg(dev, "dup", dup, f16, Tp, I), _arg(dev, "whidden", whidden, f16, Tp, I),
+          _arg(dev, "group_sizes", group_sizes, i32, E),
+          _arg(dev, "group_padded_offsets", group_padded_offsets, i32, E + 1),
+          _arg(dev, "dgate_w", dgate_w, f16), _arg(dev, "dup_w", dup_w, f16, E, I, H),
+          _arg(dev, "ddown_w", ddown_w, f16, E, H, I), H, I, E, Tp)
 
 
 _WORKSPACE = {}

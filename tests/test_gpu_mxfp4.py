@@ -358,6 +358,34 @@ def test_graph_replays_on_another_stream(variant):
         assert torch.equal(qc, wq[0]) and torch.equal(qs, wq[1]), i
 
 
+def test_binding_refusals():
+    """Types, shapes, strides, devices and sizes are refused by name before
+    anything is launched."""
+    d = _case([33, 140], 256, 384, seed=3)
+    ws = torch.empty(R.mxfp4_workspace_bytes(d["Tp"], d["I"]), dtype=torch.uint8, device="cuda")
+    good = [d["codes"], d["scales"], *d["wg"], *d["wu"], *d["wd"], d["rw"], d["gs"], d["go"], d["gpo"], d["gidx"], ws,
+            d["out"]]
+    for i, t in enumerate(good):
+        bad = [t.cpu(), t.double() if t.dtype is not torch.float64 else t.float()]
+        bad += [t.transpose(0, 1)] if t.dim() > 1 else []
+        if i == 13:
+            bad.append(t[:-1])
+        elif i not in (8, 12, 14):                     # counts that define the call's sizes
+            bad.append(torch.cat([t, t]))
+        for b in bad:
+            with pytest.raises((TypeError, ValueError, R.RmoeError)):
+                R.forward_mxfp4(*good[:i], b, *good[i + 1:])
+    x = torch.zeros(4, 256, device="cuda")
+    for kw in (dict(x=x.double()), dict(x=x[:, ::2]), dict(x=x[0]), dict(x=x, codes=torch.zeros(4, 64, device="cuda")),
+               dict(x=x, scales=torch.zeros(1, 4, 4, dtype=torch.uint8, device="cuda"))):
+        with pytest.raises((TypeError, ValueError)):
+            R.quantize_mxfp4(**kw)
+    with pytest.raises(R.RmoeError):
+        R.quantize_mxfp4(torch.zeros(4, 12, device="cuda"))
+    torch.cuda.synchronize()
+    assert (d["out"].view(torch.int16) == 0x7E5A).all()
+
+
 def test_two_streams_at_once():
     """Two forwards on different streams share nothing but the weights."""
     d = _case([60, 200, 9], 512, 384, seed=6)

@@ -274,6 +274,29 @@ def test_corrupted_tables_read_nothing_out_of_bounds():
     assert (d["dgw"][0] == 0).all()
 
 
+def test_binding_refusals():
+    """Types, shapes, strides, devices and sizes are refused by name before
+    anything is launched."""
+    d = _case([33, 140], 256, 384, seed=3)
+    good = [d[n] for n in ("x", "dout", "wg", "wu", "wd", "rw", "gate", "up", "gs", "go", "gpo", "gidx", "dgate", "dup",
+                           "whidden", "scratch", "dx", "dgw", "duw", "ddw", "drw")]
+    for i, t in enumerate(good):
+        bad = [t.cpu(), t.double() if t.dtype is not torch.int32 else t.long()] + ([t.t()] if t.dim() == 2 else [])
+        if i != 15:                                    # scratch: any shape and type that is long enough
+            bad.append(torch.cat([t, t]))
+        else:
+            bad = [t.cpu(), t[:-1]]
+        for b in bad:
+            if i == 5 and b.shape != t.shape:
+                continue                               # the routed weights' count is the pair count itself
+            with pytest.raises((TypeError, ValueError, R.RmoeError)):
+                R.backward(*good[:i], b, *good[i + 1:])
+    with pytest.raises(TypeError):
+        R.backward(None, *good[1:])
+    torch.cuda.synchronize()
+    assert (d["dx"].view(torch.int16) == BITS).all() and (d["dgw"].view(torch.int16) == BITS).all()
+
+
 def test_graph_replays_and_two_streams():
     d = _case([60, 0, 200, 9], 384, 256, seed=8)
     names = ("dgate", "dup", "whidden", "dx", "dgw", "duw", "ddw", "drw", "gate", "up", "hidden")

@@ -92,14 +92,16 @@ def test_nothing_to_do():
     assert L.rmoe_gate_up_backward_f16(*[A16] * 8, 256, 384, 2, 512, 0, 0, None) == OK
 
 
-def test_binding_refuses_shapes():
+def test_binding_refuses_cpu_tensors():
     z = lambda *s: torch.zeros(s, dtype=torch.float16)  # noqa: E731
     i = lambda n: torch.zeros(n, dtype=torch.int32)  # noqa: E731
     with pytest.raises(ValueError):
-        R.gate_up_train(z(256, 128), z(2, 128, 128), z(2, 128, 256), i(2), i(3), i(2), z(256, 128), z(256, 128),
+        R.gate_up_train(z(256, 128), z(2, 128, 128), z(2, 128, 128), i(2), i(3), i(2), z(256, 128), z(256, 128),
                         z(256, 128))
     with pytest.raises(ValueError):
-        R.gate_up_backward(z(256, 128), z(256, 256), z(2, 128, 128), z(2, 128, 128), i(2), i(3), i(2), z(256, 128))
+        R.gate_up_backward(z(256, 128), z(256, 128), z(2, 128, 128), z(2, 128, 128), i(2), i(3), i(2), z(256, 128))
     with pytest.raises(ValueError):
-        R.weight_grad(z(256, 128), z(256, 128), z(256, 128), z(256, 128), z(256, 128), i(2), i(2), z(2, 128, 128),
+        R.weight_grad(z(256, 128), z(256, 128), z(256, 128), z(256, 128), z(256, 128), i(2), i(3), z(2, 128, 128),
                       z(2, 128, 128), z(2, 128, 128))
+    with pytest.raises(TypeError):
+        R.gate_up_train(None, z(2, 128, 128), z(2, 128, 128), i(2), i(3), i(2), z(256, 128), z(256, 128), z(256, 128))
