@@ -11,6 +11,11 @@
 // sub-steps that follow that barrier, between the MFMAs, so that the memory
 // instructions leave the in-order wave while the matrix core is busy.
 //
+// A persistent workgroup overlaps its items: kfill issues the first step's
+// DMAs of the next item before the epilogue of the current one, whose vector
+// work then covers their round trip (a first step took 5-8 k cycles of a 46 k
+// cycle item when it was fetched at the item's start).
+//
 // P, the operands, provides
 //   Frag                     one 16-byte MFMA operand
 //   AR, BR                   LDS reads per A / B operand tile of a sub-step
@@ -18,6 +23,9 @@
 //                            of them fill the step after the next (0 or the
 //                            A slot's); sub-steps over which a group is spread
 //   PRE                      steps that the ring holds: 2, or 3 for A
+//   FILL                     parts of group g(-1) that kfill issues too (0, 1)
+//   nk                       K steps
+//   begin()                  before an item's K loop: its lane indexes, fresh
 //   dma(d, j)                DMA d of group g(j): steps are clamped to the
 //                            last one (the repeats land in slots that no
 //                            later step reads)
@@ -36,15 +44,41 @@ namespace rmoe {
 
 constexpr int kSub = 4;  // sub-steps per K step
 
+template <class P>
+constexpr int kPart = (P::DMAS + P::PARTS - 1) / P::PARTS;  // DMAs of a group's part
+
+// The DMAs of the first step.  The workgroup must be past the last barrier of
+// the K loop before (the slots are then free; the epilogue may still use this
+// wave's pieces of the slots that are not filled here: with PRE 2 all but
+// slot 0 of both operands, with PRE 3 all but A's 0 and 1 and B's 0).
+template <class P>
+__device__ __forceinline__ void kfill(P &p) {
+    if constexpr (P::PRE == 3) {
+#pragma unroll
+        for (int d = P::DMAS - P::LATE; d < P::DMAS; ++d) p.dma(d, -3);
+    }
+#pragma unroll
+    for (int d = 0; d < P::DMAS; ++d) p.dma(d, -2);
+    if constexpr (P::FILL > 0) {
+#pragma unroll
+        for (int d = 0; d < kPart<P>; ++d) p.dma(d, -1);
+    }
+}
+
+// newer: memory instructions that this wave has certainly issued since kfill
+// (0 or kNewer): the wait for the first step leaves that many in flight.
+constexpr int kNewer = 24;
+
 template <int NTT, class P>
-__device__ __forceinline__ void kloop(P &p, int nk, f16x (&acc)[4][4]) {
+__device__ __forceinline__ void kloop(P &p, bool newer, f16x (&acc)[4][4]) {
     constexpr int NMF = 4 * NTT;                            // MFMAs per sub-step
     constexpr int NRD = NTT > 0 ? 4 * P::AR + NTT * P::BR : 0;  // operand reads per sub-step
-    constexpr int DPS = (P::DMAS + P::PARTS - 1) / P::PARTS;
+    constexpr int DPS = kPart<P>;
+    const int nk = p.nk;
     typename P::Frag a[2][4], b[2][4];
     // MFMAs of sub-step S (buffer S & 1), interleaved with the reads of
     // sub-step sr of step kr and part `part` of group g(gj)
-    auto substep = [&](auto sc, bool rd, int kr, int sr, int gj, int part) {
+    auto substep = [&](auto sc, bool rd, int kr, int sr, int gj, int part) __attribute__((always_inline)) {
         constexpr int S = decltype(sc)::value;
         const int nrd = rd ? NRD : 0;
         const int d0 = DPS * part;
@@ -73,17 +107,15 @@ __device__ __forceinline__ void kloop(P &p, int nk, f16x (&acc)[4][4]) {
     constexpr std::integral_constant<int, 1> s1{};
     constexpr std::integral_constant<int, 2> s2{};
     constexpr std::integral_constant<int, 3> s3{};
-    // prologue: step 0 whole (with a ring of 3 also A of step 1), the first
-    // part of the group that follows
-    if constexpr (P::PRE == 3) {
+    if constexpr (P::FILL == 0) {
 #pragma unroll
-        for (int d = P::DMAS - P::LATE; d < P::DMAS; ++d) p.dma(d, -3);
+        for (int d = 0; d < DPS; ++d) p.dma(d, -1);
     }
-#pragma unroll
-    for (int d = 0; d < P::DMAS; ++d) p.dma(d, -2);
-#pragma unroll
-    for (int d = 0; d < DPS; ++d) p.dma(d, -1);
-    wait_vm<P::LATE + DPS>();
+    static_assert(P::LATE + DPS + kNewer < 64, "vmcnt range");
+    if (newer)
+        wait_vm<P::LATE + DPS + kNewer>();
+    else
+        wait_vm<P::LATE + DPS>();
     bar();
     p.publish(0);
     if constexpr (NTT > 0) {
@@ -112,18 +144,6 @@ __device__ __forceinline__ void kloop(P &p, int nk, f16x (&acc)[4][4]) {
     wait_vm<0>();
 }
 
-// kloop for the wave's live token tiles (a uniform count)
-template <class P>
-__device__ __forceinline__ void kloop_tiles(P &p, int nk, int ntt, f16x (&acc)[4][4]) {
-    switch (ntt) {
-        case 4: kloop<4>(p, nk, acc); break;
-        case 3: kloop<3>(p, nk, acc); break;
-        case 2: kloop<2>(p, nk, acc); break;
-        case 1: kloop<1>(p, nk, acc); break;
-        default: kloop<0>(p, nk, acc); break;
-    }
-}
-
 __device__ __forceinline__ void zero_acc(f16x (&acc)[4][4]) {
 #pragma unroll
     for (int t = 0; t < 4; ++t)
@@ -131,6 +151,29 @@ __device__ __forceinline__ void zero_acc(f16x (&acc)[4][4]) {
         for (int u = 0; u < 4; ++u)
 #pragma unroll
             for (int i = 0; i < 16; ++i) acc[t][u][i] = 0.f;
+}
+
+// The K loop for the wave's live token tiles (a uniform count), then
+// done(accumulators, count as a constant): one copy of the epilogue per
+// count, so that the accumulators stay in the registers of their loop (one
+// copy after all loops cost 336 register moves per item).
+template <class P, class F>
+__device__ __forceinline__ void ktiles(P &p, int ntt, bool newer, F &&done) {
+    auto run = [&](auto n) __attribute__((always_inline)) {
+        constexpr int NTT = decltype(n)::value;
+        p.begin();
+        f16x acc[4][4];
+        zero_acc(acc);
+        kloop<NTT>(p, newer, acc);
+        done(acc, n);
+    };
+    switch (ntt) {
+        case 4: run(std::integral_constant<int, 4>{}); break;
+        case 3: run(std::integral_constant<int, 3>{}); break;
+        case 2: run(std::integral_constant<int, 2>{}); break;
+        case 1: run(std::integral_constant<int, 1>{}); break;
+        default: run(std::integral_constant<int, 0>{}); break;
+    }
 }
 
 }  // namespace rmoe

@@ -23,28 +23,47 @@ constexpr int kMxChunkBytes = 128;
 // Byte of block j (0..7) of a chunk within its 8 scale bytes.
 __device__ __forceinline__ int mx_pos(int j) { return ((j & 1) << 2) | (j >> 1); }
 
-// Scale byte of a block whose largest magnitude has these fp32 bits:
-// floor(log2(amax)) - 2 + 127, so that the largest element lands in [4, 8);
-// at least 0 (amax < 2^-125, zero included).  Infinities and NaN (their bits
-// order above every number) give 255, the format's NaN.
-__device__ __forceinline__ unsigned mx_scale_byte(unsigned amax_bits) {
-    const int ex = (int)(amax_bits >> 23);
+// Running maximum of magnitudes that keeps a NaN (v_maximum3_f32, two values
+// per instruction).
+__device__ __forceinline__ float mx_amax(float m, float a, float b) {
+    return __builtin_elementwise_maximum(__builtin_elementwise_maximum(__builtin_fabsf(a), __builtin_fabsf(b)), m);
+}
+
+// Scale byte of a block by its largest magnitude: floor(log2(amax)) - 2 +
+// 127, so that the largest element lands in [4, 8); at least 0 (amax <
+// 2^-125, zero included).  Infinities and NaN give 255, the format's NaN.
+__device__ __forceinline__ unsigned mx_scale_byte(float amax) {
+    const int ex = (int)((__builtin_bit_cast(unsigned, amax) >> 23) & 255u);
     return ex == 255 ? 255u : ex > 2 ? (unsigned)(ex - 2) : 0u;
 }
 
-// E2M1 codes of 4 values over 2^(byte - 127), rounded to nearest even and
-// clamped at 6 by the conversion instruction, in the low 16 bits.  Small
-// scales are moved up by 2^64 together with the values (exact), away from
-// the subnormal scales; `up` is mx_up(byte), `scale` mx_scale(byte).
-__device__ __forceinline__ float mx_up(unsigned byte) { return byte < 64 ? 0x1p64f : 1.0f; }
-__device__ __forceinline__ float mx_scale(unsigned byte) {
-    return __builtin_bit_cast(float, (byte < 64 ? byte + 64 : byte) << 23);
-}
-__device__ __forceinline__ unsigned mx_codes4(float a, float b, float c, float d, float up, float scale) {
+// E2M1 codes of N values over 2^(byte - 127), rounded to nearest even and
+// clamped at 6 by the conversion instruction, 8 per dword.  Small scales are
+// moved up by 2^64 together with the values (exact), away from the subnormal
+// scales: a branch that no wave with a block above 2^-61 takes.
+__device__ __forceinline__ unsigned mx_pack8(const float *v, float scale) {
     unsigned r = 0;
-    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, a * up, b * up, scale, 0);
-    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, c * up, d * up, scale, 1);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, v[0], v[1], scale, 0);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, v[2], v[3], scale, 1);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, v[4], v[5], scale, 2);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, v[6], v[7], scale, 3);
     return r;
+}
+template <int N>
+__device__ __forceinline__ void mx_codes(float (&v)[N], unsigned byte, unsigned (&out)[N / 8]) {
+    unsigned sb = byte;
+    if (__builtin_expect(__any(byte < 64), 0)) {
+        const float up = byte < 64 ? 0x1p64f : 1.0f;
+        sb = byte < 64 ? byte + 64 : byte;
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] *= up;
+    }
+    const float scale = __builtin_bit_cast(float, sb << 23);
+#pragma unroll
+    for (int i = 0; i < N / 8; ++i) {
+        out[i] = mx_pack8(v + 8 * i, scale);
+        if (byte == 255u) out[i] = 0;
+    }
 }
 
 }  // namespace rmoe

@@ -4,9 +4,8 @@
 //
 // A half-wave takes one chunk of 256 elements of one row: 8 elements per
 // lane (16-byte loads for fp16 and bf16, two for fp32), 4 lanes per block.
-// The block's largest magnitude is an integer maximum over the fp32 bits, so
-// NaN and infinities survive it, combined over the 4 lanes by DPP; the
-// conversion instruction rounds two values per issue.  A lane stores 4 bytes
+// The block's largest magnitude (a maximum that keeps NaN) is combined over
+// the 4 lanes by DPP; the conversion instruction rounds two values per issue.  A lane stores 4 bytes
 // of codes, a half-wave one 128-byte line.
 #include "rmoe_internal.h"
 #include "rmoe_mx.h"
@@ -89,8 +88,8 @@ struct Row8<float> {
 
 // x from lane ^ 1 and lane ^ 2 (quad permutes)
 template <int CTRL>
-__device__ __forceinline__ unsigned quad(unsigned x) {
-    return (unsigned)__builtin_amdgcn_mov_dpp((int)x, CTRL, 0xf, 0xf, true);
+__device__ __forceinline__ float quad(float x) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, x), CTRL, 0xf, 0xf, true));
 }
 
 struct Chunk {
@@ -99,17 +98,17 @@ struct Chunk {
 };
 
 // One chunk per half-wave: 8 values per lane (zeros past the row's end).
-__device__ __forceinline__ Chunk quantize_chunk(const float *f) {
-    unsigned m = 0;
+__device__ __forceinline__ Chunk quantize_chunk(float (&f)[8]) {
+    float m = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, __builtin_bit_cast(unsigned, f[i]) & 0x7fffffffu);
-    m = max(m, quad<0xB1>(m));
-    m = max(m, quad<0x4E>(m));
+    for (int i = 0; i < 8; i += 2) m = mx_amax(m, f[i], f[i + 1]);
+    m = mx_amax(0.f, m, quad<0xB1>(m));
+    m = mx_amax(0.f, m, quad<0x4E>(m));
     const unsigned byte = mx_scale_byte(m);
-    const float up = mx_up(byte), sc = mx_scale(byte);
     Chunk c;
-    c.codes = mx_codes4(f[0], f[1], f[2], f[3], up, sc) | (mx_codes4(f[4], f[5], f[6], f[7], up, sc) << 16);
-    if (byte == 255u) c.codes = 0;
+    unsigned codes[1];
+    mx_codes<8>(f, byte, codes);
+    c.codes = codes[0];
     // block g sits in lanes 4g .. 4g+3; its byte is byte g / 2 of dword g % 2
     const int g = (threadIdx.x & 31) >> 2;
     unsigned s = byte << (8 * (g >> 1));

@@ -181,20 +181,16 @@ __device__ __forceinline__ void stream_pass(const MxArgs &a, const BlockInfo &bi
 #pragma unroll
         for (int t = 0; t < TT; ++t) {
             if (t % KS != wave) continue;
-            float v[16];
-            unsigned m = 0;
+            float v[16], m = 0.f;
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                v[r] = silu(sum(0, t, r)) * sum(1, t, r);
-                m = max(m, __builtin_bit_cast(unsigned, v[r]) & 0x7fffffffu);
-            }
-            m = max(m, (unsigned)__shfl_xor((int)m, 32));
+            for (int r = 0; r < 16; ++r) v[r] = silu(sum(0, t, r)) * sum(1, t, r);
+#pragma unroll
+            for (int r = 0; r < 16; r += 2) m = mx_amax(m, v[r], v[r + 1]);
+            m = mx_amax(0.f, m, __shfl_xor(m, 32));
             const unsigned byte = mx_scale_byte(m);
-            const float up = mx_up(byte), sc = mx_scale(byte);
-            unsigned c01 = mx_codes4(v[0], v[1], v[2], v[3], up, sc) | (mx_codes4(v[4], v[5], v[6], v[7], up, sc) << 16);
-            unsigned c23 = mx_codes4(v[8], v[9], v[10], v[11], up, sc) |
-                           (mx_codes4(v[12], v[13], v[14], v[15], up, sc) << 16);
-            if (byte == 255u) c01 = c23 = 0;
+            unsigned cd[2];  // quads 0, 1 and 2, 3: 16 bits each
+            mx_codes<16>(v, byte, cd);
+            const unsigned c01 = cd[0], c23 = cd[1];
             const unsigned h01 = (unsigned)__shfl_xor((int)c01, 32), h23 = (unsigned)__shfl_xor((int)c23, 32);
             const int tok = p0 + 32 * t + lr;
             if (lh == 0 && tok < bi.rows) {

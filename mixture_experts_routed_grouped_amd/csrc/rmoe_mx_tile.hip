@@ -33,10 +33,13 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef unsigned u4 __attribute__((ext_vector_type(4)));
 
+// NEXT: the epilogue uses no LDS, so the second step's first DMAs may be
+// issued ahead of it too.
+template <bool NEXT>
 struct MxOps {
     typedef i32x4 Frag;
     static constexpr int AR = 1, BR = 1;
-    static constexpr int DMAS = 17, LATE = 0, PARTS = 2, PRE = 2;
+    static constexpr int DMAS = 17, LATE = 0, PARTS = 2, PRE = 2, FILL = NEXT;
 
     unsigned char *smem;
     unsigned dwave;        // LDS address of this wave's 64 rows of a slot
@@ -44,20 +47,30 @@ struct MxOps {
     int64_t sstep;         // bytes between a step's scales and the next step's
     unsigned sdst;         // LDS address of this wave's scale half
     unsigned soff;         // 16 * lane
-    unsigned tkoff[8], woff[8];
+    int64_t row8;          // bytes of 8 rows
+    const unsigned char *tcur, *wcur;  // first row of the instruction issued last (a group's go out in order)
+    unsigned off[2];       // lane offset of instruction j from its rows 8 j: j even, odd
     int nk;
-    int lr, lh, arow, trow0;  // arow: first A row of this wave's tile 0; tile t at arow + 32 (t & 1) + astep (t / 2)
+    int lane, lr, lh, arow, trow0;  // arow: first A row of this wave's tile 0; tile t at arow + 32 (t & 1) + astep (t / 2)
     int astep;
     unsigned sa[4], sb[4], sna[4], snb[4];
 
+    __device__ __forceinline__ void begin() {
+        const int l = fresh(lane);
+        lr = l & 31;
+        lh = l >> 5;
+    }
     __device__ __forceinline__ void dma(int d, int j) {
         const int kt = min(j + NS, nk - 1), slot = (j + NS) % NS;
-        if (d == 0)
+        if (d == 0) {
             dma16_sb(sbase + (int64_t)kt * sstep, soff, sdst + slot * SSLOT);
-        else if (d <= 8)
-            dma16_sb(tbase + (int64_t)kt * kMxChunkBytes, tkoff[d - 1], dwave + T_OFF + slot * SLOT + 1024 * (d - 1));
-        else
-            dma16_sb(wbase + (int64_t)kt * kMxChunkBytes, woff[d - 9], dwave + W_OFF + slot * SLOT + 1024 * (d - 9));
+        } else if (d <= 8) {
+            tcur = d == 1 ? tbase + (int64_t)kt * kMxChunkBytes : tcur + row8;
+            dma16_sb(tcur, off[(d - 1) & 1], dwave + T_OFF + slot * SLOT + 1024 * (d - 1));
+        } else {
+            wcur = d == 9 ? wbase + (int64_t)kt * kMxChunkBytes : wcur + row8;
+            dma16_sb(wcur, off[(d - 9) & 1], dwave + W_OFF + slot * SLOT + 1024 * (d - 9));
+        }
     }
     __device__ __forceinline__ int row_a(int t) const { return arow + 32 * (t & 1) + astep * (t >> 1); }
     __device__ __forceinline__ void read(int k, int s, int i, Frag *a, Frag *b) {
@@ -91,102 +104,99 @@ struct MxOps {
     __device__ __forceinline__ void publish(int) {}
 };
 
-// One work item: blocks bx (rows0 valid rows) and bx+1 (rows1; has1: of the
-// same expert) against weight slice nt.
+// A work item as the kernel runs it: blocks bx (rows0 valid rows) and bx + 1
+// (rows1, 0: absent or of another expert) against weight slice nt.
+struct Item {
+    int nt, e, bx, off, rows0, rows1;
+};
+
+// What a lane and a wave hold for the whole launch, and the item's bases.
 template <bool DUAL>
-__device__ __forceinline__ void run_item(const MxArgs &a, unsigned char *smem, const TileItem &it) {
-    const int rows0 = a.gidx[it.bx] == it.e ? it.rows0 : 0;
-    const int rows1 = (it.rows1 > 0 && a.gidx[it.bx + 1] == it.e) ? it.rows1 : 0;
-    if (rows0 == 0 && rows1 == 0) return;
-    const bool has1 = rows1 > 0;
-    const int64_t N = a.N, rb = (int64_t)a.kc * kMxChunkBytes;
-    int tid = threadIdx.x;
-    asm volatile("" : "+v"(tid));  // opaque per item: addresses are not hoisted out of the item loop
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int lane = tid & 63, lr = lane & 31, lh = lane >> 5;
-    const int ww = wave & 1, wt = wave >> 1;  // weight half, token half (= block bx + wt)
-    const int64_t n0 = (int64_t)it.nt * (DUAL ? 128 : 256);
+struct Tile {
+    const MxArgs &a;
+    unsigned char *smem;
+    int wave, lane, ww, wt;  // ww: weight half, wt: token half (= block bx + wt)
+    int64_t N, rb;
+    MxOps<DUAL> p;
 
-    MxOps p;
-    p.smem = smem;
-    p.nk = a.kc;
-    p.lr = lr;
-    p.lh = lh;
-    p.trow0 = 128 * wt;
-    p.arow = DUAL ? 64 * ww : 128 * ww;  // gate/up: tiles 0, 1 gate rows, 2, 3 the same up rows
-    p.astep = DUAL ? 128 : 64;
-    // weight rows 64 w .. of the slot: gate rows for waves 0, 1, up rows for 2, 3
-    const unsigned char *wmat = DUAL && wave >= 2 ? a.w1 : a.w0;
-    int64_t wrow0 = n0 + (DUAL ? (64 * wave) & 127 : 64 * wave);
-    wrow0 = wrow0 < N ? wrow0 : N - 64;  // a narrow last slice: idle rows read valid rows
-    p.wbase = wmat + ((int64_t)it.e * N + wrow0) * rb;
-    p.tbase = a.x + (int64_t)it.bx * kBlockM * rb;
+    __device__ __forceinline__ Tile(const MxArgs &args, unsigned char *s) : a(args), smem(s) {
+        wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        lane = threadIdx.x & 63;
+        ww = wave & 1;
+        wt = wave >> 1;
+        N = a.N;
+        rb = (int64_t)a.kc * kMxChunkBytes;
+        p.smem = smem;
+        p.nk = a.kc;
+        p.lane = lane;
+        p.trow0 = 128 * wt;
+        p.arow = DUAL ? 64 * ww : 128 * ww;  // gate/up: tiles 0, 1 gate rows, 2, 3 the same up rows
+        p.astep = DUAL ? 128 : 64;
+        // instruction j moves rows 64 w + 8 j + lane / 8 of a slot, physical
+        // chunk lane % 8; the rows' swizzle repeats with j's parity
+        p.row8 = 8 * rb;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const int r = 64 * wave + 8 * j + (lane >> 3);
-        const int c = (lane & 7) ^ lds_swz(r);
-        p.woff[j] = (unsigned)((8 * j + (lane >> 3)) * rb + 16 * c);
-        int tr = r;
-        if (r >= kBlockM && !has1) tr -= kBlockM;  // absent second block: stay in bounds
-        p.tkoff[j] = (unsigned)(tr * rb + 16 * c);
+        for (int j = 0; j < 2; ++j)
+            p.off[j] = (unsigned)((lane >> 3) * rb + 16 * ((lane & 7) ^ lds_swz(8 * j + (lane >> 3))));
+        const unsigned lds0 = (unsigned)(uintptr_t)smem;
+        p.dwave = lds0 + 64 * wave * kMxChunkBytes;
+        p.sdst = lds0 + (wave < 2 ? WS_OFF : TS_OFF) + 1024 * (wave & 1);
+        p.sstep = 8 * (wave < 2 ? N : a.Tp);
+        p.soff = 16 * lane;
     }
-    const unsigned lds0 = (unsigned)(uintptr_t)smem;
-    p.dwave = lds0 + 64 * wave * kMxChunkBytes;
-    // scales: waves 0, 1 move the weight rows' (128 rows each), waves 2, 3
-    // the two blocks' token rows'
-    if (wave < 2) {
-        int64_t r0 = DUAL ? n0 : n0 + 128 * wave;
-        r0 = r0 < N ? r0 : N - 128;
-        p.sbase = (DUAL && wave == 1 ? a.w1s : a.w0s) + ((int64_t)it.e * a.kc * N + r0) * 8;
-        p.sstep = N * 8;
-        p.sdst = lds0 + WS_OFF + 1024 * wave;
-    } else {
-        p.sbase = a.xs + ((int64_t)it.bx + (wave == 3 && has1 ? 1 : 0)) * kBlockM * 8;
-        p.sstep = a.Tp * 8;
-        p.sdst = lds0 + TS_OFF + 1024 * (wave - 2);
+    __device__ __forceinline__ void set(const Item &it) {
+        const int64_t n0 = (int64_t)it.nt * (DUAL ? 128 : 256);
+        // weight rows 64 w .. of the slot: gate rows for waves 0, 1, up rows for 2, 3
+        int64_t wrow0 = n0 + (DUAL ? (64 * wave) & 127 : 64 * wave);
+        wrow0 = wrow0 < N ? wrow0 : N - 64;  // a narrow last slice: idle rows read valid rows
+        p.wbase = uniform((DUAL && wave >= 2 ? a.w1 : a.w0) + ((int64_t)it.e * N + wrow0) * rb);
+        // an absent second block: its half reads the first block's rows
+        const bool two = it.rows1 > 0;
+        p.tbase = uniform(a.x + ((int64_t)it.bx * kBlockM + (two ? 64 * wave : (64 * wave) & 127)) * rb);
+        // scales: waves 0, 1 move the weight rows' (128 rows each), waves 2,
+        // 3 the two blocks' token rows'
+        if (wave < 2) {
+            int64_t r0 = DUAL ? n0 : n0 + 128 * wave;
+            r0 = r0 < N ? r0 : N - 128;
+            p.sbase = uniform((DUAL && wave == 1 ? a.w1s : a.w0s) + ((int64_t)it.e * a.kc * N + r0) * 8);
+        } else {
+            p.sbase = uniform(a.xs + ((int64_t)it.bx + (wave == 3 && two ? 1 : 0)) * kBlockM * 8);
+        }
     }
-    p.soff = 16 * lane;
+    // valid rows and live token tiles of this wave
+    __device__ __forceinline__ int rows(const Item &it) const { return wt ? it.rows1 : it.rows0; }
+    __device__ __forceinline__ int tiles(const Item &it) const {
+        return DUAL || (int64_t)it.nt * 256 + 128 * ww < N ? (rows(it) + 31) / 32 : 0;
+    }
 
-    const int myrows = wt ? rows1 : rows0;
-    const bool wlive = DUAL || n0 + 128 * ww < N;
-    const int ntt = wlive ? (myrows + 31) / 32 : 0;
-    f16x acc[4][4];
-    zero_acc(acc);
-    kloop_tiles(p, a.kc, ntt, acc);
-    if (ntt == 0) return;
-    const int64_t row0 = (int64_t)(it.bx + wt) * kBlockM;
-
-    if constexpr (DUAL) {
-        // hidden block t (32 features) of token lr of tile u: register 4q + r
-        // holds feature 8q + 4lh + r.  Lanes 0-31 assemble and store block 0,
-        // lanes 32-63 block 1.
+    // gate/up: hidden block t (32 features) of token lr of tile u: register
+    // 4q + r holds feature 8q + 4lh + r.  Lanes 0-31 assemble and store block
+    // 0, lanes 32-63 block 1.
+    template <int NTT>
+    __device__ __forceinline__ void hidden(const Item &it, f16x (&acc)[4][4]) const {
+        const int ln = fresh(lane), lr = ln & 31, lh = ln >> 5;
+        const int64_t n0 = (int64_t)it.nt * 128, row0 = (int64_t)(it.bx + wt) * kBlockM;
         const int64_t orb = (int64_t)((N + kMxChunk - 1) / kMxChunk) * kMxChunkBytes;
-        const int64_t blk = (n0 + 64 * ww) / 32;  // first of the wave's two blocks
+        const int64_t b = (n0 + 64 * ww) / 32 + lh;  // block that this lane stores
+        const int myrows = rows(it);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            if (u >= ntt) continue;
-            unsigned c01[2], c23[2], byte[2];
+        for (int u = 0; u < NTT; ++u) {
+            unsigned cd[2][2], byte[2];  // quads 0, 1 and 2, 3 of each block: 16 bits each
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-                float v[16];
-                unsigned m = 0;
+                float v[16], m = 0.f;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    v[i] = silu(acc[t][u][i]) * acc[t + 2][u][i];
-                    m = max(m, __builtin_bit_cast(unsigned, v[i]) & 0x7fffffffu);
-                }
-                m = max(m, (unsigned)__shfl_xor((int)m, 32));
+                for (int i = 0; i < 16; ++i) v[i] = silu(acc[t][u][i]) * acc[t + 2][u][i];
+#pragma unroll
+                for (int i = 0; i < 16; i += 2) m = mx_amax(m, v[i], v[i + 1]);
+                m = mx_amax(0.f, m, __shfl_xor(m, 32));
                 byte[t] = mx_scale_byte(m);
-                const float up = mx_up(byte[t]), sc = mx_scale(byte[t]);
-                c01[t] = mx_codes4(v[0], v[1], v[2], v[3], up, sc) | (mx_codes4(v[4], v[5], v[6], v[7], up, sc) << 16);
-                c23[t] = mx_codes4(v[8], v[9], v[10], v[11], up, sc) |
-                         (mx_codes4(v[12], v[13], v[14], v[15], up, sc) << 16);
-                if (byte[t] == 255u) c01[t] = c23[t] = 0;
+                mx_codes<16>(v, byte[t], cd[t]);
             }
             // send the other lane half its block, keep the own one
-            const unsigned s01 = lh ? c01[0] : c01[1], s23 = lh ? c23[0] : c23[1];
-            const unsigned r01 = (unsigned)__shfl_xor((int)s01, 32), r23 = (unsigned)__shfl_xor((int)s23, 32);
-            const unsigned m01 = lh ? c01[1] : c01[0], m23 = lh ? c23[1] : c23[0];
+            const unsigned r01 = (unsigned)__shfl_xor((int)(lh ? cd[0][0] : cd[1][0]), 32);
+            const unsigned r23 = (unsigned)__shfl_xor((int)(lh ? cd[0][1] : cd[1][1]), 32);
+            const unsigned m01 = lh ? cd[1][0] : cd[0][0], m23 = lh ? cd[1][1] : cd[0][1];
             const unsigned l01 = lh ? r01 : m01, h01 = lh ? m01 : r01, l23 = lh ? r23 : m23, h23 = lh ? m23 : r23;
             u4 o;
             o[0] = (l01 & 0xffffu) | (h01 << 16);
@@ -195,64 +205,114 @@ __device__ __forceinline__ void run_item(const MxArgs &a, unsigned char *smem, c
             o[3] = (l23 >> 16) | (h23 & 0xffff0000u);
             const int row = 32 * u + lr;
             if (row < myrows) {
-                const int64_t b = blk + lh;
+                unsigned char *ys = a.ys + ((b >> 3) * a.Tp + row0 + row) * 8;
                 *(u4 *)(a.yc + (row0 + row) * orb + 16 * b) = o;
-                a.ys[((b >> 3) * a.Tp + row0 + row) * 8 + mx_pos((int)(b & 7))] = (unsigned char)(lh ? byte[1] : byte[0]);
+                ys[mx_pos((int)(b & 7))] = (unsigned char)(lh ? byte[1] : byte[0]);
                 // the last slice zero-fills the rest of an odd last chunk
-                // (this wave: 32 of its 64 bytes and 2 of its 4 scales)
+                // (this lane: 16 of its 64 bytes and one of its 4 scales)
                 if (n0 + 128 == N && (N & 255)) {
                     *(u4 *)(a.yc + (row0 + row) * orb + 16 * (b + 4)) = u4{0, 0, 0, 0};
-                    a.ys[((b >> 3) * a.Tp + row0 + row) * 8 + mx_pos((int)((b + 4) & 7))] = 0;
+                    ys[mx_pos((int)((b + 4) & 7))] = 0;
                 }
             }
         }
-    } else {
-        // out rows, staged through LDS for whole-line stores: a wave stages
-        // into its own 8 KB pieces of the operand slots (its DMAs have all
-        // landed, and no wave reads the ring after the last barrier): 128
-        // rows of 128 features, 16-byte chunks XOR-swizzled by row, 32 rows
-        // per piece
-        auto stage_row = [&](int row) { return smem + (row / 32) * SLOT + wave * 8192 + (row % 32) * 256; };
-        float wtok[4] = {0.f, 0.f, 0.f, 0.f};
-        const float *rwe = a.rw + a.go[it.e] + it.off + kBlockM * wt;
+    }
+
+    // down: out rows, 64 at a time staged through LDS for whole-line stores.
+    // A wave stages into its own 8 KB pieces of the operands' slots 1, which
+    // only its own DMAs fill (all landed, and no wave reads the ring after
+    // the last barrier; the next item's first step goes to slots 0): 128
+    // columns per row, 16-byte chunks XOR-swizzled by row.
+    template <int NTT>
+    __device__ __forceinline__ void out(const Item &it, f16x (&acc)[4][4]) const {
+        const int ln = fresh(lane), lr = ln & 31, lh = ln >> 5;
+        const int64_t row0 = (int64_t)(it.bx + wt) * kBlockM;
+        const int myrows = rows(it);
+        unsigned char *piece[2] = {smem + W_OFF + SLOT + wave * 8192, smem + T_OFF + SLOT + wave * 8192};
+        float w[4] = {0.f, 0.f, 0.f, 0.f};
+        const float *rwe = a.rw + table(a.go)[it.e] + it.off + kBlockM * wt;
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
-            if (u < ntt && 32 * u + lr < myrows) wtok[u] = rwe[32 * u + lr];
+        for (int u = 0; u < NTT; ++u)
+            if (32 * u + lr < myrows) w[u] = rwe[32 * u + lr];
+        _Float16 *ybase = a.y + row0 * N + (int64_t)it.nt * 256 + 128 * ww;
+        const int c = ln & 15;
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            if (u >= ntt) continue;
-            const int row = 32 * u + lr;
-            unsigned char *srow = stage_row(row);
-            const float w = wtok[u];
+        for (int u0 = 0; u0 < NTT; u0 += 2) {
 #pragma unroll
-            for (int t = 0; t < 4; ++t)
+            for (int u = u0; u < u0 + 2 && u < NTT; ++u)
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const f16x &o = acc[t][u];
-                    const int c = (4 * t + q) ^ (row & 15);
-                    *(h4 *)(srow + (c << 4) + 8 * lh) =
-                        to_h4(o[4 * q + 0] * w, o[4 * q + 1] * w, o[4 * q + 2] * w, o[4 * q + 3] * w);
+                for (int t = 0; t < 4; ++t)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const f16x &o = acc[t][u];
+                        *(h4 *)(piece[u - u0] + lr * 256 + (((4 * t + q) ^ (lr & 15)) << 4) + 8 * lh) = to_h4(
+                            o[4 * q + 0] * w[u], o[4 * q + 1] * w[u], o[4 * q + 2] * w[u], o[4 * q + 3] * w[u]);
+                    }
+            __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): this wave's staging writes are done
+#pragma unroll
+            for (int u = u0; u < u0 + 2 && u < NTT; ++u) {
+                h8 v[8];  // read together: one LDS round trip, not eight
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int r = 4 * j + (ln >> 4);
+                    v[j] = *(const h8 *)(piece[u - u0] + r * 256 + ((c ^ (r & 15)) << 4));
                 }
-        }
-        __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): this wave's staging writes are done
-        _Float16 *ybase = a.y + row0 * N + n0 + 128 * ww;
-        const int c = lane & 15;
-#pragma unroll 4
-        for (int r0 = 0; r0 < 32 * ntt; r0 += 4) {
-            const int row = r0 + (lane >> 4);
-            if (row < myrows) *(h8 *)(ybase + (int64_t)row * N + 8 * c) = *(const h8 *)(stage_row(row) + ((c ^ (row & 15)) << 4));
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int row = 32 * u + 4 * j + (ln >> 4);
+                    if (row < myrows) *(h8 *)(ybase + (int64_t)row * N + 8 * c) = v[j];
+                }
+            }
         }
     }
-}
+};
 
-// Persistent, one workgroup per CU, items in the order of rmoe_sched.h.
+// Persistent, one workgroup per CU, items in the order of rmoe_sched.h.  The
+// first step of the next item travels while the current one's epilogue runs.
 template <bool DUAL>
 __global__ __launch_bounds__(256) void mx_tile_kernel(MxArgs a, int NT) {
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
-    const TileSeq seq = tile_seq(a.gs, a.E, NT, blockIdx.x % kXcd, kXcd);
+    const Table gs = table(a.gs), gpo = table(a.gpo), gidx = table(a.gidx);
+    const TileSeq seq = tile_seq(gs, a.E, NT, blockIdx.x % kXcd, kXcd);
     const int nl = gridDim.x / kXcd;
     TileCursor cur;
-    for (int i = blockIdx.x / kXcd; i < seq.n; i += nl) run_item<DUAL>(a, smem, tile_item(a.gs, a.gpo, seq, i, cur));
+    int i = blockIdx.x / kXcd;
+    // the next item that holds rows (blocks mapped to another expert hold none)
+    auto advance = [&](Item &it) __attribute__((always_inline)) {
+        for (; i < seq.n; i += nl) {
+            const TileItem t = tile_item(gs, gpo, seq, i, cur);
+            it = Item{t.nt, t.e, t.bx, t.off, gidx[t.bx] == t.e ? t.rows0 : 0, 0};
+            if (t.rows1 > 0 && gidx[t.bx + 1] == t.e) it.rows1 = t.rows1;
+            if (it.rows0 || it.rows1) {
+                i += nl;
+                return true;
+            }
+        }
+        return false;
+    };
+    Tile<DUAL> tile(a, smem);
+    Item it;
+    if (!advance(it)) return;
+    tile.set(it);
+    kfill(tile.p);
+    bool newer = false, more = true;
+    while (more) {
+        ktiles(tile.p, tile.tiles(it), newer, [&](auto &acc, auto n) __attribute__((always_inline)) {
+            constexpr int NTT = decltype(n)::value;
+            const Item now = it;
+            more = advance(it);
+            if (more) {
+                tile.set(it);
+                kfill(tile.p);
+            }
+            if constexpr (DUAL)
+                tile.template hidden<NTT>(now, acc);
+            else
+                tile.template out<NTT>(now, acc);
+            // a whole block's out rows: 32 stores since the fill
+            newer = !DUAL && NTT == 4 && tile.rows(now) == kBlockM;
+        });
+    }
 }
 
 template <bool DUAL>

@@ -58,16 +58,16 @@ __device__ __forceinline__ h4 tr_read(const unsigned char *p) {
 }
 
 // DMA source of a k-major slot: wave w fills column group w, instruction j
-// k rows 8j .. 8j+7; byte offset of this lane from (first k row, the wave's
+// k rows 8j .. 8j+7; byte offset of this lane from (k row 8j, the wave's
 // first column) in a matrix of N columns.
-__device__ __forceinline__ unsigned k_major_off(int lane, int j, int64_t N) {
+__device__ __forceinline__ unsigned k_major_off(int lane, int64_t N) {
     const int r = lane >> 3, c = (lane & 7) ^ swz_k(r);
-    return (unsigned)(((int64_t)(8 * j + r) * N + 8 * c) * 2);
+    return (unsigned)((r * N + 8 * c) * 2);
 }
 
 struct OpsBase {
     typedef h8 Frag;
-    static constexpr int DMAS = 16, LATE = 8, PARTS = 4, PRE = 3;
+    static constexpr int DMAS = 16, LATE = 8, PARTS = 4, PRE = 3, FILL = 0;
     __device__ __forceinline__ void step(int) {}
     __device__ __forceinline__ void next() {}
     template <int S>
@@ -83,22 +83,38 @@ struct RowOps : OpsBase {
     unsigned char *smem;
     unsigned dwave;
     const _Float16 *w[2], *t[2];  // uniform bases of the two pairs
-    unsigned woff[8], toff[8];
-    int64_t wstep;                // elements per K step: 64 N
+    unsigned woff, toff[2];       // lane offsets from an instruction's first row (tokens: j even, odd)
+    int64_t N, K;                 // elements per weight row, token row
+    const _Float16 *wcur, *tcur;  // first row of the instruction issued last (a group's go out in order)
     int nk, n1;
     unsigned la[2][2];            // tr_off of tile parity, half
     int nb0;                      // first column group of this wave's A half
-    int trow0, lr, lh;
+    int trow0, lane, lr, lh;
 
+    __device__ __forceinline__ void begin() {
+        const int l = fresh(lane);
+        lr = l & 31;
+        lh = l >> 5;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) la[i >> 1][i & 1] = tr_off(l, i >> 1, i & 1);
+    }
     __device__ __forceinline__ void dma(int d, int j) {
         if (d < 8) {
-            const int k = min(j + NBS, nk - 1), two = k >= n1;
-            dma16_sb((two ? t[1] : t[0]) + (int64_t)(two ? k - n1 : k) * BK, toff[d],
-                     dwave + B_OFF + ((j + NBS) % NBS) * SLOT + 1024 * d);
+            if (d == 0) {
+                const int k = min(j + NBS, nk - 1), two = k >= n1;
+                tcur = (two ? t[1] : t[0]) + (int64_t)(two ? k - n1 : k) * BK;
+            } else {
+                tcur += 8 * K;
+            }
+            dma16_sb(tcur, toff[d & 1], dwave + B_OFF + ((j + NBS) % NBS) * SLOT + 1024 * d);
         } else {
-            const int k = min(j + NAS, nk - 1), two = k >= n1;
-            dma16_sb((two ? w[1] : w[0]) + (int64_t)(two ? k - n1 : k) * wstep, woff[d - 8],
-                     dwave + ((j + NAS) % NAS) * SLOT + 1024 * (d - 8));
+            if (d == 8) {
+                const int k = min(j + NAS, nk - 1), two = k >= n1;
+                wcur = (two ? w[1] : w[0]) + (int64_t)(two ? k - n1 : k) * BK * N;
+            } else {
+                wcur += 8 * N;
+            }
+            dma16_sb(wcur, woff, dwave + ((j + NAS) % NAS) * SLOT + 1024 * (d - 8));
         }
     }
     __device__ __forceinline__ void read(int k, int s, int i, Frag *a, Frag *b) {
@@ -119,19 +135,21 @@ struct ColOps : OpsBase {
     unsigned char *smem;
     unsigned dwave;
     const _Float16 *a, *b;
-    unsigned aoff[8], boff[8];
-    int64_t astep, bstep;
+    unsigned aoff, boff;
+    int64_t NA, NB;               // elements per row
+    const _Float16 *acur, *bcur;  // first row of the instruction issued last (a group's go out in order)
     int nk, tail;                 // rows of the last step, 0: a whole one
     unsigned la[2][2];
     int na0, nb0;                 // first column groups of this wave's halves
 
     __device__ __forceinline__ void dma(int d, int j) {
-        if (d < 8)
-            dma16_sb(b + (int64_t)min(j + NBS, nk - 1) * bstep, boff[d],
-                     dwave + B_OFF + ((j + NBS) % NBS) * SLOT + 1024 * d);
-        else
-            dma16_sb(a + (int64_t)min(j + NAS, nk - 1) * astep, aoff[d - 8],
-                     dwave + ((j + NAS) % NAS) * SLOT + 1024 * (d - 8));
+        if (d < 8) {
+            bcur = d == 0 ? b + (int64_t)min(j + NBS, nk - 1) * BK * NB : bcur + 8 * NB;
+            dma16_sb(bcur, boff, dwave + B_OFF + ((j + NBS) % NBS) * SLOT + 1024 * d);
+        } else {
+            acur = d == 8 ? a + (int64_t)min(j + NAS, nk - 1) * BK * NA : acur + 8 * NA;
+            dma16_sb(acur, aoff, dwave + ((j + NAS) % NAS) * SLOT + 1024 * (d - 8));
+        }
     }
     __device__ __forceinline__ void read(int k, int s, int i, Frag *fa, Frag *fb) {
         const int tt = (i & 7) >> 1, h = i & 1;
@@ -157,45 +175,53 @@ struct ColOps : OpsBase {
     }
 };
 
-// Piece of this wave's LDS for staging: 8 KB in each slot, which only its own
-// DMAs fill (all landed after the K loop), and no wave reads the ring after
-// the last barrier.  32 rows of 256 bytes per piece.
-__device__ __forceinline__ unsigned char *stage_row(unsigned char *smem, int wave, int row) {
-    return smem + (row / 32) * SLOT + wave * 8192 + (row % 32) * 256;
+// Pieces of this wave's LDS for staging: 8 KB each in A's slot 2 and B's slot
+// 1, which only its own DMAs fill (all landed after the K loop; no wave reads
+// the ring after the last barrier, and the next item's first step goes to
+// the other slots).
+__device__ __forceinline__ unsigned char *piece(unsigned char *smem, int wave, int i) {
+    return smem + (i ? B_OFF + SLOT : 2 * SLOT) + wave * 8192;
 }
 
-// The wave's 128 x 128 block as fp16 rows of 128 columns: B index (token or
-// output row) = row, A index = column.  Staged, then stored as whole lines.
-template <bool NT>
-__device__ __forceinline__ void store_block(const f16x (&acc)[4][4], unsigned char *smem, int wave, int lane, int ntt,
-                                            int rows, _Float16 *y, int64_t N) {
-    const int lr = lane & 31, lh = lane >> 5;
+// The wave's block as fp16 rows of 128 columns: B index (token or output
+// row) = row, A index = column.  Staged 64 rows at a time (256 bytes per row,
+// 16-byte chunks XOR-swizzled), then stored as whole lines.
+template <int NTT, bool NT>
+__device__ __forceinline__ void store_block(const f16x (&acc)[4][4], unsigned char *smem, int wave, int lane, int rows,
+                                            _Float16 *y, int64_t N) {
+    const int lr = lane & 31, lh = lane >> 5, c = lane & 15;
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-        if (u >= ntt) continue;
-        const int row = 32 * u + lr;
-        unsigned char *srow = stage_row(smem, wave, row);
+    for (int u0 = 0; u0 < NTT; u0 += 2) {
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
+        for (int u = u0; u < u0 + 2 && u < NTT; ++u)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const f16x &o = acc[t][u];
-                const int c = (4 * t + q) ^ (row & 15);
-                *(h4 *)(srow + (c << 4) + 8 * lh) = to_h4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const f16x &o = acc[t][u];
+                    *(h4 *)(piece(smem, wave, u - u0) + lr * 256 + (((4 * t + q) ^ (lr & 15)) << 4) + 8 * lh) =
+                        to_h4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+                }
+        __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): this wave's staging writes are done
+#pragma unroll
+        for (int u = u0; u < u0 + 2 && u < NTT; ++u) {
+            h8 v[8];  // read together: one LDS round trip, not eight
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int r = 4 * j + (lane >> 4);
+                v[j] = *(const h8 *)(piece(smem, wave, u - u0) + r * 256 + ((c ^ (r & 15)) << 4));
             }
-    }
-    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): this wave's staging writes are done
-    const int c = lane & 15;
-#pragma unroll 4
-    for (int r0 = 0; r0 < 32 * ntt; r0 += 4) {
-        const int row = r0 + (lane >> 4);
-        if (row >= rows) continue;
-        const h8 v = *(const h8 *)(stage_row(smem, wave, row) + ((c ^ (row & 15)) << 4));
-        h8 *dst = (h8 *)(y + (int64_t)row * N + 8 * c);
-        if constexpr (NT)
-            __builtin_nontemporal_store(v, dst);
-        else
-            *dst = v;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int row = 32 * u + 4 * j + (lane >> 4);
+                if (row >= rows) continue;
+                h8 *dst = (h8 *)(y + (int64_t)row * N + 8 * c);
+                if constexpr (NT)
+                    __builtin_nontemporal_store(v[j], dst);
+                else
+                    *dst = v[j];
+            }
+        }
     }
 }
 
@@ -212,135 +238,182 @@ __device__ __forceinline__ float sum16(float x) {
     return x;
 }
 
-// One work item of a row product (rmoe_sched.h): blocks bx, bx + 1 of expert
-// e against 256 columns.  HID: the hidden stage (b = dy . Wd and everything
-// that follows from it element by element); otherwise dx.
+// A work item of a row product: blocks bx (rows0 valid rows) and bx + 1
+// (rows1, 0: absent or of another expert) of expert e against 256 columns.
+struct Item {
+    int nt, e, bx, off, rows0, rows1;
+};
+
+// HID: the hidden stage (b = dy . Wd and everything that follows from it
+// element by element); otherwise dx.  Holds what a lane and a wave keep for
+// the whole launch, and the item's bases.
 template <bool HID>
-__device__ __forceinline__ void run_rows(const TrainArgs &a, unsigned char *smem, const TileItem &it) {
-    const int rows0 = a.gidx[it.bx] == it.e ? it.rows0 : 0;
-    const int rows1 = (it.rows1 > 0 && a.gidx[it.bx + 1] == it.e) ? it.rows1 : 0;
-    if (rows0 == 0 && rows1 == 0) return;
-    const bool has1 = rows1 > 0;
-    const int64_t K = HID ? a.H : a.I, N = HID ? a.I : a.H;  // of one pair of matrices
-    int tid = threadIdx.x;
-    asm volatile("" : "+v"(tid));  // opaque per item: addresses are not hoisted out of the item loop
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int lane = tid & 63, lr = lane & 31, lh = lane >> 5;
-    const int ww = wave & 1, wt = wave >> 1;  // column half, token half
-    const int64_t n0 = (int64_t)it.nt * 256;
-
+struct Rows {
+    const TrainArgs &a;
+    unsigned char *smem;
+    int wave, lane, ww, wt;          // ww: column half, wt: token half
+    int64_t K, N;                    // of one pair of matrices
     RowOps p;
-    p.smem = smem;
-    p.dwave = (unsigned)(uintptr_t)smem + 8192 * wave;
-    p.n1 = (int)(K / BK);
-    p.nk = HID ? p.n1 : 2 * p.n1;
-    p.wstep = BK * N;
-    int64_t col = n0 + 64 * wave;
-    col = col < N ? col : N - 64;  // a narrow last slice: idle columns read valid ones
-    const int64_t wofs = (int64_t)it.e * K * N + col, tofs = (int64_t)it.bx * kBlockM * K;
-    p.w[0] = (HID ? a.wd : a.wg) + wofs;
-    p.t[0] = (HID ? a.dy : a.dg) + tofs;
-    p.w[1] = HID ? p.w[0] : a.wu + wofs;
-    p.t[1] = HID ? p.t[0] : a.du + tofs;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        p.woff[j] = k_major_off(lane, j, N);
-        const int r = 64 * wave + 8 * j + (lane >> 3);
-        const int c = (lane & 7) ^ lds_swz(r);
-        int tr = r;
-        if (r >= kBlockM && !has1) tr -= kBlockM;  // absent second block: stay in bounds
-        p.toff[j] = (unsigned)((tr * K + 8 * c) * 2);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) p.la[i >> 1][i & 1] = tr_off(lane, i >> 1, i & 1);
-    p.nb0 = 2 * ww;
-    p.trow0 = 128 * wt;
-    p.lr = lr;
-    p.lh = lh;
 
-    const int rows = wt ? rows1 : rows0;
-    const bool live = n0 + 128 * ww < N;
-    const int ntt = live ? (rows + 31) / 32 : 0;
-    f16x acc[4][4];
-    zero_acc(acc);
-    kloop_tiles(p, p.nk, ntt, acc);
-    if (ntt == 0) return;
-    const int64_t row0 = (int64_t)(it.bx + wt) * kBlockM, col0 = n0 + 128 * ww;
-    if constexpr (!HID) {
-        store_block<false>(acc, smem, wave, lane, ntt, rows, a.dx + row0 * N + col0, N);
-    } else {
-        // 32 tokens at a time: b staged in fp32 (512 bytes per row over two
-        // pieces: columns 0-63 and 64-127), read back 8 columns per lane, 16
-        // lanes per row, next to 16-byte loads of g and u
-        const int64_t c0 = a.go[it.e] + it.off + kBlockM * wt;  // compact index of the block's first row
-        const int r4 = lane >> 4, cl = lane & 15;
-        const int64_t np = N / 128;
+    __device__ __forceinline__ Rows(const TrainArgs &args, unsigned char *s) : a(args), smem(s) {
+        K = HID ? a.H : a.I;
+        N = HID ? a.I : a.H;
+        wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        lane = threadIdx.x & 63;
+        ww = wave & 1;
+        wt = wave >> 1;
+        p.smem = smem;
+        p.dwave = (unsigned)(uintptr_t)smem + 8192 * wave;
+        p.n1 = (int)(K / BK);
+        p.nk = HID ? p.n1 : 2 * p.n1;
+        p.N = N;
+        p.K = K;
+        p.woff = k_major_off(lane, N);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            if (u >= ntt) continue;
+        for (int j = 0; j < 2; ++j)
+            p.toff[j] = (unsigned)(((lane >> 3) * K + 8 * ((lane & 7) ^ lds_swz(8 * j + (lane >> 3)))) * 2);
+        p.nb0 = 2 * ww;
+        p.trow0 = 128 * wt;
+        p.lane = lane;
+    }
+    __device__ __forceinline__ void set(const Item &it) {
+        int64_t col = (int64_t)it.nt * 256 + 64 * wave;
+        col = col < N ? col : N - 64;  // a narrow last slice: idle columns read valid ones
+        // an absent second block: its half reads the first block's rows
+        const int row = it.rows1 > 0 ? 64 * wave : (64 * wave) & 127;
+        const int64_t wofs = (int64_t)it.e * K * N + col, tofs = ((int64_t)it.bx * kBlockM + row) * K;
+        p.w[0] = uniform((HID ? a.wd : a.wg) + wofs);
+        p.t[0] = uniform((HID ? a.dy : a.dg) + tofs);
+        p.w[1] = HID ? p.w[0] : uniform(a.wu + wofs);
+        p.t[1] = HID ? p.t[0] : uniform(a.du + tofs);
+    }
+    __device__ __forceinline__ int rows(const Item &it) const { return wt ? it.rows1 : it.rows0; }
+    __device__ __forceinline__ int tiles(const Item &it) const {
+        return (int64_t)it.nt * 256 + 128 * ww < N ? (rows(it) + 31) / 32 : 0;
+    }
+
+    // Epilogue; fill() issues the next item's first step.  Returns whether at
+    // least kNewer memory instructions followed it for sure.
+    template <int NTT, class F>
+    __device__ __forceinline__ bool finish(const Item &it, f16x (&acc)[4][4], F &&fill) const {
+        const int lane = fresh(this->lane), lr = lane & 31, lh = lane >> 5;
+        const int64_t row0 = (int64_t)(it.bx + wt) * kBlockM, col0 = (int64_t)it.nt * 256 + 128 * ww;
+        const int nrows = rows(it);
+        if constexpr (!HID) {
+            fill();
+            store_block<NTT, false>(acc, smem, wave, lane, nrows, a.dx + row0 * N + col0, N);
+        } else {
+            // 32 tokens at a time: b staged in fp32 (512 bytes per row over two
+            // pieces: columns 0-63 and 64-127), read back 8 columns per lane,
+            // 16 lanes per row, next to 16-byte loads of g and u
+            const int64_t c0 = table(a.go)[it.e] + it.off + kBlockM * wt;  // compact index of the block's first row
+            const int r4 = lane >> 4, cl = lane & 15;
+            const int64_t np = N / 128;
             h8 g[8], p8[8];
             float w[8];
+            auto request = [&](int u) __attribute__((always_inline)) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int row = 32 * u + 4 * i + r4;
-                if (row < rows) {
-                    const int64_t o = (row0 + row) * N + col0 + 8 * cl;
-                    g[i] = *(const h8 *)(a.g + o);
-                    p8[i] = *(const h8 *)(a.u + o);
-                    w[i] = a.rw[c0 + row];
+                for (int i = 0; i < 8; ++i) {
+                    const int row = 32 * u + 4 * i + r4;
+                    if (row < nrows) {
+                        const int64_t o = (row0 + row) * N + col0 + 8 * cl;
+                        g[i] = *(const h8 *)(a.g + o);
+                        p8[i] = *(const h8 *)(a.u + o);
+                        w[i] = a.rw[c0 + row];
+                    }
+                }
+            };
+#pragma unroll
+            for (int u = 0; u < NTT; ++u) {
+                request(u);
+                if (u + 1 == NTT) fill();
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const f16x &o = acc[t][u];
+                        const int c = (8 * (t & 1) + 2 * q + lh) ^ (lr & 15);
+                        *(f4 *)(piece(smem, wave, t >> 1) + lr * 256 + (c << 4)) =
+                            f4{o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]};
+                    }
+                __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int sr = 4 * i + r4, row = 32 * u + sr;
+                    const unsigned char *src = (cl >> 3 ? piece(smem, wave, 1) : piece(smem, wave, 0)) + sr * 256;
+                    const int c = 2 * (cl & 7);
+                    const f4 b0 = *(const f4 *)(src + ((c ^ (sr & 15)) << 4));
+                    const f4 b1 = *(const f4 *)(src + (((c + 1) ^ (sr & 15)) << 4));
+                    float dw = 0.f;
+                    h8 dg, du, hw;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float b = j < 4 ? b0[j & 3] : b1[j & 3];
+                        const float gf = (float)g[i][j], uf = (float)p8[i][j], wf = w[i];
+                        const float s = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-gf * 1.4426950408889634f));
+                        const float sl = gf * s, h = sl * uf, dh = wf * b;
+                        dw += b * h;
+                        dg[j] = (_Float16)(dh * uf * (s + sl * (1.0f - s)));
+                        du[j] = (_Float16)(dh * sl);
+                        hw[j] = (_Float16)(wf * h);
+                    }
+                    dw = sum16(dw);
+                    if (row < nrows) {
+                        const int64_t o = (row0 + row) * N + col0 + 8 * cl;
+                        *(h8 *)(a.dg + o) = dg;
+                        *(h8 *)(a.du + o) = du;
+                        *(h8 *)(a.hw + o) = hw;
+                        if (cl == 0) a.part[(c0 + row) * np + col0 / 128] = dw;
+                    }
                 }
             }
-#pragma unroll
-            for (int t = 0; t < 4; ++t)
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const f16x &o = acc[t][u];
-                    const int c = (8 * (t & 1) + 2 * q + lh) ^ (lr & 15);
-                    *(f4 *)(smem + (t >> 1) * SLOT + wave * 8192 + lr * 256 + (c << 4)) =
-                        f4{o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]};
-                }
-            __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int sr = 4 * i + r4, row = 32 * u + sr;
-                const unsigned char *src = smem + (cl >> 3) * SLOT + wave * 8192 + sr * 256;
-                const int c = 2 * (cl & 7);
-                const f4 b0 = *(const f4 *)(src + ((c ^ (sr & 15)) << 4));
-                const f4 b1 = *(const f4 *)(src + (((c + 1) ^ (sr & 15)) << 4));
-                float dw = 0.f;
-                h8 dg, du, hw;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float b = j < 4 ? b0[j & 3] : b1[j & 3];
-                    const float gf = (float)g[i][j], uf = (float)p8[i][j];
-                    const float s = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-gf * 1.4426950408889634f));
-                    const float sl = gf * s, h = sl * uf, dh = w[i] * b;
-                    dw += b * h;
-                    dg[j] = (_Float16)(dh * uf * (s + sl * (1.0f - s)));
-                    du[j] = (_Float16)(dh * sl);
-                    hw[j] = (_Float16)(w[i] * h);
-                }
-                dw = sum16(dw);
-                if (row < rows) {
-                    const int64_t o = (row0 + row) * N + col0 + 8 * cl;
-                    *(h8 *)(a.dg + o) = dg;
-                    *(h8 *)(a.du + o) = du;
-                    *(h8 *)(a.hw + o) = hw;
-                    if (cl == 0) a.part[(c0 + row) * np + col0 / 128] = dw;
-                }
-            }
+            if constexpr (NTT == 0) fill();
         }
+        return NTT == 4 && nrows == kBlockM;  // 32 stores, or the last tile's 24 and more
     }
-}
+};
 
-// Persistent, one workgroup per CU, items in the order of rmoe_sched.h.
+// Persistent, one workgroup per CU, items in the order of rmoe_sched.h.  The
+// first step of the next item travels while the current one's epilogue runs.
 template <bool HID>
 __global__ __launch_bounds__(256) void rows_kernel(TrainArgs a, int NT) {
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
-    const TileSeq seq = tile_seq(a.gs, a.E, NT, blockIdx.x % kXcd, kXcd);
+    const Table gs = table(a.gs), gpo = table(a.gpo), gidx = table(a.gidx);
+    const TileSeq seq = tile_seq(gs, a.E, NT, blockIdx.x % kXcd, kXcd);
     const int nl = gridDim.x / kXcd;
     TileCursor cur;
-    for (int i = blockIdx.x / kXcd; i < seq.n; i += nl) run_rows<HID>(a, smem, tile_item(a.gs, a.gpo, seq, i, cur));
+    int i = blockIdx.x / kXcd;
+    // the next item that holds rows (blocks mapped to another expert hold none)
+    auto advance = [&](Item &it) __attribute__((always_inline)) {
+        for (; i < seq.n; i += nl) {
+            const TileItem t = tile_item(gs, gpo, seq, i, cur);
+            it = Item{t.nt, t.e, t.bx, t.off, gidx[t.bx] == t.e ? t.rows0 : 0, 0};
+            if (t.rows1 > 0 && gidx[t.bx + 1] == t.e) it.rows1 = t.rows1;
+            if (it.rows0 || it.rows1) {
+                i += nl;
+                return true;
+            }
+        }
+        return false;
+    };
+    Rows<HID> r(a, smem);
+    Item it;
+    if (!advance(it)) return;
+    r.set(it);
+    kfill(r.p);
+    bool newer = false, more = true;
+    while (more) {
+        ktiles(r.p, r.tiles(it), newer, [&](auto &acc, auto n) __attribute__((always_inline)) {
+            const Item now = it;
+            newer = r.template finish<decltype(n)::value>(now, acc, [&]() __attribute__((always_inline)) {
+                more = advance(it);
+                if (more) {
+                    r.set(it);
+                    kfill(r.p);
+                }
+            });
+        });
+    }
 }
 
 // drw[c] = the sum of c's partial sums in ascending order of their columns:
@@ -386,39 +459,40 @@ __global__ __launch_bounds__(256) void cols_kernel(TrainArgs a, int total) {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lane = threadIdx.x & 63;
     const int ww = wave & 1, wt = wave >> 1;
-    const int ntt = a0 + 128 * ww < NA && b0 + 128 * wt < NB ? 4 : 0;
+    const bool live = a0 + 128 * ww < NA && b0 + 128 * wt < NB;
+    _Float16 *y = (m == 0 ? a.dwg : m == 1 ? a.dwu : a.dwd) + (int64_t)e * NA * NB + (b0 + 128 * wt) * NA + a0 + 128 * ww;
+    if (nk == 0) {
+        if (!live) return;
+        const h8 z = {0, 0, 0, 0, 0, 0, 0, 0};
+        for (int r = lane >> 4; r < 128; r += 4) __builtin_nontemporal_store(z, (h8 *)(y + r * NA + 8 * (lane & 15)));
+        return;
+    }
+    ColOps p;
+    p.smem = smem;
+    p.dwave = (unsigned)(uintptr_t)smem + 8192 * wave;
+    p.nk = nk;
+    p.tail = n % BK;
+    p.NA = NA;
+    p.NB = NB;
+    int64_t ca = a0 + 64 * wave, cb = b0 + 64 * wave;
+    ca = ca < NA ? ca : NA - 64;  // narrow last tiles: idle columns read valid ones
+    cb = cb < NB ? cb : NB - 64;
+    p.a = uniform((m < 2 ? a.x : a.hw) + row0 * NA + ca);
+    p.b = uniform((m == 0 ? (const _Float16 *)a.dg : m == 1 ? (const _Float16 *)a.du : a.dy) + row0 * NB + cb);
+    p.aoff = k_major_off(lane, NA);
+    p.boff = k_major_off(lane, NB);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p.la[i >> 1][i & 1] = tr_off(lane, i >> 1, i & 1);
+    p.na0 = 2 * ww;
+    p.nb0 = 2 * wt;
+    kfill(p);
     f16x acc[4][4];
     zero_acc(acc);
-    if (nk > 0) {
-        ColOps p;
-        p.smem = smem;
-        p.dwave = (unsigned)(uintptr_t)smem + 8192 * wave;
-        p.nk = nk;
-        p.tail = n % BK;
-        p.astep = BK * NA;
-        p.bstep = BK * NB;
-        int64_t ca = a0 + 64 * wave, cb = b0 + 64 * wave;
-        ca = ca < NA ? ca : NA - 64;  // narrow last tiles: idle columns read valid ones
-        cb = cb < NB ? cb : NB - 64;
-        p.a = (m < 2 ? a.x : a.hw) + row0 * NA + ca;
-        p.b = (m == 0 ? a.dg : m == 1 ? a.du : a.dy) + row0 * NB + cb;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            p.aoff[j] = k_major_off(lane, j, NA);
-            p.boff[j] = k_major_off(lane, j, NB);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) p.la[i >> 1][i & 1] = tr_off(lane, i >> 1, i & 1);
-        p.na0 = 2 * ww;
-        p.nb0 = 2 * wt;
-        if (ntt)
-            kloop<4>(p, nk, acc);
-        else
-            kloop<0>(p, nk, acc);
-    }
-    if (ntt == 0) return;
-    _Float16 *y = (m == 0 ? a.dwg : m == 1 ? a.dwu : a.dwd) + (int64_t)e * NA * NB;
-    store_block<true>(acc, smem, wave, lane, 4, 128, y + (b0 + 128 * wt) * NA + a0 + 128 * ww, NA);
+    if (live)
+        kloop<4>(p, false, acc);
+    else
+        kloop<0>(p, false, acc);
+    if (live) store_block<4, true>(acc, smem, wave, lane, 128, y, NA);
 }
 
 template <bool HID>
