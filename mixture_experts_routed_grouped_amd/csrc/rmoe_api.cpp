@@ -848,12 +848,12 @@ int rmoe_gate_up_train_f16(const void *x, const void *gate_w, const void *up_w, 
         return RMOE_ERR_INVALID_ARGUMENT;
     if (!all16(x, gate_w, up_w, gate, up, hidden_rows) || !all4(gs, gpo, gidx)) return RMOE_ERR_MISALIGNED;
     if (num_blocks_m == 0) return RMOE_OK;
-    rmoe::StageArgs a{};
-    a.x = f16(x), a.w0 = f16(gate_w), a.w1 = f16(up_w);
+    rmoe::TrainArgs a{};
+    a.x = f16(x), a.wg = f16(gate_w), a.wu = f16(up_w);
     a.gs = gs, a.gpo = gpo, a.gidx = gidx;
-    a.y = f16(hidden_rows), a.yg = f16(gate), a.yu = f16(up);
-    a.K = hidden, a.N = intermediate, a.E = num_experts, a.M = num_blocks_m, a.pairs = total_valid_tokens;
-    return to_status(rmoe::launch_tile_gate_up_train(a, static_cast<hipStream_t>(stream)));
+    a.yg = f16(gate), a.yu = f16(up), a.yh = f16(hidden_rows);
+    a.H = hidden, a.I = intermediate, a.E = num_experts, a.Tp = total_padded_tokens, a.M = num_blocks_m;
+    return to_status(rmoe::launch_gate_up_train(a, static_cast<hipStream_t>(stream)));
 }
 
 size_t rmoe_backward_scratch_bytes(int64_t num_pairs, int64_t intermediate) {

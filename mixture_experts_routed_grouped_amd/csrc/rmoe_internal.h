@@ -62,7 +62,6 @@ struct StageArgs {
     int64_t K, N;
     int32_t E, M;
     int64_t pairs;
-    _Float16 *yg, *yu;      // [Tp, N]: gate and up themselves (the training forward only)
 };
 
 // Kernel-family launchers; return hipSuccess or the launch error.
@@ -70,8 +69,6 @@ hipError_t launch_stream_gate_up(const StageArgs &a, hipStream_t s);
 hipError_t launch_stream_down(const StageArgs &a, hipStream_t s);
 hipError_t launch_tile_gate_up(const StageArgs &a, hipStream_t s);
 hipError_t launch_tile_down(const StageArgs &a, hipStream_t s);
-// gate/up that also stores the pre-activations (a.yg, a.yu)
-hipError_t launch_tile_gate_up_train(const StageArgs &a, hipStream_t s);
 // Both tiled stages in one persistent launch (gu.y = dn.x = the hidden
 // workspace); sync as described for rmoe_forward_fused_f16; a down tile
 // waits at most wait_us for its pair's hidden rows.  local: each XCD runs
@@ -128,7 +125,7 @@ hipError_t launch_mx_tile_down(const MxArgs &a, hipStream_t s);
 hipError_t launch_mx_stream_gate_up(const MxArgs &a, hipStream_t s);
 hipError_t launch_mx_stream_down(const MxArgs &a, hipStream_t s);
 
-// ---- backward pass (rmoe_train.hip)
+// ---- training (rmoe_train.hip)
 
 struct TrainArgs {
     const _Float16 *x, *dy;             // [Tp, H] token rows, output gradient
@@ -136,6 +133,7 @@ struct TrainArgs {
     const float *rw;                    // [pairs] compact order
     const _Float16 *g, *u;              // [Tp, I] kept pre-activations
     const int32_t *gs, *go, *gpo, *gidx;
+    _Float16 *yg, *yu, *yh;             // [Tp, I] the training forward's gate, up and hidden rows
     _Float16 *dg, *du, *hw;             // [Tp, I] (dg, du may be g, u themselves)
     float *part, *drw;                  // [pairs, I / 128] partial sums; [pairs]
     _Float16 *dx;                       // [Tp, H]
@@ -143,6 +141,7 @@ struct TrainArgs {
     int64_t H, I, Tp, pairs;
     int32_t E, M;
 };
+hipError_t launch_gate_up_train(const TrainArgs &a, hipStream_t s);     // yg, yu, yh
 hipError_t launch_down_backward(const TrainArgs &a, hipStream_t s);     // dg, du, hw, drw
 hipError_t launch_gate_up_backward(const TrainArgs &a, hipStream_t s);  // dx
 hipError_t launch_weight_grad(const TrainArgs &a, hipStream_t s);       // dwg, dwu, dwd

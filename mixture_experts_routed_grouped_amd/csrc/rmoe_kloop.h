@@ -39,6 +39,8 @@
 #include <type_traits>
 
 #include "rmoe_device.h"
+#include "rmoe_internal.h"
+#include "rmoe_sched.h"
 
 namespace rmoe {
 
@@ -157,22 +159,74 @@ __device__ __forceinline__ void zero_acc(f16x (&acc)[4][4]) {
 // done(accumulators, count as a constant): one copy of the epilogue per
 // count, so that the accumulators stay in the registers of their loop (one
 // copy after all loops cost 336 register moves per item).
+template <int NTT, class P, class F>
+__device__ __forceinline__ void krun(P &p, bool newer, F &&done) {
+    p.begin();
+    f16x acc[4][4];
+    zero_acc(acc);
+    kloop<NTT>(p, newer, acc);
+    done(acc, std::integral_constant<int, NTT>{});
+}
 template <class P, class F>
 __device__ __forceinline__ void ktiles(P &p, int ntt, bool newer, F &&done) {
-    auto run = [&](auto n) __attribute__((always_inline)) {
-        constexpr int NTT = decltype(n)::value;
-        p.begin();
-        f16x acc[4][4];
-        zero_acc(acc);
-        kloop<NTT>(p, newer, acc);
-        done(acc, n);
-    };
     switch (ntt) {
-        case 4: run(std::integral_constant<int, 4>{}); break;
-        case 3: run(std::integral_constant<int, 3>{}); break;
-        case 2: run(std::integral_constant<int, 2>{}); break;
-        case 1: run(std::integral_constant<int, 1>{}); break;
-        default: run(std::integral_constant<int, 0>{}); break;
+        case 4: krun<4>(p, newer, done); break;
+        case 3: krun<3>(p, newer, done); break;
+        case 2: krun<2>(p, newer, done); break;
+        case 1: krun<1>(p, newer, done); break;
+        default: krun<0>(p, newer, done); break;
+    }
+}
+
+// A work item: blocks bx (rows0 valid rows) and bx + 1 (rows1, 0: absent or
+// of another expert) of expert e, off rows into it, against slice nt.
+struct Item {
+    int nt, e, bx, off, rows0, rows1;
+};
+
+// The items of a persistent workgroup (one per CU, in the order of
+// rmoe_sched.h).  T, the tile, provides p (its operands), set(item) (their
+// bases), tiles(item) (this wave's live token tiles) and finish<NTT>(item,
+// acc, fill): the epilogue, which calls fill() once, where the next item's
+// first step may go out, and returns whether at least kNewer memory
+// instructions of this wave certainly followed it.
+template <class T>
+__device__ __forceinline__ void run_items(T &tile, const int32_t *group_sizes, const int32_t *padded_offsets,
+                                          const int32_t *block_experts, int E, int NT) {
+    const Table gs = table(group_sizes), gpo = table(padded_offsets), gidx = table(block_experts);
+    const TileSeq seq = tile_seq(gs, E, NT, blockIdx.x % kXcd, kXcd);
+    const int nl = gridDim.x / kXcd;
+    TileCursor cur;
+    int i = blockIdx.x / kXcd;
+    // the next item that holds rows (blocks mapped to another expert hold none)
+    auto advance = [&](Item &it) __attribute__((always_inline)) {
+        for (; i < seq.n; i += nl) {
+            const TileItem t = tile_item(gs, gpo, seq, i, cur);
+            it = Item{t.nt, t.e, t.bx, t.off, gidx[t.bx] == t.e ? t.rows0 : 0, 0};
+            if (t.rows1 > 0 && gidx[t.bx + 1] == t.e) it.rows1 = t.rows1;
+            if (it.rows0 || it.rows1) {
+                i += nl;
+                return true;
+            }
+        }
+        return false;
+    };
+    Item it;
+    if (!advance(it)) return;
+    tile.set(it);
+    kfill(tile.p);
+    bool newer = false, more = true;
+    while (more) {
+        ktiles(tile.p, tile.tiles(it), newer, [&](auto &acc, auto n) __attribute__((always_inline)) {
+            const Item now = it;
+            newer = tile.template finish<decltype(n)::value>(now, acc, [&]() __attribute__((always_inline)) {
+                more = advance(it);
+                if (more) {
+                    tile.set(it);
+                    kfill(tile.p);
+                }
+            });
+        });
     }
 }
 

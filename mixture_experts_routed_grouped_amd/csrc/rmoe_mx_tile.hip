@@ -15,10 +15,8 @@
 // the hidden rows cost 4.25 bits per element of memory traffic.
 #include <atomic>
 
-#include "rmoe_internal.h"
 #include "rmoe_kloop.h"
 #include "rmoe_mx.h"
-#include "rmoe_sched.h"
 
 namespace rmoe {
 namespace {
@@ -102,12 +100,6 @@ struct MxOps {
         c = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(xa, ya, c, 4, 4, S, (int)sa[t], S, (int)sb[u]);
     }
     __device__ __forceinline__ void publish(int) {}
-};
-
-// A work item as the kernel runs it: blocks bx (rows0 valid rows) and bx + 1
-// (rows1, 0: absent or of another expert) against weight slice nt.
-struct Item {
-    int nt, e, bx, off, rows0, rows1;
 };
 
 // What a lane and a wave hold for the whole launch, and the item's bases.
@@ -265,54 +257,23 @@ struct Tile {
             }
         }
     }
+
+    template <int NTT, class F>
+    __device__ __forceinline__ bool finish(const Item &it, f16x (&acc)[4][4], F &&fill) const {
+        fill();
+        if constexpr (DUAL)
+            hidden<NTT>(it, acc);
+        else
+            out<NTT>(it, acc);
+        return !DUAL && NTT == 4 && rows(it) == kBlockM;  // a whole block of out rows: 32 stores
+    }
 };
 
-// Persistent, one workgroup per CU, items in the order of rmoe_sched.h.  The
-// first step of the next item travels while the current one's epilogue runs.
 template <bool DUAL>
 __global__ __launch_bounds__(256) void mx_tile_kernel(MxArgs a, int NT) {
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
-    const Table gs = table(a.gs), gpo = table(a.gpo), gidx = table(a.gidx);
-    const TileSeq seq = tile_seq(gs, a.E, NT, blockIdx.x % kXcd, kXcd);
-    const int nl = gridDim.x / kXcd;
-    TileCursor cur;
-    int i = blockIdx.x / kXcd;
-    // the next item that holds rows (blocks mapped to another expert hold none)
-    auto advance = [&](Item &it) __attribute__((always_inline)) {
-        for (; i < seq.n; i += nl) {
-            const TileItem t = tile_item(gs, gpo, seq, i, cur);
-            it = Item{t.nt, t.e, t.bx, t.off, gidx[t.bx] == t.e ? t.rows0 : 0, 0};
-            if (t.rows1 > 0 && gidx[t.bx + 1] == t.e) it.rows1 = t.rows1;
-            if (it.rows0 || it.rows1) {
-                i += nl;
-                return true;
-            }
-        }
-        return false;
-    };
     Tile<DUAL> tile(a, smem);
-    Item it;
-    if (!advance(it)) return;
-    tile.set(it);
-    kfill(tile.p);
-    bool newer = false, more = true;
-    while (more) {
-        ktiles(tile.p, tile.tiles(it), newer, [&](auto &acc, auto n) __attribute__((always_inline)) {
-            constexpr int NTT = decltype(n)::value;
-            const Item now = it;
-            more = advance(it);
-            if (more) {
-                tile.set(it);
-                kfill(tile.p);
-            }
-            if constexpr (DUAL)
-                tile.template hidden<NTT>(now, acc);
-            else
-                tile.template out<NTT>(now, acc);
-            // a whole block's out rows: 32 stores since the fill
-            newer = !DUAL && NTT == 4 && tile.rows(now) == kBlockM;
-        });
-    }
+    run_items(tile, a.gs, a.gpo, a.gidx, a.E, NT);
 }
 
 template <bool DUAL>

@@ -97,9 +97,7 @@ __device__ unsigned long long phase_cycles[2][kPhaseWg][5];
 // WT: store the output tile write-through at device scope (sc1), so that a
 // store that has completed (vmcnt) is visible to every XCD without an L2
 // write-back; the single-launch path hands the hidden rows over this way.
-// SAVE (gate/up): also store the gate and up rows themselves, for a backward
-// pass.
-template <bool DUAL, bool WT = false, bool SAVE = false>
+template <bool DUAL, bool WT = false>
 __device__ __forceinline__ void run_tile(const StageArgs &a, unsigned char *smem, int nt, int bx,
                                          const BlockInfo &b0, bool has1, int rows1,
                                          PhaseSums *ps = nullptr) {
@@ -327,54 +325,6 @@ __device__ __forceinline__ void run_tile(const StageArgs &a, unsigned char *smem
         for (int u = 0; u < 4; ++u)
             if (u < ntt && 32 * u + lr < myrows) wtok[u] = rwe[32 * u + lr];
     }
-    // row-contiguous read-back of the staged rows to y: OC lanes per row,
-    // 64 / OC rows per instruction
-    auto store_rows = [&](_Float16 *y) {
-        __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): this wave's staging writes are done
-        _Float16 *ybase = y + (int64_t)bmine * kBlockM * N + n0 + (DUAL ? 64 : 128) * ww;
-        const int c = lane % OC;
-        // buffer view of this wave's output tile (128 rows of N, < 2^31 bytes)
-        [[maybe_unused]] const __amdgpu_buffer_rsrc_t yres =
-            __builtin_amdgcn_make_buffer_rsrc(ybase, 0, 0x7fffffff, 0x00020000);
-#pragma unroll 4
-        for (int r0 = 0; r0 < 32 * ntt; r0 += 64 / OC) {
-            const int row = r0 + lane / OC;
-            if (row < myrows) {
-                const h8 v = *(const h8 *)(stage_row(row) + ((c ^ (row & (OC - 1))) << 4));
-                if constexpr (WT)
-                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(i32x4, v), yres,
-                                                           (int)(((int64_t)row * N + 8 * c) * 2), 0,
-                                                           kCpolSc1);
-                else
-                    *(h8 *)(ybase + (int64_t)row * N + 8 * c) = v;
-            }
-        }
-    };
-    // the kept pre-activations, through the same staging rows: gate (tiles
-    // 0, 1), then up (tiles 2, 3)
-    if constexpr (SAVE) {
-        static_assert(DUAL, "only the gate/up stage keeps its pre-activations");
-#pragma unroll
-        for (int m = 0; m < 2; ++m) {
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                if (u >= ntt) continue;
-                const int row = 32 * u + lr;
-                unsigned char *srow = stage_row(row);
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const f16x &g = acc[t + 2 * m][u];
-                        const int c = (4 * t + q) ^ (row & (OC - 1));
-                        *(h4 *)(srow + (c << 4) + 8 * lh) =
-                            to_h4(g[4 * q + 0], g[4 * q + 1], g[4 * q + 2], g[4 * q + 3]);
-                    }
-                }
-            }
-            store_rows(m ? a.yu : a.yg);
-        }
-    }
     // 32x32 accumulator layout: lane holds token column (lane & 31) and,
     // for register 4q + r, weight row 8q + 4lh + r of its 32-row tile t
 #pragma unroll
@@ -409,7 +359,26 @@ __device__ __forceinline__ void run_tile(const StageArgs &a, unsigned char *smem
             }
         }
     }
-    store_rows(a.y);
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): this wave's staging writes are done
+    // row-contiguous read-back: OC lanes per row, 64 / OC rows per instruction
+    _Float16 *ybase = a.y + (int64_t)bmine * kBlockM * N + n0 + (DUAL ? 64 : 128) * ww;
+    const int c = lane % OC;
+    // buffer view of this wave's output tile (128 rows of N, < 2^31 bytes)
+    [[maybe_unused]] const __amdgpu_buffer_rsrc_t yres =
+        __builtin_amdgcn_make_buffer_rsrc(ybase, 0, 0x7fffffff, 0x00020000);
+#pragma unroll 4
+    for (int r0 = 0; r0 < 32 * ntt; r0 += 64 / OC) {
+        const int row = r0 + lane / OC;
+        if (row < myrows) {
+            const h8 v = *(const h8 *)(stage_row(row) + ((c ^ (row & (OC - 1))) << 4));
+            if constexpr (WT)
+                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(i32x4, v), yres,
+                                                       (int)(((int64_t)row * N + 8 * c) * 2), 0,
+                                                       kCpolSc1);
+            else
+                *(h8 *)(ybase + (int64_t)row * N + 8 * c) = v;
+        }
+    }
     phase_end();
 }
 
@@ -418,7 +387,7 @@ __device__ __forceinline__ void run_tile(const StageArgs &a, unsigned char *smem
 // computed only if group_idx_for_bx maps it to the item's expert (the rule
 // the streaming family applies per block, in block_info), so both families
 // act on the same table and skip the same blocks of a corrupted one.
-template <bool DUAL, bool WT = false, bool SAVE = false>
+template <bool DUAL, bool WT = false>
 __device__ __forceinline__ void run_item(const StageArgs &a, unsigned char *smem, const TileItem &it,
                                          PhaseSums *ps = nullptr) {
     BlockInfo b0;
@@ -427,7 +396,7 @@ __device__ __forceinline__ void run_item(const StageArgs &a, unsigned char *smem
     b0.rows = a.gidx[it.bx] == it.e ? it.rows0 : 0;
     const int rows1 = (it.rows1 > 0 && a.gidx[it.bx + 1] == it.e) ? it.rows1 : 0;
     if (b0.rows == 0 && rows1 == 0) return;
-    run_tile<DUAL, WT, SAVE>(a, smem, it.nt, it.bx, b0, rows1 > 0, rows1, ps);
+    run_tile<DUAL, WT>(a, smem, it.nt, it.bx, b0, rows1 > 0, rows1, ps);
 }
 
 // Persistent kernel: one workgroup per CU (a multiple of 8 of them, LDS_BYTES
@@ -437,7 +406,7 @@ __device__ __forceinline__ void run_item(const StageArgs &a, unsigned char *smem
 // is cut into 8 contiguous parts, one per XCD (workgroup w runs on XCD
 // w % 8), so the 32 workgroups of an XCD run a rectangle of 4 consecutive
 // pairs x 8 slices at a time -- operands they share in that XCD's L2.
-template <bool DUAL, bool SAVE = false>
+template <bool DUAL>
 __global__ __launch_bounds__(256) void tile_kernel(StageArgs a, int NT) {
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
     const TileSeq seq = tile_seq(a.gs, a.E, NT, blockIdx.x % kXcd, kXcd);
@@ -446,7 +415,7 @@ __global__ __launch_bounds__(256) void tile_kernel(StageArgs a, int NT) {
     PhaseSums ps;
     [[maybe_unused]] const unsigned long long ts = phase_clock();
     for (int i = blockIdx.x / kXcd; i < seq.n; i += nl)
-        run_item<DUAL, false, SAVE>(a, smem, tile_item(a.gs, a.gpo, seq, i, cur), &ps);
+        run_item<DUAL>(a, smem, tile_item(a.gs, a.gpo, seq, i, cur), &ps);
 #if RMOE_PHASE_TIMING
     const unsigned long long te = phase_clock();
     if (threadIdx.x == 0 && blockIdx.x < kPhaseWg) {
@@ -654,16 +623,16 @@ hipError_t wall_clock_khz(int &khz) {
     return hipSuccess;
 }
 
-template <bool DUAL, bool SAVE = false>
+template <bool DUAL>
 hipError_t launch(const StageArgs &a, int NT, hipStream_t s) {
     unsigned grid = 0;
     hipError_t e = persistent_grid(grid);
     if (e != hipSuccess) return e;
     const unsigned lds = LDS_BYTES;  // above the 64 KB default, so opt in
     static std::atomic<uint64_t> lds_set{0};
-    e = lds_opt_in_once((const void *)tile_kernel<DUAL, SAVE>, (int)lds, lds_set);
+    e = lds_opt_in_once((const void *)tile_kernel<DUAL>, (int)lds, lds_set);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((tile_kernel<DUAL, SAVE>), dim3(grid), dim3(256), lds, s, a, NT);
+    hipLaunchKernelGGL(tile_kernel<DUAL>, dim3(grid), dim3(256), lds, s, a, NT);
     return hipGetLastError();
 }
 
@@ -671,10 +640,6 @@ hipError_t launch(const StageArgs &a, int NT, hipStream_t s) {
 
 hipError_t launch_tile_gate_up(const StageArgs &a, hipStream_t s) {
     return launch<true>(a, (int)(a.N / 128), s);
-}
-
-hipError_t launch_tile_gate_up_train(const StageArgs &a, hipStream_t s) {
-    return launch<true, true>(a, (int)(a.N / 128), s);
 }
 
 hipError_t launch_tile_down(const StageArgs &a, hipStream_t s) {

@@ -27,9 +27,7 @@
 // spreads the 4 rows x 64 bytes that 32 lanes read over all 64 banks.
 #include <atomic>
 
-#include "rmoe_internal.h"
 #include "rmoe_kloop.h"
-#include "rmoe_sched.h"
 
 namespace rmoe {
 namespace {
@@ -129,6 +127,41 @@ struct RowOps : OpsBase {
     __device__ __forceinline__ void publish(int) {}
 };
 
+// A (gate and up weight rows) and B (token rows) row-major, K = H.
+struct DualOps : OpsBase {
+    static constexpr int AR = 1, BR = 1;
+    unsigned char *smem;
+    unsigned dwave;
+    const _Float16 *w, *t;        // uniform bases: this wave's 64 weight rows, its 64 token rows
+    int64_t row8;                 // elements of 8 rows
+    unsigned off[2];              // lane offset of instruction j from its rows 8 j: j even, odd
+    const _Float16 *wcur, *tcur;  // first row of the instruction issued last (a group's go out in order)
+    int nk, lane, lr, lh, arow, trow0;
+
+    __device__ __forceinline__ void begin() {
+        const int l = fresh(lane);
+        lr = l & 31;
+        lh = l >> 5;
+    }
+    __device__ __forceinline__ void dma(int d, int j) {
+        if (d < 8) {
+            tcur = d == 0 ? t + (int64_t)min(j + NBS, nk - 1) * BK : tcur + row8;
+            dma16_sb(tcur, off[d & 1], dwave + B_OFF + ((j + NBS) % NBS) * SLOT + 1024 * d);
+        } else {
+            wcur = d == 8 ? w + (int64_t)min(j + NAS, nk - 1) * BK : wcur + row8;
+            dma16_sb(wcur, off[d & 1], dwave + ((j + NAS) % NAS) * SLOT + 1024 * (d - 8));
+        }
+    }
+    __device__ __forceinline__ void read(int k, int s, int i, Frag *a, Frag *b) {
+        const int ch = 2 * s + lh;
+        if (i < 4)  // tiles 0, 1 gate rows, 2, 3 the same up rows
+            a[i] = *(const h8 *)(smem + (k % NAS) * SLOT + lds_off(arow + 32 * (i & 1) + 128 * (i >> 1) + lr, ch));
+        else
+            b[i - 4] = *(const h8 *)(smem + B_OFF + (k % NBS) * SLOT + lds_off(trow0 + 32 * (i - 4) + lr, ch));
+    }
+    __device__ __forceinline__ void publish(int) {}
+};
+
 // A and B k-major: the sum runs over token rows.
 struct ColOps : OpsBase {
     static constexpr int AR = 2, BR = 2;
@@ -140,7 +173,13 @@ struct ColOps : OpsBase {
     const _Float16 *acur, *bcur;  // first row of the instruction issued last (a group's go out in order)
     int nk, tail;                 // rows of the last step, 0: a whole one
     unsigned la[2][2];
-    int na0, nb0;                 // first column groups of this wave's halves
+    int lane, na0, nb0;           // first column groups of this wave's halves
+
+    __device__ __forceinline__ void begin() {
+        const int l = fresh(lane);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) la[i >> 1][i & 1] = tr_off(l, i >> 1, i & 1);
+    }
 
     __device__ __forceinline__ void dma(int d, int j) {
         if (d < 8) {
@@ -237,12 +276,6 @@ __device__ __forceinline__ float sum16(float x) {
     x += rot<0x121>(x);
     return x;
 }
-
-// A work item of a row product: blocks bx (rows0 valid rows) and bx + 1
-// (rows1, 0: absent or of another expert) of expert e against 256 columns.
-struct Item {
-    int nt, e, bx, off, rows0, rows1;
-};
 
 // HID: the hidden stage (b = dy . Wd and everything that follows from it
 // element by element); otherwise dx.  Holds what a lane and a wave keep for
@@ -373,47 +406,96 @@ struct Rows {
     }
 };
 
-// Persistent, one workgroup per CU, items in the order of rmoe_sched.h.  The
-// first step of the next item travels while the current one's epilogue runs.
 template <bool HID>
 __global__ __launch_bounds__(256) void rows_kernel(TrainArgs a, int NT) {
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
-    const Table gs = table(a.gs), gpo = table(a.gpo), gidx = table(a.gidx);
-    const TileSeq seq = tile_seq(gs, a.E, NT, blockIdx.x % kXcd, kXcd);
-    const int nl = gridDim.x / kXcd;
-    TileCursor cur;
-    int i = blockIdx.x / kXcd;
-    // the next item that holds rows (blocks mapped to another expert hold none)
-    auto advance = [&](Item &it) __attribute__((always_inline)) {
-        for (; i < seq.n; i += nl) {
-            const TileItem t = tile_item(gs, gpo, seq, i, cur);
-            it = Item{t.nt, t.e, t.bx, t.off, gidx[t.bx] == t.e ? t.rows0 : 0, 0};
-            if (t.rows1 > 0 && gidx[t.bx + 1] == t.e) it.rows1 = t.rows1;
-            if (it.rows0 || it.rows1) {
-                i += nl;
-                return true;
+    Rows<HID> r(a, smem);
+    run_items(r, a.gs, a.gpo, a.gidx, a.E, NT);
+}
+
+// The training forward's gate/up stage: 128 features per item, their gate
+// rows in the first half of the A slot and the same up rows in the second, so
+// that a lane holds gate and up of the same (token, feature).
+struct Forward {
+    const TrainArgs &a;
+    unsigned char *smem;
+    int wave, lane, ww, wt;  // ww: feature half, wt: token half
+    DualOps p;
+
+    __device__ __forceinline__ Forward(const TrainArgs &args, unsigned char *s) : a(args), smem(s) {
+        wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        lane = threadIdx.x & 63;
+        ww = wave & 1;
+        wt = wave >> 1;
+        p.smem = smem;
+        p.dwave = (unsigned)(uintptr_t)smem + 8192 * wave;
+        p.nk = (int)(a.H / BK);
+        p.row8 = 8 * a.H;
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            p.off[j] = (unsigned)(((lane >> 3) * a.H + 8 * ((lane & 7) ^ lds_swz(8 * j + (lane >> 3)))) * 2);
+        p.arow = 64 * ww;
+        p.trow0 = 128 * wt;
+        p.lane = lane;
+    }
+    __device__ __forceinline__ void set(const Item &it) {
+        const int64_t f0 = (int64_t)it.nt * 128 + ((64 * wave) & 127);
+        const int row = it.rows1 > 0 ? 64 * wave : (64 * wave) & 127;  // as in Rows::set
+        p.w = uniform((wave < 2 ? a.wg : a.wu) + ((int64_t)it.e * a.I + f0) * a.H);
+        p.t = uniform(a.x + ((int64_t)it.bx * kBlockM + row) * a.H);
+    }
+    __device__ __forceinline__ int rows(const Item &it) const { return wt ? it.rows1 : it.rows0; }
+    __device__ __forceinline__ int tiles(const Item &it) const { return (rows(it) + 31) / 32; }
+
+    // gate, up and hidden rows, one after the other through the staging
+    // pieces: 128 rows of 64 features, 64 rows per piece
+    template <int NTT, class F>
+    __device__ __forceinline__ bool finish(const Item &it, f16x (&acc)[4][4], F &&fill) const {
+        fill();
+        const int ln = fresh(lane), lr = ln & 31, lh = ln >> 5, c = ln & 7;
+        const int nrows = rows(it);
+        const int64_t o = ((int64_t)(it.bx + wt) * kBlockM) * a.I + (int64_t)it.nt * 128 + 64 * ww + 8 * c;
+#pragma unroll
+        for (int m = 0; m < 3; ++m) {
+#pragma unroll
+            for (int u = 0; u < NTT; ++u)
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const f16x &g = acc[t][u], &p2 = acc[t + 2][u];
+                        float v[4];
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            v[r] = m == 0 ? g[4 * q + r] : m == 1 ? p2[4 * q + r] : silu(g[4 * q + r]) * p2[4 * q + r];
+                        *(h4 *)(piece(smem, wave, u >> 1) + (32 * (u & 1) + lr) * 128 + (((4 * t + q) ^ (lr & 7)) << 4) +
+                                8 * lh) = to_h4(v[0], v[1], v[2], v[3]);
+                    }
+            __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): this wave's staging writes are done
+            _Float16 *y = (m == 0 ? a.yg : m == 1 ? a.yu : a.yh) + o;
+#pragma unroll
+            for (int u = 0; u < NTT; ++u) {
+                h8 v[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int r = 8 * j + (ln >> 3);
+                    v[j] = *(const h8 *)(piece(smem, wave, u >> 1) + (32 * (u & 1) + r) * 128 + ((c ^ (r & 7)) << 4));
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int row = 32 * u + 8 * j + (ln >> 3);
+                    if (row < nrows) *(h8 *)(y + (int64_t)row * a.I) = v[j];
+                }
             }
         }
-        return false;
-    };
-    Rows<HID> r(a, smem);
-    Item it;
-    if (!advance(it)) return;
-    r.set(it);
-    kfill(r.p);
-    bool newer = false, more = true;
-    while (more) {
-        ktiles(r.p, r.tiles(it), newer, [&](auto &acc, auto n) __attribute__((always_inline)) {
-            const Item now = it;
-            newer = r.template finish<decltype(n)::value>(now, acc, [&]() __attribute__((always_inline)) {
-                more = advance(it);
-                if (more) {
-                    r.set(it);
-                    kfill(r.p);
-                }
-            });
-        });
+        return NTT == 4 && nrows == kBlockM;  // 48 stores
     }
+};
+
+__global__ __launch_bounds__(256) void forward_kernel(TrainArgs a, int NT) {
+    extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
+    Forward f(a, smem);
+    run_items(f, a.gs, a.gpo, a.gidx, a.E, NT);
 }
 
 // drw[c] = the sum of c's partial sums in ascending order of their columns:
@@ -433,66 +515,127 @@ __global__ __launch_bounds__(256) void drw_kernel(const float *part, const int32
 }
 
 // Weight gradients: every 256 x 256 tile of the three matrices of every
-// expert, its sum over the expert's rows.  An expert without rows gets
-// zeros.  Workgroups are dealt to the XCDs in runs of 32 consecutive tiles
-// (4 rows of tiles x 8), which share operands in that XCD's L2; heavy
-// experts spread over all XCDs, and the hardware starts the next tile
-// wherever a CU is free.
+// expert, its sum over the expert's rows; an expert without rows gets zeros.
+// Persistent, one workgroup per CU.  Tiles are dealt to the XCDs in runs of
+// 32 consecutive ones (4 rows of tiles x 8), one per CU, which share operands
+// in that XCD's L2 and take the same time; every expert's runs spread over
+// the XCDs.
+struct Cols {
+    const TrainArgs &a;
+    unsigned char *smem;
+    int wave, lane, ww, wt;  // ww: A half, wt: B half
+    int nh, ni;              // tiles along H and I
+    ColOps p;
+
+    struct Tile {
+        int e, m, n;           // expert, matrix, rows
+        int64_t a0, b0, row0;  // first A column (contiguous in the output), first B column (its row), first row
+    };
+
+    __device__ __forceinline__ Cols(const TrainArgs &args, unsigned char *s) : a(args), smem(s) {
+        wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        lane = threadIdx.x & 63;
+        ww = wave & 1;
+        wt = wave >> 1;
+        nh = (int)((a.H + 255) / 256);
+        ni = (int)((a.I + 255) / 256);
+        p.smem = smem;
+        p.dwave = (unsigned)(uintptr_t)smem + 8192 * wave;
+        p.lane = lane;
+        p.na0 = 2 * ww;
+        p.nb0 = 2 * wt;
+    }
+    // matrix m: 0 dWg, 1 dWu (A = x, B = dg or du), 2 dWd (A = hw, B = dy)
+    __device__ __forceinline__ int64_t cols_a(int m) const { return m < 2 ? a.H : a.I; }
+    __device__ __forceinline__ int64_t cols_b(int m) const { return m < 2 ? a.I : a.H; }
+
+    // Tile of position i; false where there is nothing to do: past the last
+    // tile, or a group whose tables break the contract (nothing is read out
+    // of bounds, its gradients are left out).
+    __device__ __forceinline__ bool at(int item, Tile &t) const {
+        const int per = nh * ni;
+        t.e = item / (3 * per);
+        t.m = (item / per) % 3;
+        const int q = item % per, nA = t.m < 2 ? nh : ni, nB = t.m < 2 ? ni : nh;
+        const int g = q / (8 * nB), width = min(8, nA - 8 * g), r = q - 8 * g * nB;
+        t.a0 = (int64_t)(8 * g + r % width) * 256;
+        t.b0 = (int64_t)(r / width) * 256;
+        t.n = table(a.gs)[t.e];
+        t.row0 = table(a.gpo)[t.e];
+        return t.n >= 0 && t.row0 >= 0 && t.row0 + ((int64_t)t.n + BK - 1) / BK * BK <= a.Tp;
+    }
+    __device__ __forceinline__ void set(const Tile &t) {
+        const int64_t NA = cols_a(t.m), NB = cols_b(t.m);
+        p.nk = (t.n + BK - 1) / BK;
+        p.tail = t.n % BK;
+        p.NA = NA;
+        p.NB = NB;
+        p.aoff = k_major_off(lane, NA);
+        p.boff = k_major_off(lane, NB);
+        int64_t ca = t.a0 + 64 * wave, cb = t.b0 + 64 * wave;
+        ca = ca < NA ? ca : NA - 64;  // narrow last tiles: idle columns read valid ones
+        cb = cb < NB ? cb : NB - 64;
+        const _Float16 *g = t.m == 0 ? a.dg : t.m == 1 ? a.du : a.dy;
+        p.a = uniform((t.m < 2 ? a.x : a.hw) + t.row0 * NA + ca);
+        p.b = uniform(g + t.row0 * NB + cb);
+    }
+    __device__ __forceinline__ bool live(const Tile &t) const {
+        return t.a0 + 128 * ww < cols_a(t.m) && t.b0 + 128 * wt < cols_b(t.m);
+    }
+    __device__ __forceinline__ _Float16 *out(const Tile &t) const {
+        const int64_t NA = cols_a(t.m);
+        return (t.m == 0 ? a.dwg : t.m == 1 ? a.dwu : a.dwd) + (int64_t)t.e * a.H * a.I + (t.b0 + 128 * wt) * NA +
+               t.a0 + 128 * ww;
+    }
+    __device__ __forceinline__ void zeros(const Tile &t) const {
+        if (!live(t)) return;
+        const h8 z = {0, 0, 0, 0, 0, 0, 0, 0};
+        _Float16 *y = out(t) + 8 * (lane & 15);
+        for (int r = lane >> 4; r < 128; r += 4) __builtin_nontemporal_store(z, (h8 *)(y + r * cols_a(t.m)));
+    }
+};
+
 __global__ __launch_bounds__(256) void cols_kernel(TrainArgs a, int total) {
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
-    const int xcd = blockIdx.x % kXcd, seq = blockIdx.x / kXcd;
-    const int item = ((seq / 32) * kXcd + xcd) * 32 + seq % 32;
-    if (item >= total) return;
-    const int nh = (int)((a.H + 255) / 256), ni = (int)((a.I + 255) / 256), per = nh * ni;
-    const int e = item / (3 * per), m = (item / per) % 3, q = item % per;
-    // matrix m: A columns (contiguous in the output), B columns (its rows)
-    const int64_t NA = m < 2 ? a.H : a.I, NB = m < 2 ? a.I : a.H;
-    const int nA = m < 2 ? nh : ni, nB = m < 2 ? ni : nh;
-    const int g = q / (8 * nB), width = min(8, nA - 8 * g), r = q - 8 * g * nB;
-    const int64_t a0 = (int64_t)(8 * g + r % width) * 256, b0 = (int64_t)(r / width) * 256;
-    const int n = a.gs[e];
-    const int64_t row0 = a.gpo[e];
-    const int nk = (n + BK - 1) / BK;
-    // tables that break the contract: nothing read out of bounds, tile left out
-    if (n < 0 || row0 < 0 || row0 + (int64_t)nk * BK > a.Tp) return;
-
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int lane = threadIdx.x & 63;
-    const int ww = wave & 1, wt = wave >> 1;
-    const bool live = a0 + 128 * ww < NA && b0 + 128 * wt < NB;
-    _Float16 *y = (m == 0 ? a.dwg : m == 1 ? a.dwu : a.dwd) + (int64_t)e * NA * NB + (b0 + 128 * wt) * NA + a0 + 128 * ww;
-    if (nk == 0) {
-        if (!live) return;
-        const h8 z = {0, 0, 0, 0, 0, 0, 0, 0};
-        for (int r = lane >> 4; r < 128; r += 4) __builtin_nontemporal_store(z, (h8 *)(y + r * NA + 8 * (lane & 15)));
-        return;
+    Cols c(a, smem);
+    const int xcd = blockIdx.x % kXcd, nl = gridDim.x / kXcd;
+    int j = blockIdx.x / kXcd;  // position in this XCD's list
+    // the next tile whose expert holds rows; the zeros of the others on the way
+    auto advance = [&](Cols::Tile &t) __attribute__((always_inline)) {
+        for (;; j += nl) {
+            const int item = (j / 32 * kXcd + xcd) * 32 + j % 32;
+            if (j / 32 * kXcd * 32 >= total) return false;
+            if (item >= total || !c.at(item, t)) continue;
+            if (t.n == 0) {
+                c.zeros(t);
+                continue;
+            }
+            j += nl;
+            return true;
+        }
+    };
+    Cols::Tile t;
+    if (!advance(t)) return;
+    c.set(t);
+    kfill(c.p);
+    bool newer = false, more = true;
+    while (more) {
+        auto finish = [&](auto &acc, auto n) __attribute__((always_inline)) {
+            const Cols::Tile now = t;
+            more = advance(t);
+            if (more) {
+                c.set(t);
+                kfill(c.p);
+            }
+            constexpr int NTT = decltype(n)::value;
+            store_block<NTT, true>(acc, smem, c.wave, fresh(c.lane), kBlockM, c.out(now), c.cols_a(now.m));
+            newer = NTT == 4;  // 32 stores
+        };
+        if (c.live(t))
+            krun<4>(c.p, newer, finish);
+        else
+            krun<0>(c.p, newer, finish);
     }
-    ColOps p;
-    p.smem = smem;
-    p.dwave = (unsigned)(uintptr_t)smem + 8192 * wave;
-    p.nk = nk;
-    p.tail = n % BK;
-    p.NA = NA;
-    p.NB = NB;
-    int64_t ca = a0 + 64 * wave, cb = b0 + 64 * wave;
-    ca = ca < NA ? ca : NA - 64;  // narrow last tiles: idle columns read valid ones
-    cb = cb < NB ? cb : NB - 64;
-    p.a = uniform((m < 2 ? a.x : a.hw) + row0 * NA + ca);
-    p.b = uniform((m == 0 ? (const _Float16 *)a.dg : m == 1 ? (const _Float16 *)a.du : a.dy) + row0 * NB + cb);
-    p.aoff = k_major_off(lane, NA);
-    p.boff = k_major_off(lane, NB);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) p.la[i >> 1][i & 1] = tr_off(lane, i >> 1, i & 1);
-    p.na0 = 2 * ww;
-    p.nb0 = 2 * wt;
-    kfill(p);
-    f16x acc[4][4];
-    zero_acc(acc);
-    if (live)
-        kloop<4>(p, false, acc);
-    else
-        kloop<0>(p, false, acc);
-    if (live) store_block<4, true>(acc, smem, wave, lane, 128, y, NA);
 }
 
 template <bool HID>
@@ -509,6 +652,17 @@ hipError_t launch_rows(const TrainArgs &a, hipStream_t s) {
 }
 
 }  // namespace
+
+hipError_t launch_gate_up_train(const TrainArgs &a, hipStream_t s) {
+    unsigned grid = 0;
+    hipError_t e = persistent_grid(grid);
+    if (e != hipSuccess) return e;
+    static std::atomic<uint64_t> lds_set{0};
+    e = lds_opt_in_once((const void *)forward_kernel, LDS_BYTES, lds_set);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(forward_kernel, dim3(grid), dim3(256), LDS_BYTES, s, a, (int)(a.I / 128));
+    return hipGetLastError();
+}
 
 hipError_t launch_down_backward(const TrainArgs &a, hipStream_t s) {
     const hipError_t e = launch_rows<true>(a, s);
@@ -531,9 +685,11 @@ hipError_t launch_weight_grad(const TrainArgs &a, hipStream_t s) {
     static std::atomic<uint64_t> lds_set{0};
     hipError_t e = lds_opt_in_once((const void *)cols_kernel, LDS_BYTES, lds_set);
     if (e != hipSuccess) return e;
-    const int64_t total = weight_grad_tiles(a.H, a.I, a.E);
-    const int64_t grid = (total + 255) / 256 * 256;  // whole runs of 32 on each of 8 XCDs
-    hipLaunchKernelGGL(cols_kernel, dim3((unsigned)grid), dim3(256), LDS_BYTES, s, a, (int)total);
+    unsigned grid = 0;
+    e = persistent_grid(grid);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(cols_kernel, dim3(grid), dim3(256), LDS_BYTES, s, a,
+                       (int)weight_grad_tiles(a.H, a.I, a.E));
     return hipGetLastError();
 }
 
