@@ -29,6 +29,19 @@ __device__ __forceinline__ float mx_amax(float m, float a, float b) {
     return __builtin_elementwise_maximum(__builtin_elementwise_maximum(__builtin_fabsf(a), __builtin_fabsf(b)), m);
 }
 
+// Swaps a's lanes 32-63 with b's lanes 0-31.
+__device__ __forceinline__ void swap32(unsigned &a, unsigned &b) {
+    const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+    a = r[0];
+    b = r[1];
+}
+// The maximum of lanes l and l ^ 32, in both.
+__device__ __forceinline__ float mx_amax32(float m) {
+    unsigned a = __builtin_bit_cast(unsigned, m), b = a;
+    swap32(a, b);  // the lower half's in a, the upper's in b
+    return mx_amax(0.f, __builtin_bit_cast(float, a), __builtin_bit_cast(float, b));
+}
+
 // Scale byte of a block by its largest magnitude: floor(log2(amax)) - 2 +
 // 127, so that the largest element lands in [4, 8); at least 0 (amax <
 // 2^-125, zero included).  Infinities and NaN give 255, the format's NaN.
@@ -37,10 +50,9 @@ __device__ __forceinline__ unsigned mx_scale_byte(float amax) {
     return ex == 255 ? 255u : ex > 2 ? (unsigned)(ex - 2) : 0u;
 }
 
-// E2M1 codes of N values over 2^(byte - 127), rounded to nearest even and
-// clamped at 6 by the conversion instruction, 8 per dword.  Small scales are
-// moved up by 2^64 together with the values (exact), away from the subnormal
-// scales: a branch that no wave with a block above 2^-61 takes.
+// E2M1 codes of 8 values over 2^(byte - 127), rounded to nearest even and
+// clamped at 6 by the conversion instruction, which takes the scale's exponent
+// field as it is (byte 0: 2^-127, subnormal values included).
 __device__ __forceinline__ unsigned mx_pack8(const float *v, float scale) {
     unsigned r = 0;
     r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, v[0], v[1], scale, 0);
@@ -50,20 +62,10 @@ __device__ __forceinline__ unsigned mx_pack8(const float *v, float scale) {
     return r;
 }
 template <int N>
-__device__ __forceinline__ void mx_codes(float (&v)[N], unsigned byte, unsigned (&out)[N / 8]) {
-    unsigned sb = byte;
-    if (__builtin_expect(__any(byte < 64), 0)) {
-        const float up = byte < 64 ? 0x1p64f : 1.0f;
-        sb = byte < 64 ? byte + 64 : byte;
+__device__ __forceinline__ void mx_codes(const float (&v)[N], unsigned byte, unsigned (&out)[N / 8]) {
+    const float scale = __builtin_bit_cast(float, byte << 23);
 #pragma unroll
-        for (int i = 0; i < N; ++i) v[i] *= up;
-    }
-    const float scale = __builtin_bit_cast(float, sb << 23);
-#pragma unroll
-    for (int i = 0; i < N / 8; ++i) {
-        out[i] = mx_pack8(v + 8 * i, scale);
-        if (byte == 255u) out[i] = 0;
-    }
+    for (int i = 0; i < N / 8; ++i) out[i] = byte == 255u ? 0u : mx_pack8(v + 8 * i, scale);
 }
 
 }  // namespace rmoe

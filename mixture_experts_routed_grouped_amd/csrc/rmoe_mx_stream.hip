@@ -186,19 +186,19 @@ __device__ __forceinline__ void stream_pass(const MxArgs &a, const BlockInfo &bi
             for (int r = 0; r < 16; ++r) v[r] = silu(sum(0, t, r)) * sum(1, t, r);
 #pragma unroll
             for (int r = 0; r < 16; r += 2) m = mx_amax(m, v[r], v[r + 1]);
-            m = mx_amax(0.f, m, __shfl_xor(m, 32));
-            const unsigned byte = mx_scale_byte(m);
-            unsigned cd[2];  // quads 0, 1 and 2, 3: 16 bits each
-            mx_codes<16>(v, byte, cd);
-            const unsigned c01 = cd[0], c23 = cd[1];
-            const unsigned h01 = (unsigned)__shfl_xor((int)c01, 32), h23 = (unsigned)__shfl_xor((int)c23, 32);
+            const unsigned byte = mx_scale_byte(mx_amax32(m));
+            unsigned lo[2];  // quads 0, 1 and 2, 3: 16 bits each
+            mx_codes<16>(v, byte, lo);
+            unsigned hi[2] = {lo[0], lo[1]};  // the upper lanes' half
+            swap32(lo[0], hi[0]);
+            swap32(lo[1], hi[1]);
             const int tok = p0 + 32 * t + lr;
             if (lh == 0 && tok < bi.rows) {
                 u4 o;
-                o[0] = (c01 & 0xffffu) | (h01 << 16);
-                o[1] = (c01 >> 16) | (h01 & 0xffff0000u);
-                o[2] = (c23 & 0xffffu) | (h23 << 16);
-                o[3] = (c23 >> 16) | (h23 & 0xffff0000u);
+                o[0] = (lo[0] & 0xffffu) | (hi[0] << 16);
+                o[1] = (lo[0] >> 16) | (hi[0] & 0xffff0000u);
+                o[2] = (lo[1] & 0xffffu) | (hi[1] << 16);
+                o[3] = (lo[1] >> 16) | (hi[1] & 0xffff0000u);
                 const int64_t row = (int64_t)bx * kBlockM + tok;
                 *(u4 *)(a.yc + row * orb + 16 * b) = o;
                 unsigned char *ys = a.ys + ((int64_t)(b >> 3) * a.Tp + row) * 8;

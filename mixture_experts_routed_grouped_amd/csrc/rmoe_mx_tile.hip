@@ -45,9 +45,9 @@ struct MxOps {
     int64_t sstep;         // bytes between a step's scales and the next step's
     unsigned sdst;         // LDS address of this wave's scale half
     unsigned soff;         // 16 * lane
-    int64_t row8;          // bytes of 8 rows
-    const unsigned char *tcur, *wcur;  // first row of the instruction issued last (a group's go out in order)
-    unsigned off[2];       // lane offset of instruction j from its rows 8 j: j even, odd
+    unsigned row16;        // bytes of 16 rows
+    unsigned off[2];       // lane offsets of instructions 0 and 1 of a slot; j: 16 rows past j - 2
+    unsigned to[2], wo[2];
     int nk;
     int lane, lr, lh, arow, trow0;  // arow: first A row of this wave's tile 0; tile t at arow + 32 (t & 1) + astep (t / 2)
     int astep;
@@ -63,12 +63,17 @@ struct MxOps {
         if (d == 0) {
             dma16_sb(sbase + (int64_t)kt * sstep, soff, sdst + slot * SSLOT);
         } else if (d <= 8) {
-            tcur = d == 1 ? tbase + (int64_t)kt * kMxChunkBytes : tcur + row8;
-            dma16_sb(tcur, off[(d - 1) & 1], dwave + T_OFF + slot * SLOT + 1024 * (d - 1));
+            const unsigned o = row_off(to, d - 1);
+            dma16_sb(tbase + (int64_t)kt * kMxChunkBytes, o, dwave + T_OFF + slot * SLOT + 1024 * (d - 1));
         } else {
-            wcur = d == 9 ? wbase + (int64_t)kt * kMxChunkBytes : wcur + row8;
-            dma16_sb(wcur, off[(d - 9) & 1], dwave + W_OFF + slot * SLOT + 1024 * (d - 9));
+            const unsigned o = row_off(wo, d - 9);
+            dma16_sb(wbase + (int64_t)kt * kMxChunkBytes, o, dwave + W_OFF + slot * SLOT + 1024 * (d - 9));
         }
+    }
+    // lane offset of instruction j of a slot, whose instructions go out in order
+    __device__ __forceinline__ unsigned row_off(unsigned (&o)[2], int j) {
+        o[j & 1] = j < 2 ? (unsigned)fresh((int)off[j]) : o[j & 1] + row16;
+        return o[j & 1];
     }
     __device__ __forceinline__ int row_a(int t) const { return arow + 32 * (t & 1) + astep * (t >> 1); }
     __device__ __forceinline__ void read(int k, int s, int i, Frag *a, Frag *b) {
@@ -126,10 +131,12 @@ struct Tile {
         p.astep = DUAL ? 128 : 64;
         // instruction j moves rows 64 w + 8 j + lane / 8 of a slot, physical
         // chunk lane % 8; the rows' swizzle repeats with j's parity
-        p.row8 = 8 * rb;
+        p.row16 = (unsigned)(16 * rb);
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-            p.off[j] = (unsigned)((lane >> 3) * rb + 16 * ((lane & 7) ^ lds_swz(8 * j + (lane >> 3))));
+        for (int j = 0; j < 2; ++j) {
+            const int r = 8 * j + (lane >> 3);
+            p.off[j] = (unsigned)(r * rb + 16 * ((lane & 7) ^ lds_swz(r)));
+        }
         const unsigned lds0 = (unsigned)(uintptr_t)smem;
         p.dwave = lds0 + 64 * wave * kMxChunkBytes;
         p.sdst = lds0 + (wave < 2 ? WS_OFF : TS_OFF) + 1024 * (wave & 1);
@@ -181,20 +188,18 @@ struct Tile {
                 for (int i = 0; i < 16; ++i) v[i] = silu(acc[t][u][i]) * acc[t + 2][u][i];
 #pragma unroll
                 for (int i = 0; i < 16; i += 2) m = mx_amax(m, v[i], v[i + 1]);
-                m = mx_amax(0.f, m, __shfl_xor(m, 32));
-                byte[t] = mx_scale_byte(m);
+                byte[t] = mx_scale_byte(mx_amax32(m));
                 mx_codes<16>(v, byte[t], cd[t]);
             }
-            // send the other lane half its block, keep the own one
-            const unsigned r01 = (unsigned)__shfl_xor((int)(lh ? cd[0][0] : cd[1][0]), 32);
-            const unsigned r23 = (unsigned)__shfl_xor((int)(lh ? cd[0][1] : cd[1][1]), 32);
-            const unsigned m01 = lh ? cd[1][0] : cd[0][0], m23 = lh ? cd[1][1] : cd[0][1];
-            const unsigned l01 = lh ? r01 : m01, h01 = lh ? m01 : r01, l23 = lh ? r23 : m23, h23 = lh ? m23 : r23;
+            // lower lanes take block 0, upper ones block 1: after the swaps
+            // cd[0] holds the lower lanes' half of it, cd[1] the upper ones'
+            swap32(cd[0][0], cd[1][0]);
+            swap32(cd[0][1], cd[1][1]);
             u4 o;
-            o[0] = (l01 & 0xffffu) | (h01 << 16);
-            o[1] = (l01 >> 16) | (h01 & 0xffff0000u);
-            o[2] = (l23 & 0xffffu) | (h23 << 16);
-            o[3] = (l23 >> 16) | (h23 & 0xffff0000u);
+            o[0] = (cd[0][0] & 0xffffu) | (cd[1][0] << 16);
+            o[1] = (cd[0][0] >> 16) | (cd[1][0] & 0xffff0000u);
+            o[2] = (cd[0][1] & 0xffffu) | (cd[1][1] << 16);
+            o[3] = (cd[0][1] >> 16) | (cd[1][1] & 0xffff0000u);
             const int row = 32 * u + lr;
             if (row < myrows) {
                 unsigned char *ys = a.ys + ((b >> 3) * a.Tp + row0 + row) * 8;
@@ -230,6 +235,7 @@ struct Tile {
         const int c = ln & 15;
 #pragma unroll
         for (int u0 = 0; u0 < NTT; u0 += 2) {
+            __builtin_amdgcn_sched_barrier(0);  // no accumulator is copied out early: registers
 #pragma unroll
             for (int u = u0; u < u0 + 2 && u < NTT; ++u)
 #pragma unroll

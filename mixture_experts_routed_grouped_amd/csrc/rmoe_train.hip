@@ -55,13 +55,39 @@ __device__ __forceinline__ h4 tr_read(const unsigned char *p) {
         h4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4 *)p));
 }
 
-// DMA source of a k-major slot: wave w fills column group w, instruction j
-// k rows 8j .. 8j+7; byte offset of this lane from (k row 8j, the wave's
-// first column) in a matrix of N columns.
-__device__ __forceinline__ unsigned k_major_off(int lane, int64_t N) {
-    const int r = lane >> 3, c = (lane & 7) ^ swz_k(r);
-    return (unsigned)((r * N + 8 * c) * 2);
-}
+// Lane offsets of a slot's instructions, which go out in order: a row-major
+// slot's rows 8 j .. 8 j + 7 (the swizzle repeats with j's parity), a k-major
+// slot's k rows 8 j ...  One vector add per instruction (from a fresh first
+// one, so that the sums are not kept per instruction: 16 registers through
+// the epilogue, which spill); as scalar base additions they delayed the MFMAs
+// (5% of the row products' time).
+struct RowSteps {
+    unsigned first[2], step, cur[2];  // bytes: of 16 rows
+    __device__ __forceinline__ void init(int lane, int64_t K) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int r = 8 * j + (lane >> 3);
+            first[j] = (unsigned)((r * K + 8 * ((lane & 7) ^ lds_swz(r))) * 2);
+        }
+        step = (unsigned)(32 * K);
+    }
+    __device__ __forceinline__ unsigned at(int j) {
+        cur[j & 1] = j < 2 ? (unsigned)fresh((int)first[j]) : cur[j & 1] + step;
+        return cur[j & 1];
+    }
+};
+struct ColSteps {
+    unsigned first, step, cur;  // bytes: of 8 k rows
+    __device__ __forceinline__ void init(int lane, int64_t N) {
+        const int r = lane >> 3;
+        first = (unsigned)((r * N + 8 * ((lane & 7) ^ swz_k(r))) * 2);
+        step = (unsigned)(16 * N);
+    }
+    __device__ __forceinline__ unsigned at(int j) {
+        cur = j == 0 ? (unsigned)fresh((int)first) : cur + step;
+        return cur;
+    }
+};
 
 struct OpsBase {
     typedef h8 Frag;
@@ -81,9 +107,9 @@ struct RowOps : OpsBase {
     unsigned char *smem;
     unsigned dwave;
     const _Float16 *w[2], *t[2];  // uniform bases of the two pairs
-    unsigned woff, toff[2];       // lane offsets from an instruction's first row (tokens: j even, odd)
-    int64_t N, K;                 // elements per weight row, token row
-    const _Float16 *wcur, *tcur;  // first row of the instruction issued last (a group's go out in order)
+    ColSteps ws;
+    RowSteps ts;
+    int64_t N;                    // elements per weight row
     int nk, n1;
     unsigned la[2][2];            // tr_off of tile parity, half
     int nb0;                      // first column group of this wave's A half
@@ -98,21 +124,15 @@ struct RowOps : OpsBase {
     }
     __device__ __forceinline__ void dma(int d, int j) {
         if (d < 8) {
-            if (d == 0) {
-                const int k = min(j + NBS, nk - 1), two = k >= n1;
-                tcur = (two ? t[1] : t[0]) + (int64_t)(two ? k - n1 : k) * BK;
-            } else {
-                tcur += 8 * K;
-            }
-            dma16_sb(tcur, toff[d & 1], dwave + B_OFF + ((j + NBS) % NBS) * SLOT + 1024 * d);
+            const int k = min(j + NBS, nk - 1), two = k >= n1;
+            const unsigned o = ts.at(d);
+            dma16_sb((two ? t[1] : t[0]) + (int64_t)(two ? k - n1 : k) * BK, o,
+                     dwave + B_OFF + ((j + NBS) % NBS) * SLOT + 1024 * d);
         } else {
-            if (d == 8) {
-                const int k = min(j + NAS, nk - 1), two = k >= n1;
-                wcur = (two ? w[1] : w[0]) + (int64_t)(two ? k - n1 : k) * BK * N;
-            } else {
-                wcur += 8 * N;
-            }
-            dma16_sb(wcur, woff, dwave + ((j + NAS) % NAS) * SLOT + 1024 * (d - 8));
+            const int k = min(j + NAS, nk - 1), two = k >= n1;
+            const unsigned o = ws.at(d - 8);
+            dma16_sb((two ? w[1] : w[0]) + (int64_t)(two ? k - n1 : k) * BK * N, o,
+                     dwave + ((j + NAS) % NAS) * SLOT + 1024 * (d - 8));
         }
     }
     __device__ __forceinline__ void read(int k, int s, int i, Frag *a, Frag *b) {
@@ -168,7 +188,7 @@ struct ColOps : OpsBase {
     unsigned char *smem;
     unsigned dwave;
     const _Float16 *a, *b;
-    unsigned aoff, boff;
+    ColSteps as, bs;
     int64_t NA, NB;               // elements per row
     const _Float16 *acur, *bcur;  // first row of the instruction issued last (a group's go out in order)
     int nk, tail;                 // rows of the last step, 0: a whole one
@@ -184,10 +204,10 @@ struct ColOps : OpsBase {
     __device__ __forceinline__ void dma(int d, int j) {
         if (d < 8) {
             bcur = d == 0 ? b + (int64_t)min(j + NBS, nk - 1) * BK * NB : bcur + 8 * NB;
-            dma16_sb(bcur, boff, dwave + B_OFF + ((j + NBS) % NBS) * SLOT + 1024 * d);
+            dma16_sb(bcur, bs.first, dwave + B_OFF + ((j + NBS) % NBS) * SLOT + 1024 * d);
         } else {
             acur = d == 8 ? a + (int64_t)min(j + NAS, nk - 1) * BK * NA : acur + 8 * NA;
-            dma16_sb(acur, aoff, dwave + ((j + NAS) % NAS) * SLOT + 1024 * (d - 8));
+            dma16_sb(acur, as.first, dwave + ((j + NAS) % NAS) * SLOT + 1024 * (d - 8));
         }
     }
     __device__ __forceinline__ void read(int k, int s, int i, Frag *fa, Frag *fb) {
@@ -300,11 +320,8 @@ struct Rows {
         p.n1 = (int)(K / BK);
         p.nk = HID ? p.n1 : 2 * p.n1;
         p.N = N;
-        p.K = K;
-        p.woff = k_major_off(lane, N);
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-            p.toff[j] = (unsigned)(((lane >> 3) * K + 8 * ((lane & 7) ^ lds_swz(8 * j + (lane >> 3)))) * 2);
+        p.ws.init(lane, N);
+        p.ts.init(lane, K);
         p.nb0 = 2 * ww;
         p.trow0 = 128 * wt;
         p.lane = lane;
@@ -338,28 +355,35 @@ struct Rows {
         } else {
             // 32 tokens at a time: b staged in fp32 (512 bytes per row over two
             // pieces: columns 0-63 and 64-127), read back 8 columns per lane,
-            // 16 lanes per row, next to 16-byte loads of g and u
+            // 16 lanes and 4 rows per pass, next to 16-byte loads of g and u;
+            // a pass requests its rows of the next 32 tokens once it is done
+            // with its own
             const int64_t c0 = table(a.go)[it.e] + it.off + kBlockM * wt;  // compact index of the block's first row
             const int r4 = lane >> 4, cl = lane & 15;
             const int64_t np = N / 128;
             h8 g[8], p8[8];
             float w[8];
-            auto request = [&](int u) __attribute__((always_inline)) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int row = 32 * u + 4 * i + r4;
-                    if (row < nrows) {
-                        const int64_t o = (row0 + row) * N + col0 + 8 * cl;
-                        g[i] = *(const h8 *)(a.g + o);
-                        p8[i] = *(const h8 *)(a.u + o);
-                        w[i] = a.rw[c0 + row];
-                    }
+            auto request = [&](int u, int i) __attribute__((always_inline)) {
+                const int row = 32 * u + 4 * i + r4;
+                if (row < nrows) {
+                    const int64_t o = (row0 + row) * N + col0 + 8 * cl;
+                    g[i] = *(const h8 *)(a.g + o);
+                    p8[i] = *(const h8 *)(a.u + o);
+                    w[i] = a.rw[c0 + row];
                 }
             };
+            if constexpr (NTT > 0) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) request(0, i);
+            }
 #pragma unroll
             for (int u = 0; u < NTT; ++u) {
-                request(u);
-                if (u + 1 == NTT) fill();
+                // the last requests have landed before the next item's DMAs
+                // go out: a later wait for one would wait for the DMAs too
+                if (u + 1 == NTT) {
+                    wait_vm<0>();
+                    fill();
+                }
 #pragma unroll
                 for (int t = 0; t < 4; ++t)
 #pragma unroll
@@ -398,6 +422,7 @@ struct Rows {
                         *(h8 *)(a.hw + o) = hw;
                         if (cl == 0) a.part[(c0 + row) * np + col0 / 128] = dw;
                     }
+                    if (u + 1 < NTT) request(u + 1, i);
                 }
             }
             if constexpr (NTT == 0) fill();
@@ -570,8 +595,8 @@ struct Cols {
         p.tail = t.n % BK;
         p.NA = NA;
         p.NB = NB;
-        p.aoff = k_major_off(lane, NA);
-        p.boff = k_major_off(lane, NB);
+        p.as.init(lane, NA);
+        p.bs.init(lane, NB);
         int64_t ca = t.a0 + 64 * wave, cb = t.b0 + 64 * wave;
         ca = ca < NA ? ca : NA - 64;  // narrow last tiles: idle columns read valid ones
         cb = cb < NB ? cb : NB - 64;
