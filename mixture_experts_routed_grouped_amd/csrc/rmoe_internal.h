@@ -122,8 +122,8 @@ struct MxArgs {
 };
 hipError_t launch_mx_tile_gate_up(const MxArgs &a, hipStream_t s);
 hipError_t launch_mx_tile_down(const MxArgs &a, hipStream_t s);
-hipError_t launch_mx_stream_gate_up(const MxArgs &a, hipStream_t s);
-hipError_t launch_mx_stream_down(const MxArgs &a, hipStream_t s);
+hipError_t launch_mx_stream_gate_up(const MxArgs &a, int64_t pairs, hipStream_t s);
+hipError_t launch_mx_stream_down(const MxArgs &a, int64_t pairs, hipStream_t s);
 
 // ---- training (rmoe_train.hip)
 

@@ -4,13 +4,17 @@
 //
 // As the fp16 streaming family, a workgroup takes one 128-row block x FT
 // tiles of 32 output features, its KS waves split K into contiguous ranges
-// and run without barriers until a fixed-order reduction through LDS, and
-// everything travels by DMA into per-wave rings: 32 weight rows x 128 bytes
-// (256 elements) per tile and chunk, the pass's token rows, and 256 bytes of
-// scales per 32 rows (one dword per lane: global_load_lds_dword).  A row is
-// a quarter as long as in fp16 (16 chunks at K = 4096), so a workgroup's
-// start and end weigh more: two waves and at most 78 KB per workgroup let
-// two workgroups share a CU, one reading while the other starts or reduces.
+// and run without barriers, and everything travels by DMA into per-wave
+// rings: 32 weight rows x 128 bytes (256 elements) per tile and chunk, the
+// pass's token rows, and 256 bytes of scales per 32 rows (one dword per lane:
+// global_load_lds_dword).  A row is a quarter as long as in fp16 (16 chunks at
+// K = 4096), so a workgroup's start and end weigh more; what hides them is
+// small workgroups, many per CU.  One wave per workgroup (KS = 1: no reduction
+// either) with two ring slots, 34 KB of LDS for passes of up to 64 tokens,
+// measured best on a decode batch (64 tokens, 8 experts, 4096 x 14336): its
+// two stages take 124 us, 6.0 TB/s of weights; two waves 128, four 160, three
+// ring slots 127.  KS = 2 and 4 serve calls with few workgroups, where one
+// wave's K loop would be the whole time.
 #include <atomic>
 #include <type_traits>
 
@@ -24,7 +28,6 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef unsigned u4 __attribute__((ext_vector_type(4)));
 
-constexpr int KS = 2;                // waves (K ranges) per workgroup
 constexpr int TILE_B = 32 * 128;     // 32 rows of a chunk
 constexpr int SCALE_B = 32 * 8;      // their scales
 constexpr int TILE_ALL = TILE_B + SCALE_B;
@@ -34,25 +37,25 @@ __device__ __forceinline__ void dma4(const void *g, unsigned lds) {
     asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dword %1, off" ::"s"(lds), "v"(g) : "memory", "m0");
 }
 
-template <bool DUAL, int TT>
+template <bool DUAL, int KS, int TT>
 struct Cfg {
-    static constexpr int FT = DUAL ? 1 : 2;           // feature tiles per workgroup
-    static constexpr int NM = 2;                      // weight tiles: gate and up, or two of down
-    static constexpr int D = TT == 1 ? 3 : 2;         // ring slots per wave
+    static constexpr int FT = DUAL ? 1 : 2;            // feature tiles per workgroup
+    static constexpr int NM = 2;                       // weight tiles: gate and up, or two of down
+    static constexpr int D = 2;                        // ring slots per wave
     static constexpr int SLOT = (NM + TT) * TILE_ALL;  // tiles, then their scales
     static constexpr int RING = KS * D * SLOT;
-    static constexpr int RED = KS * NM * TT * 16 * 64 * 4;
+    static constexpr int RED = KS > 1 ? KS * NM * TT * 16 * 64 * 4 : 0;
     static constexpr int LDS_BYTES = RING > RED ? RING : RED;
-    static_assert(LDS_BYTES <= 80 * 1024, "two workgroups per CU");
+    static_assert(LDS_BYTES <= 160 * 1024, "LDS");
 };
 
 // One pass: token rows p0 .. p0 + 32 TT - 1 of block bx (the first 8 TD of
 // them are moved: LDS rows past them keep stale values, which only reach
 // output columns that are not stored) against features n0 ...
-template <bool DUAL, int TT, int TD>
+template <bool DUAL, int KS, int TT, int TD>
 __device__ __forceinline__ void stream_pass(const MxArgs &a, const BlockInfo &bi, int bx, int p0, int n0,
                                             unsigned char *smem, int wave, int lane) {
-    using C = Cfg<DUAL, TT>;
+    using C = Cfg<DUAL, KS, TT>;
     constexpr int NM = C::NM, D = C::D;
     constexpr int DMA_PER_CHUNK = 4 * NM + TD + NM + TT;
     static_assert((D - 1) * DMA_PER_CHUNK < 64, "vmcnt range");
@@ -159,14 +162,17 @@ __device__ __forceinline__ void stream_pass(const MxArgs &a, const BlockInfo &bi
 
     // ---- fixed-order reduction of the KS partial sums
     float *red = reinterpret_cast<float *>(smem);  // [KS][NM][TT][16][64]
+    if constexpr (KS > 1) {
 #pragma unroll
-    for (int m = 0; m < NM; ++m)
+        for (int m = 0; m < NM; ++m)
 #pragma unroll
-        for (int t = 0; t < TT; ++t)
+            for (int t = 0; t < TT; ++t)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) red[(((wave * NM + m) * TT + t) * 16 + r) * 64 + lane] = acc[m][t][r];
-    __syncthreads();
+                for (int r = 0; r < 16; ++r) red[(((wave * NM + m) * TT + t) * 16 + r) * 64 + lane] = acc[m][t][r];
+        __syncthreads();
+    }
     auto sum = [&](int m, int t, int r) {
+        if constexpr (KS == 1) return acc[m][t][r];
         float s = red[((m * TT + t) * 16 + r) * 64 + lane];
 #pragma unroll
         for (int w = 1; w < KS; ++w) s += red[(((w * NM + m) * TT + t) * 16 + r) * 64 + lane];
@@ -238,7 +244,7 @@ __device__ __forceinline__ void stream_pass(const MxArgs &a, const BlockInfo &bi
 
 // grid: (N / (32 FT), num_blocks_m), 64 KS threads.  A block of up to 64 rows
 // reads its expert's weights once, a larger one once per 64 rows.
-template <bool DUAL>
+template <bool DUAL, int KS>
 __global__ __launch_bounds__(64 * KS) void mx_stream_kernel(MxArgs a) {
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
     const int bx = blockIdx.y;
@@ -246,31 +252,45 @@ __global__ __launch_bounds__(64 * KS) void mx_stream_kernel(MxArgs a) {
     if (bi.rows == 0) return;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lane = threadIdx.x & 63;
-    const int n0 = blockIdx.x * 32 * Cfg<DUAL, 1>::FT;
+    const int n0 = blockIdx.x * 32 * Cfg<DUAL, KS, 1>::FT;
     for (int p0 = 0; p0 < bi.rows; p0 += 64) {
         const int td = (bi.rows - p0 + 7) / 8;  // token rows of the pass, in 8s
-        if (td <= 1) stream_pass<DUAL, 1, 1>(a, bi, bx, p0, n0, smem, wave, lane);
-        else if (td == 2) stream_pass<DUAL, 1, 2>(a, bi, bx, p0, n0, smem, wave, lane);
-        else if (td <= 4) stream_pass<DUAL, 1, 4>(a, bi, bx, p0, n0, smem, wave, lane);
-        else if (td <= 6) stream_pass<DUAL, 2, 6>(a, bi, bx, p0, n0, smem, wave, lane);
-        else stream_pass<DUAL, 2, 8>(a, bi, bx, p0, n0, smem, wave, lane);
+        if (td <= 1) stream_pass<DUAL, KS, 1, 1>(a, bi, bx, p0, n0, smem, wave, lane);
+        else if (td == 2) stream_pass<DUAL, KS, 1, 2>(a, bi, bx, p0, n0, smem, wave, lane);
+        else if (td <= 4) stream_pass<DUAL, KS, 1, 4>(a, bi, bx, p0, n0, smem, wave, lane);
+        else if (td <= 6) stream_pass<DUAL, KS, 2, 6>(a, bi, bx, p0, n0, smem, wave, lane);
+        else stream_pass<DUAL, KS, 2, 8>(a, bi, bx, p0, n0, smem, wave, lane);
     }
 }
 
-template <bool DUAL>
-hipError_t launch(const MxArgs &a, hipStream_t s) {
-    constexpr int lds = Cfg<DUAL, 1>::LDS_BYTES > Cfg<DUAL, 2>::LDS_BYTES ? Cfg<DUAL, 1>::LDS_BYTES : Cfg<DUAL, 2>::LDS_BYTES;
+template <bool DUAL, int KS>
+hipError_t launch_ks(const MxArgs &a, hipStream_t s) {
+    using C = Cfg<DUAL, KS, 2>;  // the largest pass's LDS
     static std::atomic<uint64_t> lds_set{0};
-    hipError_t e = lds_opt_in_once((const void *)mx_stream_kernel<DUAL>, lds, lds_set);
+    hipError_t e = lds_opt_in_once((const void *)mx_stream_kernel<DUAL, KS>, C::LDS_BYTES, lds_set);
     if (e != hipSuccess) return e;
-    const dim3 grid((unsigned)(a.N / (32 * Cfg<DUAL, 1>::FT)), (unsigned)a.M);
-    hipLaunchKernelGGL(mx_stream_kernel<DUAL>, grid, dim3(64 * KS), lds, s, a);
+    const dim3 grid((unsigned)(a.N / (32 * C::FT)), (unsigned)a.M);
+    hipLaunchKernelGGL((mx_stream_kernel<DUAL, KS>), grid, dim3(64 * KS), C::LDS_BYTES, s, a);
     return hipGetLastError();
+}
+
+constexpr int64_t kWg1 = 512;  // from here on one wave each
+// Waves per workgroup, by the workgroups that will hold rows (at most one
+// block per pair or, with few rows, per expert).  Measured borders of 256,
+// 512 and 1024 (one MI355X, both stages, one token): 1 expert (4096, 14336)
+// 28, 27, 32 us; 2 of 8 experts 40, 38, 39; 6 of 64 (2048, 1408) 15.5, 16.3,
+// 18.5; 64 tokens over 8 experts 124, 124, 126.
+template <bool DUAL>
+hipError_t launch(const MxArgs &a, int64_t pairs, hipStream_t s) {
+    const int64_t wgs = a.N / (32 * Cfg<DUAL, 1, 2>::FT) * (pairs < a.E ? pairs : a.E);
+    if (wgs >= kWg1) return launch_ks<DUAL, 1>(a, s);
+    if (wgs >= kWg1 / 2) return launch_ks<DUAL, 2>(a, s);
+    return launch_ks<DUAL, 4>(a, s);
 }
 
 }  // namespace
 
-hipError_t launch_mx_stream_gate_up(const MxArgs &a, hipStream_t s) { return launch<true>(a, s); }
-hipError_t launch_mx_stream_down(const MxArgs &a, hipStream_t s) { return launch<false>(a, s); }
+hipError_t launch_mx_stream_gate_up(const MxArgs &a, int64_t pairs, hipStream_t s) { return launch<true>(a, pairs, s); }
+hipError_t launch_mx_stream_down(const MxArgs &a, int64_t pairs, hipStream_t s) { return launch<false>(a, pairs, s); }
 
 }  // namespace rmoe
