@@ -577,12 +577,13 @@ def _call(fn, dev, stream, *args):
     current one) and ``stream``, or that GPU's current stream, as its last
     argument."""
     torch = _torch()
+    bindings = torch._C
     if stream is None:
         # the handle alone: building a Stream object costs as much as a launch
-        handle = torch._C._cuda_getCurrentRawStream(dev)
+        handle = bindings._cuda_getCurrentRawStream(dev)
     else:
         handle = int(getattr(stream, "cuda_stream", stream))
-    if torch.cuda.current_device() == dev:
+    if bindings._cuda_getDevice() == dev:
         st = getattr(lib(), fn)(*args, handle)
     else:
         with torch.cuda.device(dev):
@@ -647,10 +648,15 @@ def quantize_mxfp4(x, codes=None, scales=None, stream=None):
     cs, ss = mxfp4_shapes(shape)
     if codes is None:
         codes = _empty(cs, u8, dev, stream)
+        pc = codes.data_ptr()
+    else:
+        pc = _arg(dev, "codes", codes, u8, *cs)
     if scales is None:
         scales = _empty(ss, u8, dev, stream)
-    _call("rmoe_quantize_mxfp4", dev, stream, px, ty, shape[0] if len(shape) == 3 else 1, shape[-2], shape[-1],
-          _arg(dev, "codes", codes, u8, *cs), _arg(dev, "scales", scales, u8, *ss))
+        ps = scales.data_ptr()
+    else:
+        ps = _arg(dev, "scales", scales, u8, *ss)
+    _call("rmoe_quantize_mxfp4", dev, stream, px, ty, shape[0] if len(shape) == 3 else 1, shape[-2], shape[-1], pc, ps)
     return codes, scales
 
 
@@ -667,8 +673,10 @@ def dequantize_mxfp4(codes, scales, cols: int, dtype=None, out=None, stream=None
     pc, ps = _arg(dev, "codes", codes, u8, *cs), _arg(dev, "scales", scales, u8, *ss)
     if out is None:
         out = _empty(shape, dtype, dev, stream)
-    _call("rmoe_dequantize_mxfp4", dev, stream, pc, ps, ty, shape[0] if len(shape) == 3 else 1, shape[-2], shape[-1],
-          _arg(dev, "out", out, dtype, *shape))
+        po = out.data_ptr()
+    else:
+        po = _arg(dev, "out", out, dtype, *shape)
+    _call("rmoe_dequantize_mxfp4", dev, stream, pc, ps, ty, shape[0] if len(shape) == 3 else 1, shape[-2], shape[-1], po)
     return out
 
 

@@ -877,7 +877,9 @@ int rmoe_down_backward_f16(const void *dout, const void *down_w, const float *rw
     if (st != RMOE_OK) return st;
     st = down_backward_args(&a, dout, down_w, rw, gate, up, gs, go, gpo, gidx, dgate, dup, whidden, scratch, drw);
     if (st != RMOE_OK || num_blocks_m == 0) return st;
-    return to_status(rmoe::launch_down_backward(a, static_cast<hipStream_t>(stream)));
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    st = to_status(rmoe::launch_hidden_grad(a, s));
+    return st != RMOE_OK ? st : to_status(rmoe::launch_drw(a, s));
 }
 
 int rmoe_gate_up_backward_f16(const void *dgate, const void *dup, const void *gate_w, const void *up_w,
@@ -923,9 +925,9 @@ int rmoe_backward_f16(const void *x, const void *dout, const void *gate_w, const
     if (st != RMOE_OK) return st;
     hipStream_t s = static_cast<hipStream_t>(stream);
     if (num_blocks_m > 0) {
-        st = to_status(rmoe::launch_down_backward(a, s));
+        st = to_status(rmoe::launch_hidden_grad(a, s));
         if (st != RMOE_OK) return st;
-        st = to_status(rmoe::launch_gate_up_backward(a, s));
+        st = to_status(rmoe::launch_gate_up_backward(a, s));  // and drw
         if (st != RMOE_OK) return st;
     }
     return to_status(rmoe::launch_weight_grad(a, s));

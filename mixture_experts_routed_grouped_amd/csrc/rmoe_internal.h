@@ -142,8 +142,9 @@ struct TrainArgs {
     int32_t E, M;
 };
 hipError_t launch_gate_up_train(const TrainArgs &a, hipStream_t s);     // yg, yu, yh
-hipError_t launch_down_backward(const TrainArgs &a, hipStream_t s);     // dg, du, hw, drw
-hipError_t launch_gate_up_backward(const TrainArgs &a, hipStream_t s);  // dx
+hipError_t launch_hidden_grad(const TrainArgs &a, hipStream_t s);       // dg, du, hw, part
+hipError_t launch_drw(const TrainArgs &a, hipStream_t s);               // drw from part
+hipError_t launch_gate_up_backward(const TrainArgs &a, hipStream_t s);  // dx, and drw from part if a.drw is given
 hipError_t launch_weight_grad(const TrainArgs &a, hipStream_t s);       // dwg, dwu, dwd
 int64_t weight_grad_tiles(int64_t H, int64_t I, int32_t E);
 

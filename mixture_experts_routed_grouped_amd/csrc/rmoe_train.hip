@@ -431,9 +431,27 @@ struct Rows {
     }
 };
 
+// drw[c] = the sum of c's partial sums, one per 128 columns: 16 lanes per c
+// take every 16th in ascending order, then the lanes are added.
+__device__ __forceinline__ void sum_drw(const TrainArgs &a) {
+    const int64_t n = min((int64_t)a.go[a.E], a.pairs);
+    const int np = (int)(a.I / 128), l = threadIdx.x & 15;
+    for (int64_t c0 = (int64_t)blockIdx.x * 16; c0 < n; c0 += (int64_t)gridDim.x * 16) {
+        const int64_t c = c0 + (threadIdx.x >> 4);
+        float s = 0.f;
+        if (c < n)
+            for (int j = l; j < np; j += 16) s += a.part[c * np + j];
+        s = sum16(s);
+        if (c < n && l == 0) a.drw[c] = s;
+    }
+}
+
+// The dx launch of a whole backward pass also finishes drw (a.drw given): the
+// partial sums are complete, and a launch of its own costs 4 us.
 template <bool HID>
 __global__ __launch_bounds__(256) void rows_kernel(TrainArgs a, int NT) {
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
+    if (!HID && a.drw) sum_drw(a);
     Rows<HID> r(a, smem);
     run_items(r, a.gs, a.gpo, a.gidx, a.E, NT);
 }
@@ -523,21 +541,7 @@ __global__ __launch_bounds__(256) void forward_kernel(TrainArgs a, int NT) {
     run_items(f, a.gs, a.gpo, a.gidx, a.E, NT);
 }
 
-// drw[c] = the sum of c's partial sums in ascending order of their columns:
-// 16 lanes per c, then over the lanes
-__global__ __launch_bounds__(256) void drw_kernel(const float *part, const int32_t *go, int32_t E, int64_t pairs,
-                                                  int np, float *drw) {
-    const int64_t n = min((int64_t)go[E], pairs);
-    const int l = threadIdx.x & 15;
-    for (int64_t c0 = (int64_t)blockIdx.x * 16; c0 < n; c0 += (int64_t)gridDim.x * 16) {
-        const int64_t c = c0 + (threadIdx.x >> 4);
-        float s = 0.f;
-        if (c < n)
-            for (int j = l; j < np; j += 16) s += part[c * np + j];
-        s = sum16(s);
-        if (c < n && l == 0) drw[c] = s;
-    }
-}
+__global__ __launch_bounds__(256) void drw_kernel(TrainArgs a) { sum_drw(a); }
 
 // Weight gradients: every 256 x 256 tile of the three matrices of every
 // expert, its sum over the expert's rows; an expert without rows gets zeros.
@@ -689,14 +693,13 @@ hipError_t launch_gate_up_train(const TrainArgs &a, hipStream_t s) {
     return hipGetLastError();
 }
 
-hipError_t launch_down_backward(const TrainArgs &a, hipStream_t s) {
-    const hipError_t e = launch_rows<true>(a, s);
-    if (e != hipSuccess) return e;
+hipError_t launch_hidden_grad(const TrainArgs &a, hipStream_t s) { return launch_rows<true>(a, s); }
+
+hipError_t launch_drw(const TrainArgs &a, hipStream_t s) {
     int64_t g = (a.pairs + 15) / 16;
     if (g > 256 * 16) g = 256 * 16;  // strides beyond
     if (g == 0) return hipSuccess;
-    hipLaunchKernelGGL(drw_kernel, dim3((unsigned)g), dim3(256), 0, s, a.part, a.go, a.E, a.pairs, (int)(a.I / 128),
-                       a.drw);
+    hipLaunchKernelGGL(drw_kernel, dim3((unsigned)g), dim3(256), 0, s, a);
     return hipGetLastError();
 }
 
