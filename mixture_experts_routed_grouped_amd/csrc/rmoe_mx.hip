@@ -28,11 +28,15 @@ struct Row8<_Float16> {
 #pragma unroll
         for (int i = 0; i < 8; ++i) f[i] = (float)h[i];
     }
-    static __device__ __forceinline__ void put(void *p, int64_t v, const float *f) {
-        h8 h;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) h[i] = (_Float16)f[i];
-        __builtin_nontemporal_store(__builtin_bit_cast(u4, h), (u4 *)p + v);
+    // the values of 8 codes under one scale; nan: NaN instead
+    static __device__ __forceinline__ void put(void *p, int64_t v, unsigned q, float scale, bool nan) {
+        u4 o;
+        o[0] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(q, scale, 0));
+        o[1] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(q, scale, 1));
+        o[2] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(q, scale, 2));
+        o[3] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(q, scale, 3));
+        if (nan) o = u4{0x7e007e00u, 0x7e007e00u, 0x7e007e00u, 0x7e007e00u};
+        __builtin_nontemporal_store(o, (u4 *)p + v);
     }
 };
 struct bf16_t {};
@@ -47,14 +51,13 @@ struct Row8<bf16_t> {
             f[2 * i + 1] = __builtin_bit_cast(float, a[i] & 0xffff0000u);
         }
     }
-    static __device__ __forceinline__ unsigned rne(float f) {  // bf16 bits, round to nearest even, NaN kept
-        const unsigned u = __builtin_bit_cast(unsigned, f);
-        return f != f ? (u >> 16) | 0x40u : (u + 0x7fffu + ((u >> 16) & 1u)) >> 16;
-    }
-    static __device__ __forceinline__ void put(void *p, int64_t v, const float *f) {
+    static __device__ __forceinline__ void put(void *p, int64_t v, unsigned q, float scale, bool nan) {
         u4 o;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] = rne(f[2 * i]) | (rne(f[2 * i + 1]) << 16);
+        o[0] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, scale, 0));
+        o[1] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, scale, 1));
+        o[2] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, scale, 2));
+        o[3] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, scale, 3));
+        if (nan) o = u4{0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u};
         __builtin_nontemporal_store(o, (u4 *)p + v);
     }
 };
@@ -74,15 +77,15 @@ struct Row8<float> {
             f[4 + i] = __builtin_bit_cast(float, y);
         }
     }
-    static __device__ __forceinline__ void put(void *p, int64_t v, const float *f) {
-        u4 x, y;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            x[i] = __builtin_bit_cast(unsigned, f[i]);
-            y[i] = __builtin_bit_cast(unsigned, f[4 + i]);
-        }
-        __builtin_nontemporal_store(x, (u4 *)p + 2 * v);
-        __builtin_nontemporal_store(y, (u4 *)p + 2 * v + 1);
+    static __device__ __forceinline__ void put(void *p, int64_t v, unsigned q, float scale, bool nan) {
+        typedef float f2 __attribute__((ext_vector_type(2)));
+        const f2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, scale, 0), b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, scale, 1);
+        const f2 c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, scale, 2), d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, scale, 3);
+        f4 x = {a.x, a.y, b.x, b.y}, y = {c.x, c.y, d.x, d.y};
+        const float n = __builtin_nanf("");
+        if (nan) x = y = f4{n, n, n, n};
+        __builtin_nontemporal_store(x, (f4 *)p + 2 * v);
+        __builtin_nontemporal_store(y, (f4 *)p + 2 * v + 1);
     }
 };
 
@@ -180,19 +183,9 @@ __global__ __launch_bounds__(256) void dequantize_kernel(const unsigned char *__
         const unsigned row = u / kc, ch = u - row * kc;
         const int64_t v = (int64_t)ch * 32 + l;
         if (v >= vpr) continue;
-        // value = E2M1 number times 2^(byte - 127): exact in fp32 (subnormals
-        // included) before the one rounding to the output type
-        float f[8];
-        const float nan = __builtin_nanf("");
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const unsigned k = (q[i] >> (4 * j)) & 15u;
-            const int m = (int)(k & 7u);  // 2 x magnitude: 0 1 2 3 4 6 8 12
-            const float mag = m < 5 ? (float)m : (m == 5 ? 6.0f : m == 6 ? 8.0f : 12.0f);
-            const float val = __builtin_ldexpf(mag, (int)sb[i] - 128);
-            f[j] = sb[i] == 255u ? nan : (k & 8u) ? -val : val;
-        }
-        Row8<T>::put(y, row * vpr + v, f);
+        // value = E2M1 number times 2^(byte - 127), rounded once to the output
+        // type by the conversion (two values each)
+        Row8<T>::put(y, row * vpr + v, q[i], __builtin_bit_cast(float, sb[i] << 23), sb[i] == 255u);
     }
 }
 
