@@ -88,39 +88,6 @@ __device__ __forceinline__ void dma16_nt(const void *g, unsigned lds) {
                  : "memory", "m0");
 }
 
-// A pointer or number known to be the same in every lane, in scalar registers.
-__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
-template <class T>
-__device__ __forceinline__ const T *uniform(const T *p) {
-    const uint64_t u = (uint64_t)p;
-    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)u), hi = __builtin_amdgcn_readfirstlane((uint32_t)(u >> 32));
-    return (const T *)(((uint64_t)hi << 32) | lo);
-}
-
-// A table that no kernel of the launch writes, in the constant address space:
-// a uniform index reads it with a scalar load, also after stores (which the
-// compiler must otherwise assume may have changed it: such vector loads cost
-// 1-2 k cycles each in a persistent kernel's step to its next item).
-typedef const __attribute__((address_space(4))) int32_t *Table;
-__device__ __forceinline__ Table table(const int32_t *p) { return (Table)(uintptr_t)p; }
-
-// x, as if it were a new value: keeps the compiler from computing what
-// depends on it ahead of a loop, where it would stay live (and spill).
-__device__ __forceinline__ int fresh(int x) {
-    asm volatile("" : "+v"(x));
-    return x;
-}
-
-// One 1 KB global -> LDS DMA addressed as a wave-uniform base plus a 32-bit
-// per-lane byte offset (the scalar-base form of global_load_lds_dwordx4):
-// a K step moves only the base, in scalar registers, so no 64-bit vector
-// address add precedes each DMA (measured 2-3% faster on every workload than
-// full per-lane addresses).  Counted by vmcnt like a load.
-__device__ __forceinline__ void dma16_sb(const void *base, unsigned off, unsigned lds) {
-    asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base)
-                 : "memory", "m0");
-}
-
 // s_waitcnt vmcnt(N) only (expcnt and lgkmcnt left at their no-wait maxima).
 template <int N>
 __device__ __forceinline__ void wait_vm() {

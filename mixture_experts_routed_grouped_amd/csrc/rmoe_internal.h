@@ -23,27 +23,6 @@ inline hipError_t lds_opt_in_once(const void *fn, int bytes, std::atomic<uint64_
     return e;
 }
 
-constexpr int kXcd = 8;  // MI355X: workgroups go round-robin over 8 XCDs
-
-// Workgroup slots of the persistent kernel on the current device: its CU
-// count rounded down to a multiple of 8 (cached per device).
-inline hipError_t persistent_grid(unsigned &grid) {
-    static std::atomic<int> cached[64];
-    int dev = 0;
-    hipError_t e = hipGetDevice(&dev);
-    if (e != hipSuccess) return e;
-    int n = dev < 64 ? cached[dev].load(std::memory_order_relaxed) : 0;
-    if (n == 0) {
-        e = hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev);
-        if (e != hipSuccess) return e;
-        n = n / kXcd * kXcd;
-        if (n < kXcd) n = kXcd;
-        if (dev < 64) cached[dev].store(n, std::memory_order_relaxed);
-    }
-    grid = (unsigned)n;
-    return hipSuccess;
-}
-
 // One stage of the routed expert FFN as the kernels see it: a grouped GEMM
 // Y[r, n] = epilogue( sum_k X[r, k] * W[e(r), n, k] ) over the valid rows r
 // of every 128-row block.  For the gate/up stage W0 = gate_w, W1 = up_w and

@@ -226,16 +226,16 @@ struct Tile {
         const int64_t row0 = (int64_t)(it.bx + wt) * kBlockM;
         const int myrows = rows(it);
         unsigned char *piece[2] = {smem + W_OFF + SLOT + wave * 8192, smem + T_OFF + SLOT + wave * 8192};
-        float w[4] = {0.f, 0.f, 0.f, 0.f};
         const float *rwe = a.rw + table(a.go)[it.e] + it.off + kBlockM * wt;
-#pragma unroll
-        for (int u = 0; u < NTT; ++u)
-            if (32 * u + lr < myrows) w[u] = rwe[32 * u + lr];
         _Float16 *ybase = a.y + row0 * N + (int64_t)it.nt * 256 + 128 * ww;
         const int c = ln & 15;
 #pragma unroll
         for (int u0 = 0; u0 < NTT; u0 += 2) {
             __builtin_amdgcn_sched_barrier(0);  // no accumulator is copied out early: registers
+            float w[2] = {0.f, 0.f};
+#pragma unroll
+            for (int u = u0; u < u0 + 2 && u < NTT; ++u)
+                if (32 * u + lr < myrows) w[u - u0] = rwe[32 * u + lr];
 #pragma unroll
             for (int u = u0; u < u0 + 2 && u < NTT; ++u)
 #pragma unroll
@@ -244,7 +244,8 @@ struct Tile {
                     for (int q = 0; q < 4; ++q) {
                         const f16x &o = acc[t][u];
                         *(h4 *)(piece[u - u0] + lr * 256 + (((4 * t + q) ^ (lr & 15)) << 4) + 8 * lh) = to_h4(
-                            o[4 * q + 0] * w[u], o[4 * q + 1] * w[u], o[4 * q + 2] * w[u], o[4 * q + 3] * w[u]);
+                            o[4 * q + 0] * w[u - u0], o[4 * q + 1] * w[u - u0], o[4 * q + 2] * w[u - u0],
+                            o[4 * q + 3] * w[u - u0]);
                     }
             __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): this wave's staging writes are done
 #pragma unroll
@@ -285,7 +286,7 @@ __global__ __launch_bounds__(256) void mx_tile_kernel(MxArgs a, int NT) {
 template <bool DUAL>
 hipError_t launch(const MxArgs &a, int NT, hipStream_t s) {
     unsigned grid = 0;
-    hipError_t e = persistent_grid(grid);
+    hipError_t e = cu_grid(grid);
     if (e != hipSuccess) return e;
     static std::atomic<uint64_t> lds_set{0};
     e = lds_opt_in_once((const void *)mx_tile_kernel<DUAL>, LDS_BYTES, lds_set);

@@ -52,16 +52,11 @@ struct TileCursor {
     int e = 0, base = 0;
 };
 
-// The tables are read through any pointer to int32 (the kernels may pass one
-// of the constant address space, whose loads are scalar).
-template <class Tab>
-RMOE_HD int live_blocks(Tab gs, int e) { return (gs[e] + kItemRows - 1) / kItemRows; }
-template <class Tab>
-RMOE_HD int entries_of(Tab gs, int e) { return (live_blocks(gs, e) + 1) / 2; }
+RMOE_HD int live_blocks(const int32_t *gs, int e) { return (gs[e] + kItemRows - 1) / kItemRows; }
+RMOE_HD int entries_of(const int32_t *gs, int e) { return (live_blocks(gs, e) + 1) / 2; }
 
 // The part of locality group grp (of ngrp).
-template <class Tab>
-RMOE_HD TileSeq tile_seq(Tab gs, int E, int NT, int grp, int ngrp) {
+RMOE_HD TileSeq tile_seq(const int32_t *gs, int E, int NT, int grp, int ngrp) {
     TileSeq s;
     s.NT = NT;
     s.P = 0;
@@ -76,8 +71,7 @@ RMOE_HD TileSeq tile_seq(Tab gs, int E, int NT, int grp, int ngrp) {
 // Item i of the group's part.  The cursor only moves forward while i does
 // (and starts over when the entry index steps back, at a new rectangle), so
 // a workgroup's walk over the experts is amortised over its items.
-template <class Tab>
-RMOE_HD TileItem tile_item(Tab gs, Tab gpo, const TileSeq &s, int i, TileCursor &c) {
+RMOE_HD TileItem tile_item(const int32_t *gs, const int32_t *gpo, const TileSeq &s, int i, TileCursor &c) {
     TileItem it;
     const int q = s.lo + i;
     const int gsz = RMOE_TILE_GROUP * s.P;

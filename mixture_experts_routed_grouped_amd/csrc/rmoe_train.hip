@@ -670,7 +670,7 @@ __global__ __launch_bounds__(256) void cols_kernel(TrainArgs a, int total) {
 template <bool HID>
 hipError_t launch_rows(const TrainArgs &a, hipStream_t s) {
     unsigned grid = 0;
-    hipError_t e = persistent_grid(grid);
+    hipError_t e = cu_grid(grid);
     if (e != hipSuccess) return e;
     static std::atomic<uint64_t> lds_set{0};
     e = lds_opt_in_once((const void *)rows_kernel<HID>, LDS_BYTES, lds_set);
@@ -684,7 +684,7 @@ hipError_t launch_rows(const TrainArgs &a, hipStream_t s) {
 
 hipError_t launch_gate_up_train(const TrainArgs &a, hipStream_t s) {
     unsigned grid = 0;
-    hipError_t e = persistent_grid(grid);
+    hipError_t e = cu_grid(grid);
     if (e != hipSuccess) return e;
     static std::atomic<uint64_t> lds_set{0};
     e = lds_opt_in_once((const void *)forward_kernel, LDS_BYTES, lds_set);
@@ -714,7 +714,7 @@ hipError_t launch_weight_grad(const TrainArgs &a, hipStream_t s) {
     hipError_t e = lds_opt_in_once((const void *)cols_kernel, LDS_BYTES, lds_set);
     if (e != hipSuccess) return e;
     unsigned grid = 0;
-    e = persistent_grid(grid);
+    e = cu_grid(grid);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(cols_kernel, dim3(grid), dim3(256), LDS_BYTES, s, a,
                        (int)weight_grad_tiles(a.H, a.I, a.E));
