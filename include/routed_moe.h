@@ -470,8 +470,8 @@ RMOE_API int rmoe_quantize_mxfp4(const void *x, int32_t type, int64_t batch, int
 
 /*
  * The inverse: y [batch, rows, cols] of element type RMOE_TYPE_* = the values
- * the codes stand for, rounded once to the type (exact in fp32; in fp16 a
- * value above 65504 becomes an infinity).  Blocks with scale byte 255 give
+ * the codes stand for, rounded once to the type (exact in fp32; a value
+ * beyond the type's range becomes an infinity).  Blocks with scale byte 255 give
  * NaN.  Sizes, alignment (y as x) and errors as rmoe_quantize_mxfp4.
  */
 RMOE_API int rmoe_dequantize_mxfp4(const void *codes, const void *scales, int32_t type, int64_t batch,
@@ -568,7 +568,8 @@ RMOE_API int rmoe_gate_up_train_f16(const void *stacked_expert_tokens, const voi
  * Products accumulate in fp32, in an order fixed by the shapes and tables
  * (no atomics): equal calls give equal bits.
  * x [Tp, H]: the stacked token rows of the forward; gate, up: what
- * rmoe_gate_up_train_f16 kept.  dgate may be gate's own memory and dup up's;
+ * rmoe_gate_up_train_f16 kept (infinities, values beyond fp16's range, count
+ * as its largest numbers).  dgate may be gate's own memory and dup up's;
  * other overlaps are not allowed.  scratch: rmoe_backward_scratch_bytes(
  * pairs, I) bytes, contents irrelevant on entry.  Padding rows of dgate, dup,
  * whidden and dx are not written, padding rows of the inputs may hold

@@ -66,8 +66,7 @@ inline hipError_t cu_grid(unsigned &grid) {
     return hipSuccess;
 }
 
-// A pointer or number known to be the same in every lane, in scalar registers.
-__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+// A pointer known to be the same in every lane, in scalar registers.
 template <class T>
 __device__ __forceinline__ const T *uniform(const T *p) {
     const uint64_t u = (uint64_t)p;
@@ -98,8 +97,6 @@ __device__ __forceinline__ void dma16_sb(const void *base, unsigned off, unsigne
     asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base)
                  : "memory", "m0");
 }
-
-constexpr int kSub = 4;  // sub-steps per K step
 
 template <class P>
 constexpr int kPart = (P::DMAS + P::PARTS - 1) / P::PARTS;  // DMAs of a group's part

@@ -1,6 +1,9 @@
 // MXFP4 quantisation, its inverse, and the token pack that quantises on the
 // way (format: rmoe_mx.h).  Bound by HBM: a row is read once and its codes
-// (4.25 bits per element with the scales) are written once.
+// (4.25 bits per element with the scales) are written once.  470 M bf16
+// elements (8 x 14336 x 4096): 215 us to quantise (5.5 TB/s), 175 us back
+// (6.8 TB/s); the large layer's pack (16384 tokens of 7168 to 8 rows each)
+// 205 us (3.6 TB/s).  Small calls are bound by their launch.
 //
 // A half-wave takes one chunk of 256 elements of one row: 8 elements per
 // lane (16-byte loads for fp16 and bf16, two for fp32), 4 lanes per block.
@@ -130,29 +133,30 @@ __global__ __launch_bounds__(256) void quantize_kernel(const void *__restrict__ 
                                                        unsigned char *__restrict__ scales) {
     const unsigned half = threadIdx.x >> 5, l = threadIdx.x & 31;
     const unsigned stride = gridDim.x * 8u;
-    const unsigned u0 = blockIdx.x * 8u + half;
     const int64_t vpr = cols / 8;  // 8-element vectors per row
-    Row8<T> v[U];
-    unsigned row[U], ch[U];
+    for (unsigned u0 = blockIdx.x * 8u + half; u0 < units; u0 += U * stride) {
+        Row8<T> v[U];
+        unsigned row[U], ch[U];
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
-        const unsigned u = u0 + i * stride;
-        row[i] = u / kc;
-        ch[i] = u - row[i] * kc;
-        v[i] = Row8<T>{};
-        if (u < units && (int64_t)ch[i] * 32 + l < vpr) v[i].load(x, row[i] * vpr + (int64_t)ch[i] * 32 + l);
-    }
+        for (int i = 0; i < U; ++i) {
+            const unsigned u = u0 + i * stride;
+            row[i] = u / kc;
+            ch[i] = u - row[i] * kc;
+            v[i] = Row8<T>{};
+            if (u < units && (int64_t)ch[i] * 32 + l < vpr) v[i].load(x, row[i] * vpr + (int64_t)ch[i] * 32 + l);
+        }
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
-        const unsigned u = u0 + i * stride;
-        float f[8];
-        v[i].get(f);
-        const Chunk c = quantize_chunk(f);
-        if (u >= units) continue;
-        *(unsigned *)(codes + ((int64_t)u * kMxChunkBytes + 4 * l)) = c.codes;
-        if ((l & ~4u) == 0) {
-            const unsigned b = row[i] / rpb, r = row[i] - b * rpb;
-            *(unsigned *)(scales + (((int64_t)b * kc + ch[i]) * rpb + r) * 8 + l) = c.scales;
+        for (int i = 0; i < U; ++i) {
+            const unsigned u = u0 + i * stride;
+            float f[8];
+            v[i].get(f);
+            const Chunk c = quantize_chunk(f);
+            if (u >= units) continue;
+            *(unsigned *)(codes + ((int64_t)u * kMxChunkBytes + 4 * l)) = c.codes;
+            if ((l & ~4u) == 0) {
+                const unsigned b = row[i] / rpb, r = row[i] - b * rpb;
+                *(unsigned *)(scales + (((int64_t)b * kc + ch[i]) * rpb + r) * 8 + l) = c.scales;
+            }
         }
     }
 }
@@ -163,29 +167,30 @@ __global__ __launch_bounds__(256) void dequantize_kernel(const unsigned char *__
                                                          unsigned kc, unsigned rpb, int64_t cols, void *__restrict__ y) {
     const unsigned half = threadIdx.x >> 5, l = threadIdx.x & 31;
     const unsigned stride = gridDim.x * 8u;
-    const unsigned u0 = blockIdx.x * 8u + half;
     const int64_t vpr = cols / 8;
-    unsigned q[U], sb[U];
+    for (unsigned u0 = blockIdx.x * 8u + half; u0 < units; u0 += U * stride) {
+        unsigned q[U], sb[U];
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
-        const unsigned u = u0 + i * stride;
-        q[i] = sb[i] = 0;
-        if (u < units) {
-            const unsigned row = u / kc, ch = u - row * kc, b = row / rpb, r = row - b * rpb;
-            q[i] = __builtin_nontemporal_load((const unsigned *)(codes + ((int64_t)u * kMxChunkBytes + 4 * l)));
-            sb[i] = scales[(((int64_t)b * kc + ch) * rpb + r) * 8 + mx_pos(l >> 2)];
+        for (int i = 0; i < U; ++i) {
+            const unsigned u = u0 + i * stride;
+            q[i] = sb[i] = 0;
+            if (u < units) {
+                const unsigned row = u / kc, ch = u - row * kc, b = row / rpb, r = row - b * rpb;
+                q[i] = __builtin_nontemporal_load((const unsigned *)(codes + ((int64_t)u * kMxChunkBytes + 4 * l)));
+                sb[i] = scales[(((int64_t)b * kc + ch) * rpb + r) * 8 + mx_pos(l >> 2)];
+            }
         }
-    }
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
-        const unsigned u = u0 + i * stride;
-        if (u >= units) continue;
-        const unsigned row = u / kc, ch = u - row * kc;
-        const int64_t v = (int64_t)ch * 32 + l;
-        if (v >= vpr) continue;
-        // value = E2M1 number times 2^(byte - 127), rounded once to the output
-        // type by the conversion (two values each)
-        Row8<T>::put(y, row * vpr + v, q[i], __builtin_bit_cast(float, sb[i] << 23), sb[i] == 255u);
+        for (int i = 0; i < U; ++i) {
+            const unsigned u = u0 + i * stride;
+            if (u >= units) continue;
+            const unsigned row = u / kc, ch = u - row * kc;
+            const int64_t v = (int64_t)ch * 32 + l;
+            if (v >= vpr) continue;
+            // value = E2M1 number times 2^(byte - 127), rounded once to the
+            // output type by the conversion (two values each)
+            Row8<T>::put(y, row * vpr + v, q[i], __builtin_bit_cast(float, sb[i] << 23), sb[i] == 255u);
+        }
     }
 }
 
@@ -227,11 +232,13 @@ __global__ __launch_bounds__(256) void pack_mx_kernel(const _Float16 *__restrict
 }
 
 // units per half-wave: 4 once every CU has several waves of work, else 1 so
-// that a small call spreads over the chip
+// that a small call spreads over the chip (expert weights of 470 M elements
+// there and back: 472 us with 4, 486 with 1, 480 with 8); at most 2^20
+// workgroups, which stride beyond
 constexpr int64_t kMxWideUnits = 256 * 8 * 16;
 unsigned grid_units(int64_t units, int per) {
     const int64_t g = (units + 8 * per - 1) / (8 * per);
-    return (unsigned)(g < 1 ? 1 : g);
+    return (unsigned)(g < 1 ? 1 : g > (1 << 20) ? 1 << 20 : g);
 }
 
 template <typename T>

@@ -123,6 +123,21 @@ def test_quantize_past_32_bit_offsets():
     assert torch.count_nonzero(back.view(torch.int32).any(1)) == len(some)
 
 
+def test_quantize_many_short_rows():
+    """More rows than one pass of the largest grid takes (2^20 workgroups of
+    32 rows), 8 elements each: rows before, at and behind the border."""
+    rows = (1 << 25) + 70
+    x = torch.zeros((rows, 8), dtype=torch.float16, device="cuda")
+    some = [0, 31, 32, (1 << 23) - 1, 1 << 23, (1 << 25) - 1, 1 << 25, rows - 1]
+    v = torch.randn((len(some), 8), generator=torch.Generator().manual_seed(4)).half()
+    x[some] = v.cuda()
+    codes, scales = R.quantize_mxfp4(x)
+    back = R.dequantize_mxfp4(codes, scales, 8)
+    torch.cuda.synchronize()
+    assert np.array_equal(_np(back[some]), MX.quantized_values(v.double().numpy()))
+    assert int((back != 0).any(1).sum()) == len(some)
+
+
 # -------------------------------------------------------------------- pack
 @pytest.mark.parametrize("T,k,H", [(1, 1, 8), (5, 3, 264), (130, 2, 512), (700, 8, 1408)])
 def test_pack(T, k, H):
@@ -269,6 +284,32 @@ def test_stages(counts, H, I, variant):
     _down(d, variant)
     torch.cuda.synchronize()
     _check(d)
+
+
+@pytest.mark.parametrize("H,I", [(1 << 20, 128), (128, 1 << 20)])
+def test_maximum_hidden_and_intermediate(H, I):
+    """The largest H and I that the entries take, three rows over two experts:
+    both families' out rows against 64 bits on the codes that each stored."""
+    print(f"[mx] H={H} I={I}", flush=True)
+    d = _case([1, 2], H, I, seed=1)
+    val = lambda c, s, cols: R.dequantize_mxfp4(c.contiguous(), s.contiguous(), cols, dtype=torch.float32).double()  # noqa: E731
+    for variant in ("stream", "tile"):
+        _gate_up(d, variant)
+        _down(d, variant)
+        torch.cuda.synchronize()
+        for e, n in enumerate(d["counts"]):
+            p, q = int(d["c"]["group_padded_offsets"][e]), int(d["c"]["group_offsets"][e])
+            rows = slice(p, p + n)
+            x = val(d["codes"][rows], d["scales"][:, rows], H)
+            g, u = x @ val(d["wg"][0][e], d["wg"][1][e], H).T, x @ val(d["wu"][0][e], d["wu"][1][e], H).T
+            h, hq = g * torch.sigmoid(g) * u, val(d["hc"][rows], d["hs"][:, rows], I)
+            top = h.abs().view(n, -1, 32).amax(-1).repeat_interleave(32, 1)
+            # half of E2M1's widest step, or the clamp at 6, of a maximum in [4, 8)
+            assert ((hq - h).abs() <= top * 0.5 * (1 + 2.0 ** -10)).all(), (variant, e)
+            wd, w = val(d["wd"][0][e], d["wd"][1][e], I), d["rw"][q:q + n].double()[:, None]
+            y, ey = (hq @ wd.T) * w, I * 2.0 ** -23 * (hq.abs() @ wd.abs().T) * w
+            bound = ey + (y.abs() + ey) * (F16_HALF_STEP + 2.0 ** -23) + 2.0 ** -25
+            assert ((d["out"][rows].double() - y).abs() <= bound).all(), (variant, e)
 
 
 @pytest.mark.parametrize("variant", ["stream", "tile", "auto"])

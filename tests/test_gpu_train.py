@@ -240,6 +240,7 @@ def test_extreme_gates():
     torch.cuda.synchronize()
     r = d["rows"]
     keep = (d["dgate"], d["dup"], d["whidden"])
+    kept = {n: d[n][r].clone() for n in ("dgate", "dup", "whidden", "gate", "up")}
     fin = torch.isfinite
     ok = fin(keep[0][r]) & fin(keep[2][r])
     assert ok.all()
@@ -251,6 +252,71 @@ def test_extreme_gates():
     s = torch.sigmoid(gg)
     _near(d["dgate"][r], dg, u.abs() * w[:, None] * (s + (gg * s).abs() * (1 - s)) * (eb + (b.abs() + eb) * FN), "dgate")
     _near(d["whidden"][r], hw, hw.abs() * FN, "whidden")
+    # a gate or up row that left fp16's range counts as the largest number
+    inf = torch.full_like(d["gate"][r], float("inf"))
+    for n in ("gate", "up"):
+        d[n][r] = torch.where(kept[n].abs() == 65504, torch.copysign(inf, kept[n]), kept[n])
+    assert torch.isinf(d["gate"][r]).any()
+    _backward(d)
+    torch.cuda.synchronize()
+    for n in ("dgate", "dup", "whidden"):
+        assert torch.equal(d[n][r], kept[n]), n
+    d["gate"][int(r[3])] = float("nan")               # and NaN stays NaN
+    _backward(d)
+    torch.cuda.synchronize()
+    assert torch.isnan(d["dgate"][int(r[3])]).all() and not torch.isnan(d["dgate"][int(r[4])]).any()
+
+
+def test_pairs_left_out_by_the_contract():
+    """Pairs with an expert id out of range have no row and no compact place:
+    the places past the last valid pair keep what they held."""
+    T, k, E, H, I = 30, 2, 4, 128, 128
+    g = torch.Generator(device="cuda").manual_seed(3)
+    ids = torch.randint(0, E, (T, k), generator=g, device="cuda", dtype=torch.int32)   # repeats allowed
+    ids[5, 1], ids[20, 0] = E, -1
+    t = R.build_contract_device(ids, E)
+    Tp, pairs = t["total_padded_tokens"], t["pairs"]
+    tables = (t["group_sizes"], t["group_offsets"], t["group_padded_offsets"], t["group_idx_for_bx"])
+    rnd = lambda *s: torch.randn(s, generator=g, device="cuda").half()  # noqa: E731
+    bits = lambda *s: torch.full(s, BITS, dtype=torch.int16, device="cuda").view(torch.float16)  # noqa: E731
+    w, prow = torch.full((pairs,), float("nan"), device="cuda"), t["padded_row_of_pair"]
+    xs, dys = bits(Tp, H), bits(Tp, H)
+    for src, dst in ((rnd(T, H), xs), (rnd(T, H), dys)):
+        R.pack(src, torch.rand(pairs, generator=g, device="cuda"), prow, t["compact_pos_of_pair"], dst, w)
+    d = {"c": R.build_contract(ids.cpu().clamp(0, E - 1).numpy(), E), "E": E, "H": H, "I": I, "Tp": Tp, "pairs": pairs}
+    torch.cuda.synchronize()
+    sizes, offsets, starts = (x.cpu().numpy() for x in tables[:3])
+    d["c"] = {"group_padded_offsets": starts, "group_offsets": offsets}
+    d["counts"] = sizes.tolist()
+    assert sum(d["counts"]) == pairs - 2
+    d.update(x=xs, dout=dys, wg=rnd(E, I, H), wu=rnd(E, I, H), wd=rnd(E, H, I), rw=w, gs=tables[0], go=tables[1],
+             gpo=tables[2], gidx=tables[3])
+    for n in ("gate", "up", "hidden", "dgate", "dup", "whidden"):
+        d[n] = bits(Tp, I)
+    d["dx"], d["dgw"], d["duw"], d["ddw"] = bits(Tp, H), bits(E, I, H), bits(E, I, H), bits(E, H, I)
+    d["drw"] = torch.full((pairs,), -7.0, device="cuda")
+    d["scratch"] = torch.full((R.backward_scratch_bytes(pairs, I) // 4,), float("nan"), device="cuda")
+    _forward(d)
+    torch.cuda.synchronize()
+    _check_forward(d)
+    _backward(d)
+    torch.cuda.synchronize()
+    _check_backward(d)
+    _untouched(d, ["dgate", "dup", "whidden", "dx"])
+    assert (d["drw"][-2:] == -7.0).all()
+
+
+@pytest.mark.parametrize("H,I", [(1 << 20, 128), (128, 1 << 20)])
+def test_maximum_hidden_and_intermediate(H, I):
+    """The largest H and I that the entries take, three rows over two experts."""
+    print(f"[train] H={H} I={I}", flush=True)
+    d = _case([1, 2], H, I, seed=1)
+    _forward(d)
+    torch.cuda.synchronize()
+    _check_forward(d)
+    _backward(d)
+    torch.cuda.synchronize()
+    _check_backward(d)
 
 
 def test_corrupted_tables_read_nothing_out_of_bounds():
