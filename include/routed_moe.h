@@ -578,9 +578,8 @@ RMOE_API int rmoe_gate_up_train_f16(const void *stacked_expert_tokens, const voi
  * rmoe_combine_f16 of dx.
  * H, I multiples of 128; fp16 pointers 16-byte, others 4-byte aligned; at
  * most 2^23 weight-gradient tiles, 3 E ceil(H/256) ceil(I/256)
- * (RMOE_ERR_UNSUPPORTED_SHAPE).  rmoe_backward_f16 runs the three stages
- * below in this order, in three launches on `stream` (drw is finished by the
- * second one's).
+ * (RMOE_ERR_UNSUPPORTED_SHAPE).  rmoe_backward_f16 gives the three stages'
+ * results below, bit for bit, in two launches on `stream`.
  */
 RMOE_API size_t rmoe_backward_scratch_bytes(int64_t num_pairs, int64_t intermediate);
 RMOE_API int rmoe_backward_f16(const void *x, const void *dout, const void *gate_w, const void *up_w,

@@ -924,13 +924,9 @@ int rmoe_backward_f16(const void *x, const void *dout, const void *gate_w, const
     st = weight_grad_args(&a, x, dout, dgate, dup, whidden, gs, gpo, dgate_w, dup_w, ddown_w);
     if (st != RMOE_OK) return st;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    if (num_blocks_m > 0) {
-        st = to_status(rmoe::launch_hidden_grad(a, s));
-        if (st != RMOE_OK) return st;
-        st = to_status(rmoe::launch_gate_up_backward(a, s));  // and drw
-        if (st != RMOE_OK) return st;
-    }
-    return to_status(rmoe::launch_weight_grad(a, s));
+    if (num_blocks_m == 0) return to_status(rmoe::launch_weight_grad(a, s));
+    st = to_status(rmoe::launch_hidden_grad(a, s));
+    return st != RMOE_OK ? st : to_status(rmoe::launch_grads(a, s));
 }
 
 }  // extern "C"

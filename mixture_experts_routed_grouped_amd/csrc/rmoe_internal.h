@@ -123,8 +123,9 @@ struct TrainArgs {
 hipError_t launch_gate_up_train(const TrainArgs &a, hipStream_t s);     // yg, yu, yh
 hipError_t launch_hidden_grad(const TrainArgs &a, hipStream_t s);       // dg, du, hw, part
 hipError_t launch_drw(const TrainArgs &a, hipStream_t s);               // drw from part
-hipError_t launch_gate_up_backward(const TrainArgs &a, hipStream_t s);  // dx, and drw from part if a.drw is given
+hipError_t launch_gate_up_backward(const TrainArgs &a, hipStream_t s);  // dx
 hipError_t launch_weight_grad(const TrainArgs &a, hipStream_t s);       // dwg, dwu, dwd
+hipError_t launch_grads(const TrainArgs &a, hipStream_t s);             // the last three in one launch
 int64_t weight_grad_tiles(int64_t H, int64_t I, int32_t E);
 
 // Words of the static scratch the allocation-free contract build uses

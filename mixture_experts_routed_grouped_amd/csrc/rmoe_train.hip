@@ -459,12 +459,9 @@ __device__ __forceinline__ void sum_drw(const TrainArgs &a) {
     }
 }
 
-// The dx launch of a whole backward pass also finishes drw (a.drw given): the
-// partial sums are complete, and a launch of its own costs 4 us.
 template <bool HID>
 __global__ __launch_bounds__(256) void rows_kernel(TrainArgs a, int NT) {
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
-    if (!HID && a.drw) sum_drw(a);
     Rows<HID> r(a, smem);
     run_items(r, a.gs, a.gpo, a.gidx, a.E, NT);
 }
@@ -637,23 +634,29 @@ struct Cols {
     }
 };
 
-__global__ __launch_bounds__(256) void cols_kernel(TrainArgs a, int total) {
-    extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
+// The tiles of one workgroup.  An XCD's list is dealt to its workgroups round
+// robin; where workgroups busy, busy + 1, ... are free while the first `busy`
+// finish other work that takes as long as `lead` tiles, they first share
+// lead * (their number) tiles among themselves.
+__device__ __forceinline__ void run_cols(const TrainArgs &a, unsigned char *smem, int total, int busy, int lead) {
     Cols c(a, smem);
-    const int xcd = blockIdx.x % kXcd, nl = gridDim.x / kXcd;
-    int j = blockIdx.x / kXcd;  // position in this XCD's list
+    const int xcd = blockIdx.x % kXcd, nl = gridDim.x / kXcd, me = blockIdx.x / kXcd;
+    const int head = lead * (nl - busy);
+    bool ahead = head > 0 && me >= busy;
+    int j = ahead ? me - busy : head + me;  // position in this XCD's list
     // the next tile whose expert holds rows; the zeros of the others on the way
     auto advance = [&](Cols::Tile &t) __attribute__((always_inline)) {
-        for (;; j += nl) {
-            const int item = (j / 32 * kXcd + xcd) * 32 + j % 32;
-            if (j / 32 * kXcd * 32 >= total) return false;
-            if (item >= total || !c.at(item, t)) continue;
-            if (t.n == 0) {
-                c.zeros(t);
-                continue;
+        for (;;) {
+            if (ahead && j >= head) {
+                ahead = false;
+                j = head + me;
             }
-            j += nl;
-            return true;
+            const int run = j / 32 * kXcd * 32, item = run + xcd * 32 + j % 32;
+            if (run >= total) return false;
+            j += ahead ? nl - busy : nl;
+            if (item >= total || !c.at(item, t)) continue;
+            if (t.n > 0) return true;
+            c.zeros(t);
         }
     };
     Cols::Tile t;
@@ -678,6 +681,37 @@ __global__ __launch_bounds__(256) void cols_kernel(TrainArgs a, int total) {
         else
             krun<0>(c.p, newer, finish);
     }
+}
+
+__global__ __launch_bounds__(256) void cols_kernel(TrainArgs a, int total) {
+    extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
+    run_cols(a, smem, total, 0, 0);
+}
+
+// The rest of a whole backward pass in one launch: drw, dx, and the weight
+// gradients, which need nothing from dx.  dx has few, long items (8 experts
+// of 4096 x 14336, 8192 rows: 592 of 448 K steps for 256 workgroups, 2.3
+// rounds, 23% of its launch idle): the workgroups that have one item fewer
+// than the others of their XCD start on the weight gradients meanwhile, as
+// many tiles as an item's K steps are certainly worth: tiles of the expert
+// with the most rows (by the average, the start ran late on 64 uneven experts,
+// 2% of their pass).  6 steps stand for what surrounds a K loop.
+// Against the two launches: 9 tokens of 256 x 128 27.6 -> 20.6 us, the 8192 rows
+// above 5935 -> 5825 (6030 with the free workgroups waiting), 64 experts equal.
+__global__ __launch_bounds__(256) void grads_kernel(TrainArgs a, int NT, int total) {
+    extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
+    sum_drw(a);
+    const ItemWalk walk(a.gs, a.gpo, a.gidx, a.E, NT);
+    const int nl = gridDim.x / kXcd, items = walk.end - walk.i + (int)(blockIdx.x / kXcd);  // of this XCD
+    {
+        Rows<false> r(a, smem);
+        run_items(r, a.gs, a.gpo, a.gidx, a.E, NT);
+    }
+    __syncthreads();
+    int most = 0;
+    for (int e = 0; e < a.E; ++e) most = max(most, (int)table(a.gs)[e]);
+    const int busy = items > 0 ? items % nl : 0;
+    run_cols(a, smem, total, busy, busy ? ((int)(2 * a.I / BK) + 6) / (most / BK + 6) : 0);
 }
 
 template <bool HID>
@@ -730,6 +764,18 @@ hipError_t launch_weight_grad(const TrainArgs &a, hipStream_t s) {
     e = cu_grid(grid);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(cols_kernel, dim3(grid), dim3(256), LDS_BYTES, s, a,
+                       (int)weight_grad_tiles(a.H, a.I, a.E));
+    return hipGetLastError();
+}
+
+hipError_t launch_grads(const TrainArgs &a, hipStream_t s) {
+    static std::atomic<uint64_t> lds_set{0};
+    hipError_t e = lds_opt_in_once((const void *)grads_kernel, LDS_BYTES, lds_set);
+    if (e != hipSuccess) return e;
+    unsigned grid = 0;
+    e = cu_grid(grid);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(grads_kernel, dim3(grid), dim3(256), LDS_BYTES, s, a, (int)((a.H + 255) / 256),
                        (int)weight_grad_tiles(a.H, a.I, a.E));
     return hipGetLastError();
 }

@@ -182,8 +182,14 @@ def test_in_place_and_equal_bits():
     assert torch.equal(d["drw"], drw)
 
 
-def test_stages_are_the_whole():
-    d = _case([33, 140], 256, 384, seed=3)
+# two items of 256 rows; few long items, so that most workgroups start on the
+# weight gradients while the others work on dx; more items than workgroups and
+# a last, partly free round of them; uneven and empty groups
+@pytest.mark.parametrize("counts,H,I", [([33, 140], 256, 384), ([700, 600, 700, 500], 1024, 4096),
+                                        ([2000, 0, 30, 900, 6000], 2048, 8192), ([0, 0, 3, 0], 384, 1152),
+                                        ([1] * 40, 512, 512)])
+def test_stages_are_the_whole(counts, H, I):
+    d = _case(counts, H, I, seed=3)
     _forward(d)
     _backward(d)
     torch.cuda.synchronize()
