@@ -789,7 +789,7 @@ bool all4(T... p) {
     return (aligned4(p) && ...);
 }
 
-constexpr int64_t kMaxGradTiles = (int64_t)1 << 23;  // one workgroup each, within the grid's limit
+constexpr int64_t kMaxGradTiles = (int64_t)1 << 23;  // their positions are ints
 
 int check_train_dims(rmoe::TrainArgs *a, int64_t hidden, int64_t intermediate, int32_t E, int64_t Tp, int64_t pairs,
                      int32_t M) {
