@@ -88,16 +88,6 @@ __device__ __forceinline__ int fresh(int x) {
     return x;
 }
 
-// One 1 KB global -> LDS DMA addressed as a wave-uniform base plus a 32-bit
-// per-lane byte offset (the scalar-base form of global_load_lds_dwordx4):
-// a K step moves only the base, in scalar registers, so no 64-bit vector
-// address add precedes each DMA (measured 2-3% faster on every workload than
-// full per-lane addresses).  Counted by vmcnt like a load.
-__device__ __forceinline__ void dma16_sb(const void *base, unsigned off, unsigned lds) {
-    asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base)
-                 : "memory", "m0");
-}
-
 template <class P>
 constexpr int kPart = (P::DMAS + P::PARTS - 1) / P::PARTS;  // DMAs of a group's part
 

@@ -34,7 +34,7 @@ constexpr int TILE_ALL = TILE_B + SCALE_B;
 
 // 256-byte DMA: lane i stores the dword at g to LDS byte lds + 4 i
 __device__ __forceinline__ void dma4(const void *g, unsigned lds) {
-    asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dword %1, off" ::"s"(lds), "v"(g) : "memory", "m0");
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(lds), "v"(g) : "memory", "m0");
 }
 
 template <bool DUAL, int KS, int TT>

@@ -64,16 +64,6 @@ constexpr int kCpolSc1 = 16;  // cache-policy operand of the buffer builtins: sc
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 static_assert(kItemRows == kBlockM, "work items are contract blocks");
 
-// One 1 KB global -> LDS DMA addressed as a wave-uniform base plus a 32-bit
-// per-lane byte offset (the scalar-base form of global_load_lds_dwordx4):
-// a K step moves only the base, in scalar registers, so no 64-bit vector
-// address add precedes each DMA (measured 2-3% faster on every workload than
-// full per-lane addresses).  Counted by vmcnt like a load.
-__device__ __forceinline__ void dma16_sb(const void *base, unsigned off, unsigned lds) {
-    asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base)
-                 : "memory", "m0");
-}
-
 // ---- Phase timing, compiled only into the diagnostic library
 //      (RMOE_PHASE_TIMING=1: librmoe_phase.so).  Each workgroup of a
 //      persistent launch sums the shader-clock ticks (s_memtime) that its
