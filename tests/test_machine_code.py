@@ -2,14 +2,17 @@
 hardware does not provide by itself.
 
 The LDS DMAs are written in inline assembly, whose inside the compiler's
-hazard pass does not see.  This rule of the instruction set concerns them:
+hazard pass does not see.  Two rules of the instruction set concern them:
 
   * a scalar write of M0 needs one wait state before a load whose
-    destination is LDS (the load takes its LDS address from M0).
+    destination is LDS (the load takes its LDS address from M0);
+  * a scalar register that a vector instruction has written (a read lane, a
+    comparison's mask) needs five before a memory instruction reads it.
 
 Every instruction between two others is one wait state, `s_nop n` is n + 1.
 """
 import os
+import re
 import shutil
 import struct
 import subprocess
@@ -84,3 +87,42 @@ def test_m0_settles_before_an_lds_dma(kernels):
             if operands[0] == "m0" and _to_lds(after):
                 bad.append((fn, name, after))
     assert not bad, f"{len(bad)} loads right behind the write of M0, the first in {bad[0]}"
+
+
+def _scalars(operand):
+    """Numbers of the scalar registers that an operand names (vcc as -1)."""
+    if operand.startswith("vcc"):
+        return {-1}
+    m = re.match(r"s\[(\d+):(\d+)\]|s(\d+)\b", operand)
+    if not m:
+        return set()
+    return {int(m[3])} if m[3] else set(range(int(m[1]), int(m[2]) + 1))
+
+
+def _vector_writes(name, operands):
+    """Scalar registers that a vector instruction writes."""
+    if name.startswith(("v_readlane", "v_readfirstlane", "v_cmp_")):
+        return _scalars(operands[0])
+    if "_co_" in name or name.startswith("v_div_scale"):
+        return _scalars(operands[1])
+    return set()
+
+
+def test_scalar_registers_settle_before_memory_instructions_read_them(kernels):
+    bad = []
+    for fn, code in kernels:
+        recent = []                                    # (written registers, states passed since), newest last
+        for name, operands in code:
+            if name.startswith(("global_", "buffer_", "flat_", "scratch_")):
+                read = set().union(*map(_scalars, operands))
+                bad += [(fn, name, operands, n) for written, n in recent if n < 5 and written & read]
+            passed = _states(name, operands)
+            recent = [(w, n + passed) for w, n in recent if n + passed < 5]
+            if name.startswith("s_"):                  # a scalar instruction's own result is ready at once
+                recent = [(w - _scalars(operands[0]), n) for w, n in recent]
+            written = _vector_writes(name, operands)
+            if written:
+                recent.append((written, 0))
+            if name in ("s_branch", "s_endpgm"):
+                recent = []
+    assert not bad, f"{len(bad)} reads too early, the first {bad[0]}"
