@@ -21,7 +21,8 @@ constexpr int32_t kMaxDeviceExperts = 8192;  // the device contract keeps per-ex
 // rows (the longest real wait is one gate/up stage: milliseconds)
 constexpr int64_t kFusedWaitUs = 2000000;
 
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+// ceil(a / b) without forming a + b - 1, which wraps around next to INT64_MAX
+int64_t ceil_div(int64_t a, int64_t b) { return a / b + (a % b > 0); }
 
 // Shape checks shared by the forward and the two stage entry points.
 int check_dims(int64_t hidden, int64_t intermediate, int32_t num_experts,

@@ -163,3 +163,17 @@ def test_binding_refuses_cpu_tensors_and_types():
     with pytest.raises(TypeError):
         R.dequantize_mxfp4(torch.zeros(4, 128, dtype=torch.uint8), torch.zeros(1, 4, 8, dtype=torch.uint8), 256,
                            dtype=torch.float64)
+
+
+# the longest row lengths that 64 bits hold, a multiple of 8: the chunk count must not wrap around
+HUGE = [(1 << 63) - 8, (1 << 63) - 256, 1 << 62]
+
+
+@pytest.mark.parametrize("cols", HUGE)
+def test_row_lengths_next_to_the_end_of_64_bits(cols):
+    L = R.lib()
+    assert L.rmoe_mxfp4_chunks(cols) == -(-cols // 256)
+    for rows in (1, 4):
+        assert L.rmoe_quantize_mxfp4(A16, 0, 1, rows, cols, A16, A16, None) == SHAPE
+        assert L.rmoe_dequantize_mxfp4(A16, A16, 0, 1, rows, cols, A16, None) == SHAPE
+        assert L.rmoe_pack_mxfp4_f16(A16, A16, A16, A16, rows, 2, cols, A16, A16, A16, 512, None) == SHAPE
