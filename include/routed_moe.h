@@ -504,8 +504,9 @@ RMOE_API int rmoe_pack_mxfp4_f16(const void *x, const float *topk_weights,
  * bytes(I)] followed by their scales [chunks(I), Tp, 8]; contents irrelevant
  * on entry.  Only valid rows of out and of the workspace are written.
  * variant: RMOE_VARIANT_STREAM or _TILE, or _AUTO for the choice of
- * rmoe_pick_variant_mxfp4.  Codes, scales and workspace 16-byte aligned.  Two
- * launches on `stream`.
+ * rmoe_pick_variant_mxfp4.  Codes, scales and workspace 16-byte aligned, and
+ * total_padded_tokens even, so that every chunk's scales are too
+ * (RMOE_ERR_UNSUPPORTED_SHAPE).  Two launches on `stream`.
  */
 RMOE_API size_t rmoe_mxfp4_workspace_bytes(int64_t total_padded_tokens, int64_t intermediate);
 RMOE_API int rmoe_pick_variant_mxfp4(int32_t variant, int64_t num_pairs, int32_t num_experts);

@@ -653,7 +653,10 @@ int check_mx_dims(int64_t hidden, int64_t intermediate, int32_t E, int64_t Tp, i
                   int32_t variant) {
     const int st = check_dims(hidden, intermediate, E, Tp, M);
     if (st != RMOE_OK) return st;
-    return bad_variant(variant) || pairs < 0 ? RMOE_ERR_INVALID_ARGUMENT : RMOE_OK;
+    if (bad_variant(variant) || pairs < 0) return RMOE_ERR_INVALID_ARGUMENT;
+    // a chunk's token scales start 8 Tp bytes after the chunk's before: they
+    // travel 16 bytes at a time, which an odd Tp would misalign
+    return Tp % 2 ? RMOE_ERR_UNSUPPORTED_SHAPE : RMOE_OK;
 }
 
 }  // namespace

@@ -177,3 +177,14 @@ def test_row_lengths_next_to_the_end_of_64_bits(cols):
         assert L.rmoe_quantize_mxfp4(A16, 0, 1, rows, cols, A16, A16, None) == SHAPE
         assert L.rmoe_dequantize_mxfp4(A16, A16, 0, 1, rows, cols, A16, None) == SHAPE
         assert L.rmoe_pack_mxfp4_f16(A16, A16, A16, A16, rows, 2, cols, A16, A16, A16, 512, None) == SHAPE
+
+
+@pytest.mark.parametrize("fn,names", [("rmoe_gate_up_mxfp4", GU), ("rmoe_down_mxfp4", DN), ("rmoe_forward_mxfp4", FW)])
+@pytest.mark.parametrize("variant", [0, 1, 2])
+def test_odd_padded_row_counts(fn, names, variant):
+    """The scales of a chunk lie 8 Tp bytes after the chunk's before, and are
+    16-byte aligned only for an even Tp."""
+    f = getattr(R.lib(), fn)
+    for Tp in (385, 511, 513):
+        assert f(*[A16] * len(names), 512, 512, 2, Tp, 5, 3, variant, None) == SHAPE
+    assert f(*[A16] * len(names), 512, 512, 2, 514, 0, 0, variant, None) == OK
