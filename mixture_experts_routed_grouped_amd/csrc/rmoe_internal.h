@@ -7,6 +7,8 @@
 
 #include <atomic>
 
+#include "rmoe_sched.h"
+
 namespace rmoe {
 
 // Opt a kernel into `bytes` of dynamic LDS, once per device: the attribute
@@ -21,6 +23,25 @@ inline hipError_t lds_opt_in_once(const void *fn, int bytes, std::atomic<uint64_
     e = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e == hipSuccess && bit) done.fetch_or(bit, std::memory_order_release);
     return e;
+}
+
+// Workgroup slots of the persistent kernel on the current device: its CU
+// count rounded down to a multiple of 8 (cached per device).
+inline hipError_t cu_grid(unsigned &grid) {
+    static std::atomic<int> cached[64];
+    int dev = 0;
+    hipError_t e = hipGetDevice(&dev);
+    if (e != hipSuccess) return e;
+    int n = dev < 64 ? cached[dev].load(std::memory_order_relaxed) : 0;
+    if (n == 0) {
+        e = hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev);
+        if (e != hipSuccess) return e;
+        n = n / kXcd * kXcd;
+        if (n < kXcd) n = kXcd;
+        if (dev < 64) cached[dev].store(n, std::memory_order_relaxed);
+    }
+    grid = (unsigned)n;
+    return hipSuccess;
 }
 
 // One stage of the routed expert FFN as the kernels see it: a grouped GEMM

@@ -36,7 +36,6 @@
 //   publish(k)               after the barrier that publishes step k
 #pragma once
 
-#include <atomic>
 #include <type_traits>
 
 #include "rmoe_device.h"
@@ -44,27 +43,6 @@
 #include "rmoe_sched.h"
 
 namespace rmoe {
-
-constexpr int kXcd = 8;  // MI355X: workgroups go round-robin over 8 XCDs
-
-// Workgroup slots of the persistent kernel on the current device: its CU
-// count rounded down to a multiple of 8 (cached per device).
-inline hipError_t cu_grid(unsigned &grid) {
-    static std::atomic<int> cached[64];
-    int dev = 0;
-    hipError_t e = hipGetDevice(&dev);
-    if (e != hipSuccess) return e;
-    int n = dev < 64 ? cached[dev].load(std::memory_order_relaxed) : 0;
-    if (n == 0) {
-        e = hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev);
-        if (e != hipSuccess) return e;
-        n = n / kXcd * kXcd;
-        if (n < kXcd) n = kXcd;
-        if (dev < 64) cached[dev].store(n, std::memory_order_relaxed);
-    }
-    grid = (unsigned)n;
-    return hipSuccess;
-}
 
 // A pointer known to be the same in every lane, in scalar registers.
 template <class T>
@@ -80,6 +58,7 @@ __device__ __forceinline__ const T *uniform(const T *p) {
 // 1-2 k cycles each in a persistent kernel's step to its next item).
 typedef const __attribute__((address_space(4))) int32_t *Table;
 __device__ __forceinline__ Table table(const int32_t *p) { return (Table)(uintptr_t)p; }
+typedef ItemWalk<Table> Walk;
 
 // x, as if it were a new value: keeps the compiler from computing what
 // depends on it ahead of a loop, where it would stay live (and spill).
@@ -220,56 +199,6 @@ __device__ __forceinline__ void ktiles(P &p, int ntt, bool newer, F &&done) {
     }
 }
 
-// A work item: blocks bx (rows0 valid rows) and bx + 1 (rows1, 0: absent or
-// of another expert) of expert e, off rows into it, against slice nt.
-struct Item {
-    int nt, e, bx, off, rows0, rows1;
-};
-
-// The items of one workgroup, in the order of rmoe_sched.h: entry x slice,
-// rectangles of RMOE_TILE_GROUP slices, entries in expert order within one,
-// slices innermost; the list is cut into one contiguous part per XCD, which
-// its workgroups take round robin.  (The same walk as tile_item there, on
-// tables read by scalar loads.)
-struct ItemWalk {
-    Table gs, gpo, gidx;
-    int NT, P, i, end, step;  // list positions: next, end of this XCD's part, stride
-    int e = 0, base = 0;      // expert of the walk, entries before it
-
-    __device__ __forceinline__ int entries(int x) const { return (gs[x] + 2 * kBlockM - 1) / (2 * kBlockM); }
-    __device__ __forceinline__ ItemWalk(const int32_t *sizes, const int32_t *padded, const int32_t *blocks, int E,
-                                        int slices)
-        : gs(table(sizes)), gpo(table(padded)), gidx(table(blocks)), NT(slices), P(0) {
-        for (int x = 0; x < E; ++x) P += entries(x);
-        const int tot = P * NT, per = (tot + kXcd - 1) / kXcd, lo = (int)(blockIdx.x % kXcd) * per;
-        i = lo + (int)(blockIdx.x / kXcd);
-        end = min(tot, lo + per);
-        step = (int)(gridDim.x / kXcd);
-    }
-    // The next item that holds rows (blocks mapped to another expert hold none).
-    __device__ __forceinline__ bool next(Item &it) {
-        for (; i < end; i += step) {
-            const int g = i / (RMOE_TILE_GROUP * P), r = i - g * RMOE_TILE_GROUP * P;
-            const int width = min(RMOE_TILE_GROUP, NT - g * RMOE_TILE_GROUP);
-            const int entry = r / width;
-            if (entry < base) e = base = 0;  // a new rectangle
-            while (entry >= base + entries(e)) base += entries(e++);
-            it.nt = g * RMOE_TILE_GROUP + r - entry * width;
-            it.e = e;
-            it.off = 2 * kBlockM * (entry - base);
-            it.bx = gpo[e] / kBlockM + 2 * (entry - base);
-            const int rows = gs[e] - it.off;  // of the entry, at least one
-            it.rows0 = gidx[it.bx] == e ? min(rows, kBlockM) : 0;
-            it.rows1 = rows > kBlockM && gidx[it.bx + 1] == e ? min(rows - kBlockM, kBlockM) : 0;
-            if (it.rows0 || it.rows1) {
-                i += step;
-                return true;
-            }
-        }
-        return false;
-    }
-};
-
 // Runs a persistent workgroup (one per CU).  T, the tile, provides p (its
 // operands), set(item) (their bases), tiles(item) (this wave's live token
 // tiles) and finish<NTT>(item, acc, fill): the epilogue, which calls fill()
@@ -278,15 +207,15 @@ struct ItemWalk {
 template <class T>
 __device__ __forceinline__ void run_items(T &tile, const int32_t *group_sizes, const int32_t *padded_offsets,
                                           const int32_t *block_experts, int E, int NT) {
-    ItemWalk walk(group_sizes, padded_offsets, block_experts, E, NT);
-    Item it;
+    Walk walk(table(group_sizes), table(padded_offsets), table(block_experts), E, NT, (int)blockIdx.x, (int)gridDim.x);
+    TileItem it;
     if (!walk.next(it)) return;
     tile.set(it);
     kfill(tile.p);
     bool newer = false, more = true;
     while (more) {
         ktiles(tile.p, tile.tiles(it), newer, [&](auto &acc, auto n) __attribute__((always_inline)) {
-            const Item now = it;
+            const TileItem now = it;
             newer = tile.template finish<decltype(n)::value>(now, acc, [&]() __attribute__((always_inline)) {
                 more = walk.next(it);
                 if (more) {

@@ -143,7 +143,7 @@ struct Tile {
         p.sstep = 8 * (wave < 2 ? N : a.Tp);
         p.soff = 16 * lane;
     }
-    __device__ __forceinline__ void set(const Item &it) {
+    __device__ __forceinline__ void set(const TileItem &it) {
         const int64_t n0 = (int64_t)it.nt * (DUAL ? 128 : 256);
         // weight rows 64 w .. of the slot: gate rows for waves 0, 1, up rows for 2, 3
         int64_t wrow0 = n0 + (DUAL ? (64 * wave) & 127 : 64 * wave);
@@ -163,8 +163,8 @@ struct Tile {
         }
     }
     // valid rows and live token tiles of this wave
-    __device__ __forceinline__ int rows(const Item &it) const { return wt ? it.rows1 : it.rows0; }
-    __device__ __forceinline__ int tiles(const Item &it) const {
+    __device__ __forceinline__ int rows(const TileItem &it) const { return wt ? it.rows1 : it.rows0; }
+    __device__ __forceinline__ int tiles(const TileItem &it) const {
         return DUAL || (int64_t)it.nt * 256 + 128 * ww < N ? (rows(it) + 31) / 32 : 0;
     }
 
@@ -172,7 +172,7 @@ struct Tile {
     // 4q + r holds feature 8q + 4lh + r.  Lanes 0-31 assemble and store block
     // 0, lanes 32-63 block 1.
     template <int NTT>
-    __device__ __forceinline__ void hidden(const Item &it, f16x (&acc)[4][4]) const {
+    __device__ __forceinline__ void hidden(const TileItem &it, f16x (&acc)[4][4]) const {
         const int ln = fresh(lane), lr = ln & 31, lh = ln >> 5;
         const int64_t n0 = (int64_t)it.nt * 128, row0 = (int64_t)(it.bx + wt) * kBlockM;
         const int64_t orb = (int64_t)((N + kMxChunk - 1) / kMxChunk) * kMxChunkBytes;
@@ -221,7 +221,7 @@ struct Tile {
     // the last barrier; the next item's first step goes to slots 0): 128
     // columns per row, 16-byte chunks XOR-swizzled by row.
     template <int NTT>
-    __device__ __forceinline__ void out(const Item &it, f16x (&acc)[4][4]) const {
+    __device__ __forceinline__ void out(const TileItem &it, f16x (&acc)[4][4]) const {
         const int ln = fresh(lane), lr = ln & 31, lh = ln >> 5;
         const int64_t row0 = (int64_t)(it.bx + wt) * kBlockM;
         const int myrows = rows(it);
@@ -266,7 +266,7 @@ struct Tile {
     }
 
     template <int NTT, class F>
-    __device__ __forceinline__ bool finish(const Item &it, f16x (&acc)[4][4], F &&fill) const {
+    __device__ __forceinline__ bool finish(const TileItem &it, f16x (&acc)[4][4], F &&fill) const {
         fill();
         if constexpr (DUAL)
             hidden<NTT>(it, acc);

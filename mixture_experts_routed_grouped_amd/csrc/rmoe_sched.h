@@ -30,6 +30,7 @@
 namespace rmoe {
 
 constexpr int kItemRows = 128;  // rows per contract block
+constexpr int kXcd = 8;         // MI355X: workgroups go round-robin over 8 XCDs
 
 struct TileItem {
     int nt;     // weight slice
@@ -52,11 +53,19 @@ struct TileCursor {
     int e = 0, base = 0;
 };
 
-RMOE_HD int live_blocks(const int32_t *gs, int e) { return (gs[e] + kItemRows - 1) / kItemRows; }
-RMOE_HD int entries_of(const int32_t *gs, int e) { return (live_blocks(gs, e) + 1) / 2; }
+// T, here and below: a table of int32_t (a pointer into any address space).
+template <class T>
+RMOE_HD int live_blocks(T gs, int e) {
+    return (gs[e] + kItemRows - 1) / kItemRows;
+}
+template <class T>
+RMOE_HD int entries_of(T gs, int e) {
+    return (live_blocks(gs, e) + 1) / 2;
+}
 
 // The part of locality group grp (of ngrp).
-RMOE_HD TileSeq tile_seq(const int32_t *gs, int E, int NT, int grp, int ngrp) {
+template <class T>
+RMOE_HD TileSeq tile_seq(T gs, int E, int NT, int grp, int ngrp) {
     TileSeq s;
     s.NT = NT;
     s.P = 0;
@@ -71,7 +80,8 @@ RMOE_HD TileSeq tile_seq(const int32_t *gs, int E, int NT, int grp, int ngrp) {
 // Item i of the group's part.  The cursor only moves forward while i does
 // (and starts over when the entry index steps back, at a new rectangle), so
 // a workgroup's walk over the experts is amortised over its items.
-RMOE_HD TileItem tile_item(const int32_t *gs, const int32_t *gpo, const TileSeq &s, int i, TileCursor &c) {
+template <class T>
+RMOE_HD TileItem tile_item(T gs, T gpo, const TileSeq &s, int i, TileCursor &c) {
     TileItem it;
     const int q = s.lo + i;
     const int gsz = RMOE_TILE_GROUP * s.P;
@@ -93,6 +103,85 @@ RMOE_HD TileItem tile_item(const int32_t *gs, const int32_t *gpo, const TileSeq 
     it.rows1 = r1 < 0 ? 0 : (r1 > kItemRows ? kItemRows : r1);
     return it;
 }
+
+// The items of one workgroup of a launch of `grid` (a multiple of kXcd), in
+// turn: workgroup w belongs to locality group w % kXcd and takes the group's
+// items round robin.  Blocks that the block table maps to another expert
+// hold no rows; an item without any is passed over.
+template <class T>
+struct ItemWalk {
+    T gs, gpo, gidx;
+    TileSeq s;
+    TileCursor c;
+    int i, step;  // next item of the group's part, stride
+
+    RMOE_HD ItemWalk(T sizes, T padded, T blocks, int E, int NT, int block, int grid)
+        : gs(sizes), gpo(padded), gidx(blocks), s(tile_seq(sizes, E, NT, block % kXcd, kXcd)), i(block / kXcd),
+          step(grid / kXcd) {}
+    RMOE_HD bool next(TileItem &it) {
+        for (; i < s.n; i += step) {
+            it = tile_item(gs, gpo, s, i, c);
+            if (gidx[it.bx] != it.e) it.rows0 = 0;
+            if (it.rows1 > 0 && gidx[it.bx + 1] != it.e) it.rows1 = 0;
+            if (it.rows0 || it.rows1) {
+                i += step;
+                return true;
+            }
+        }
+        return false;
+    }
+};
+
+// ---- Weight gradients: the tiles of three matrices per expert (two of
+// nh x ni tiles, the third its transpose), dealt to the XCDs in runs of 32
+// consecutive ones (4 rows of tiles x 8), one per CU, which share operands in
+// that XCD's L2 and take the same time; every expert's runs spread over the
+// XCDs.
+constexpr int kGradRun = 32;
+
+struct GradTile {
+    int e, m;  // expert, matrix
+    int a, b;  // tile along the output's rows' contiguous side, and across its rows
+};
+RMOE_HD GradTile grad_tile(int item, int nh, int ni) {
+    const int per = nh * ni;
+    GradTile t;
+    t.e = item / (3 * per);
+    t.m = (item / per) % 3;
+    const int q = item % per, nA = t.m < 2 ? nh : ni, nB = t.m < 2 ? ni : nh;
+    const int g = q / (8 * nB), width = nA - 8 * g < 8 ? nA - 8 * g : 8, r = q - 8 * g * nB;
+    t.a = 8 * g + r % width;
+    t.b = r / width;
+    return t;
+}
+
+// The tiles of one workgroup, in turn: an XCD's list is dealt to its
+// workgroups round robin; where its workgroups busy, busy + 1, ... are free
+// while the first `busy` finish other work that takes as long as `lead` tiles,
+// they first share lead * (their number) tiles among themselves.
+struct GradWalk {
+    int total, xcd, nl, me, busy, head, j;  // j: position in this XCD's list
+    bool ahead;
+
+    RMOE_HD GradWalk(int tiles, int busy_, int lead, int block, int grid)
+        : total(tiles), xcd(block % kXcd), nl(grid / kXcd), me(block / kXcd), busy(busy_), head(lead * (nl - busy_)) {
+        ahead = head > 0 && me >= busy;
+        j = ahead ? me - busy : head + me;
+    }
+    // The next tile, -1 past the last.
+    RMOE_HD int next() {
+        for (;;) {
+            if (ahead && j >= head) {
+                ahead = false;
+                j = head + me;
+            }
+            const int run = j / kGradRun * kXcd * kGradRun, item = run + xcd * kGradRun + j % kGradRun;
+            if (run >= total) return -1;
+            j += ahead ? nl - busy : nl;
+            if (item < total) return item;
+        }
+    }
+};
 
 // ---- Single launch with the hidden hand-over kept inside one locality
 // group (XCD).  Every entry (a pair of blocks or a lone last block) belongs

@@ -43,7 +43,6 @@
 namespace rmoe {
 namespace {
 
-constexpr int kXcd = 8;     // MI355X: workgroups go round-robin over 8 XCDs
 constexpr int BK = 64;      // K per step
 constexpr int ROWB = 2 * BK;  // bytes per LDS row: one 128-byte line
 constexpr int CPR = ROWB / 16;  // 16-byte chunks per row
@@ -606,25 +605,6 @@ __global__ __launch_bounds__(256) void fused_kernel(StageArgs gu, StageArgs dn, 
     }
 }
 
-// Workgroup slots of the persistent kernel on the current device: its CU
-// count rounded down to a multiple of 8 (cached per device).
-hipError_t persistent_grid(unsigned &grid) {
-    static std::atomic<int> cached[64];
-    int dev = 0;
-    hipError_t e = hipGetDevice(&dev);
-    if (e != hipSuccess) return e;
-    int n = dev < 64 ? cached[dev].load(std::memory_order_relaxed) : 0;
-    if (n == 0) {
-        e = hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev);
-        if (e != hipSuccess) return e;
-        n = n / kXcd * kXcd;
-        if (n < kXcd) n = kXcd;
-        if (dev < 64) cached[dev].store(n, std::memory_order_relaxed);
-    }
-    grid = (unsigned)n;
-    return hipSuccess;
-}
-
 // Rate of the real-time counter (s_memrealtime) on the current device, in
 // kHz (cached per device; 100 MHz where the runtime reports none).
 hipError_t wall_clock_khz(int &khz) {
@@ -646,7 +626,7 @@ hipError_t wall_clock_khz(int &khz) {
 template <bool DUAL>
 hipError_t launch(const StageArgs &a, int NT, hipStream_t s) {
     unsigned grid = 0;
-    hipError_t e = persistent_grid(grid);
+    hipError_t e = cu_grid(grid);
     if (e != hipSuccess) return e;
     const unsigned lds = LDS_BYTES;  // above the 64 KB default, so opt in
     static std::atomic<uint64_t> lds_set{0};
@@ -669,7 +649,7 @@ hipError_t launch_tile_down(const StageArgs &a, hipStream_t s) {
 hipError_t launch_fused(const StageArgs &gu, const StageArgs &dn, int32_t *sync, int64_t wait_us,
                         bool local, hipStream_t s) {
     unsigned grid = 0;
-    hipError_t e = persistent_grid(grid);
+    hipError_t e = cu_grid(grid);
     if (e != hipSuccess) return e;
     int khz = 0;
     e = wall_clock_khz(khz);

@@ -338,7 +338,7 @@ struct Rows {
         p.trow0 = 128 * wt;
         p.lane = lane;
     }
-    __device__ __forceinline__ void set(const Item &it) {
+    __device__ __forceinline__ void set(const TileItem &it) {
         int64_t col = (int64_t)it.nt * 256 + 64 * wave;
         col = col < N ? col : N - 64;  // a narrow last slice: idle columns read valid ones
         // an absent second block: its half reads the first block's rows
@@ -349,15 +349,15 @@ struct Rows {
         p.w[1] = HID ? p.w[0] : uniform(a.wu + wofs);
         p.t[1] = HID ? p.t[0] : uniform(a.du + tofs);
     }
-    __device__ __forceinline__ int rows(const Item &it) const { return wt ? it.rows1 : it.rows0; }
-    __device__ __forceinline__ int tiles(const Item &it) const {
+    __device__ __forceinline__ int rows(const TileItem &it) const { return wt ? it.rows1 : it.rows0; }
+    __device__ __forceinline__ int tiles(const TileItem &it) const {
         return (int64_t)it.nt * 256 + 128 * ww < N ? (rows(it) + 31) / 32 : 0;
     }
 
     // Epilogue; fill() issues the next item's first step.  Returns whether at
     // least kNewer memory instructions followed it for sure.
     template <int NTT, class F>
-    __device__ __forceinline__ bool finish(const Item &it, f16x (&acc)[4][4], F &&fill) const {
+    __device__ __forceinline__ bool finish(const TileItem &it, f16x (&acc)[4][4], F &&fill) const {
         const int lane = fresh(this->lane), lr = lane & 31, lh = lane >> 5;
         const int64_t row0 = (int64_t)(it.bx + wt) * kBlockM, col0 = (int64_t)it.nt * 256 + 128 * ww;
         const int nrows = rows(it);
@@ -491,19 +491,19 @@ struct Forward {
         p.trow0 = 128 * wt;
         p.lane = lane;
     }
-    __device__ __forceinline__ void set(const Item &it) {
+    __device__ __forceinline__ void set(const TileItem &it) {
         const int64_t f0 = (int64_t)it.nt * 128 + ((64 * wave) & 127);
         const int row = it.rows1 > 0 ? 64 * wave : (64 * wave) & 127;  // as in Rows::set
         p.w = uniform((wave < 2 ? a.wg : a.wu) + ((int64_t)it.e * a.I + f0) * a.H);
         p.t = uniform(a.x + ((int64_t)it.bx * kBlockM + row) * a.H);
     }
-    __device__ __forceinline__ int rows(const Item &it) const { return wt ? it.rows1 : it.rows0; }
-    __device__ __forceinline__ int tiles(const Item &it) const { return (rows(it) + 31) / 32; }
+    __device__ __forceinline__ int rows(const TileItem &it) const { return wt ? it.rows1 : it.rows0; }
+    __device__ __forceinline__ int tiles(const TileItem &it) const { return (rows(it) + 31) / 32; }
 
     // gate, up and hidden rows, one after the other through the staging
     // pieces: 128 rows of 64 features, 64 rows per piece
     template <int NTT, class F>
-    __device__ __forceinline__ bool finish(const Item &it, f16x (&acc)[4][4], F &&fill) const {
+    __device__ __forceinline__ bool finish(const TileItem &it, f16x (&acc)[4][4], F &&fill) const {
         fill();
         const int ln = fresh(lane), lr = ln & 31, lh = ln >> 5, c = ln & 7;
         const int nrows = rows(it);
@@ -555,10 +555,8 @@ __global__ __launch_bounds__(256) void drw_kernel(TrainArgs a) { sum_drw(a); }
 
 // Weight gradients: every 256 x 256 tile of the three matrices of every
 // expert, its sum over the expert's rows; an expert without rows gets zeros.
-// Persistent, one workgroup per CU.  Tiles are dealt to the XCDs in runs of
-// 32 consecutive ones (4 rows of tiles x 8), one per CU, which share operands
-// in that XCD's L2 and take the same time; every expert's runs spread over
-// the XCDs.
+// Persistent, one workgroup per CU; the tiles' order and who takes them:
+// rmoe_sched.h.
 struct Cols {
     const TrainArgs &a;
     unsigned char *smem;
@@ -588,17 +586,14 @@ struct Cols {
     __device__ __forceinline__ int64_t cols_a(int m) const { return m < 2 ? a.H : a.I; }
     __device__ __forceinline__ int64_t cols_b(int m) const { return m < 2 ? a.I : a.H; }
 
-    // Tile of position i; false where there is nothing to do: past the last
-    // tile, or a group whose tables break the contract (nothing is read out
-    // of bounds, its gradients are left out).
+    // Tile `item`; false where a group's tables break the contract (nothing
+    // is read out of bounds, its gradients are left out).
     __device__ __forceinline__ bool at(int item, Tile &t) const {
-        const int per = nh * ni;
-        t.e = item / (3 * per);
-        t.m = (item / per) % 3;
-        const int q = item % per, nA = t.m < 2 ? nh : ni, nB = t.m < 2 ? ni : nh;
-        const int g = q / (8 * nB), width = min(8, nA - 8 * g), r = q - 8 * g * nB;
-        t.a0 = (int64_t)(8 * g + r % width) * 256;
-        t.b0 = (int64_t)(r / width) * 256;
+        const GradTile g = grad_tile(item, nh, ni);
+        t.e = g.e;
+        t.m = g.m;
+        t.a0 = (int64_t)g.a * 256;
+        t.b0 = (int64_t)g.b * 256;
         t.n = table(a.gs)[t.e];
         t.row0 = table(a.gpo)[t.e];
         return t.n >= 0 && t.row0 >= 0 && t.row0 + ((int64_t)t.n + BK - 1) / BK * BK <= a.Tp;
@@ -634,27 +629,16 @@ struct Cols {
     }
 };
 
-// The tiles of one workgroup.  An XCD's list is dealt to its workgroups round
-// robin; where workgroups busy, busy + 1, ... are free while the first `busy`
-// finish other work that takes as long as `lead` tiles, they first share
-// lead * (their number) tiles among themselves.
+// The tiles of one workgroup (GradWalk).
 __device__ __forceinline__ void run_cols(const TrainArgs &a, unsigned char *smem, int total, int busy, int lead) {
     Cols c(a, smem);
-    const int xcd = blockIdx.x % kXcd, nl = gridDim.x / kXcd, me = blockIdx.x / kXcd;
-    const int head = lead * (nl - busy);
-    bool ahead = head > 0 && me >= busy;
-    int j = ahead ? me - busy : head + me;  // position in this XCD's list
+    GradWalk walk(total, busy, lead, (int)blockIdx.x, (int)gridDim.x);
     // the next tile whose expert holds rows; the zeros of the others on the way
     auto advance = [&](Cols::Tile &t) __attribute__((always_inline)) {
         for (;;) {
-            if (ahead && j >= head) {
-                ahead = false;
-                j = head + me;
-            }
-            const int run = j / 32 * kXcd * 32, item = run + xcd * 32 + j % 32;
-            if (run >= total) return false;
-            j += ahead ? nl - busy : nl;
-            if (item >= total || !c.at(item, t)) continue;
+            const int item = walk.next();
+            if (item < 0) return false;
+            if (!c.at(item, t)) continue;
             if (t.n > 0) return true;
             c.zeros(t);
         }
@@ -701,8 +685,7 @@ __global__ __launch_bounds__(256) void cols_kernel(TrainArgs a, int total) {
 __global__ __launch_bounds__(256) void grads_kernel(TrainArgs a, int NT, int total) {
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
     sum_drw(a);
-    const ItemWalk walk(a.gs, a.gpo, a.gidx, a.E, NT);
-    const int nl = gridDim.x / kXcd, items = walk.end - walk.i + (int)(blockIdx.x / kXcd);  // of this XCD
+    const int nl = gridDim.x / kXcd, items = tile_seq(table(a.gs), a.E, NT, blockIdx.x % kXcd, kXcd).n;  // of this XCD
     {
         Rows<false> r(a, smem);
         run_items(r, a.gs, a.gpo, a.gidx, a.E, NT);
@@ -710,7 +693,7 @@ __global__ __launch_bounds__(256) void grads_kernel(TrainArgs a, int NT, int tot
     __syncthreads();
     int most = 0;
     for (int e = 0; e < a.E; ++e) most = max(most, (int)table(a.gs)[e]);
-    const int busy = items > 0 ? items % nl : 0;
+    const int busy = items % nl;
     run_cols(a, smem, total, busy, busy ? ((int)(2 * a.I / BK) + 6) / (most / BK + 6) : 0);
 }
 
