@@ -102,3 +102,50 @@ def test_calls_on_given_memory_and_streams():
     R.pack_mxfp4(torch.empty((0, 256), dtype=torch.float16, device="cuda"), f32, i32, i32, codes, scales, f32)
     torch.cuda.synchronize()
     assert (codes == 0x5A).all() and (scales == 0x5A).all()
+
+
+BASE = 4096  # rows that repeat
+
+
+@pytest.mark.parametrize("variant", ["stream", "tile"])
+def test_largest_block_table(variant):
+    """65535 blocks of one expert, rows of 640 code bytes: offsets past 2^32
+    bytes in the tokens, the hidden rows and the output.  The rows repeat after
+    4096, and so must the results, bit for bit; the first 4096 against 64 bits."""
+    M_, H, I = 65535, 1152, 1152
+    pairs, Tp = (M_ - 1) * 128, M_ * 128
+    print(f"[mx] {variant} {M_} blocks H={H} I={I}", flush=True)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    rnd = lambda *s: torch.randn(s, generator=g, device="cuda")  # noqa: E731
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    u8 = lambda s, v: torch.full(s, v, dtype=torch.uint8, device="cuda")  # noqa: E731
+    qc, qs = R.quantize_mxfp4(rnd(BASE, H))
+    (cs, ss), (hcs, hss) = R.mxfp4_shapes((Tp, H)), R.mxfp4_shapes((Tp, I))
+    d = {"E": 1, "H": H, "I": I, "Tp": Tp, "pairs": pairs, "codes": u8(cs, 0xFF), "scales": u8(ss, 0xFF),
+         "hc": u8(hcs, 0x5A), "hs": u8(hss, 0xA5), "gs": i32(pairs), "go": i32(0, pairs), "gpo": i32(0, Tp),
+         "gidx": torch.zeros(M_, dtype=torch.int32, device="cuda"),
+         "wg": R.quantize_mxfp4(rnd(1, I, H) / H ** 0.5), "wu": R.quantize_mxfp4(rnd(1, I, H) / H ** 0.5),
+         "wd": R.quantize_mxfp4(rnd(1, H, I) / I ** 0.5)}
+    whole = pairs // BASE * BASE
+    d["codes"][:whole].view(-1, BASE, cs[1]).copy_(qc)
+    d["codes"][whole:pairs].copy_(qc[:pairs - whole])
+    d["scales"][:, :whole].view(ss[0], -1, BASE, 8).copy_(qs[:, None])
+    d["scales"][:, whole:pairs].copy_(qs[:, :pairs - whole])
+    d["rw"] = torch.rand(BASE, generator=g, device="cuda").repeat(whole // BASE + 1)[:pairs].contiguous()
+    d["out"] = torch.full((Tp, H), 0x7E5A, dtype=torch.int16, device="cuda").view(torch.float16)
+    M._gate_up(d, variant)
+    M._down(d, variant)
+    torch.cuda.synchronize()
+    bits = d["out"].view(torch.int16)
+    for t, rows in ((d["hc"], 0), (bits, 0), (d["hs"], 1)):
+        first = t.narrow(rows, 0, BASE)
+        for p in range(BASE, pairs, BASE):
+            n = min(BASE, pairs - p)
+            assert torch.equal(t.narrow(rows, p, n), first.narrow(rows, 0, n)), p
+    assert (d["hc"][pairs:] == 0x5A).all() and (d["hs"][:, pairs:] == 0xA5).all() and (bits[pairs:] == 0x7E5A).all()
+    f = {**d, "Tp": BASE, "counts": [BASE], "c": {"group_padded_offsets": [0], "group_offsets": [0]}}
+    for n in ("codes", "hc", "out"):
+        f[n] = d[n][:BASE]
+    for n in ("scales", "hs"):
+        f[n] = d[n][:, :BASE].contiguous()
+    M._check(f)
