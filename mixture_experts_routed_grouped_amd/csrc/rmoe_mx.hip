@@ -1,9 +1,13 @@
 // MXFP4 quantisation, its inverse, and the token pack that quantises on the
 // way (format: rmoe_mx.h).  Bound by HBM: a row is read once and its codes
-// (4.25 bits per element with the scales) are written once.  470 M bf16
-// elements (8 x 14336 x 4096): 215 us to quantise (5.5 TB/s), 175 us back
-// (6.8 TB/s); the large layer's pack (16384 tokens of 7168 to 8 rows each)
-// 205 us (3.6 TB/s).  Small calls are bound by their launch.
+// (4.25 bits per element with the scales) are written once.  470 M elements
+// (8 x 14336 x 4096), each direction by itself: bf16 200 us to quantise (6.0
+// TB/s), 213 us back (5.6; 183 us right behind the quantisation, part of whose
+// codes the last-level cache still holds); fp16 the same; fp32 425 us (5.0
+// TB/s) and 500 us (4.3), its 32 bytes per lane in two halves.  The large
+// layer's pack (16384 tokens of 7168 to 8 rows each) 202 us: 0.73 GB, 3.6
+// TB/s, scale lines written 8 bytes at a time from several XCDs.  Small calls
+// are bound by their launch.
 //
 // A half-wave takes one chunk of 256 elements of one row: 8 elements per
 // lane (16-byte loads for fp16 and bf16, two for fp32), 4 lanes per block.
@@ -232,9 +236,10 @@ __global__ __launch_bounds__(256) void pack_mx_kernel(const _Float16 *__restrict
 }
 
 // units per half-wave: 4 once every CU has several waves of work, else 1 so
-// that a small call spreads over the chip (expert weights of 470 M elements
-// there and back: 472 us with 4, 486 with 1, 480 with 8); at most 2^20
-// workgroups, which stride beyond
+// that a small call spreads over the chip.  470 M elements with 1, 4 and 8:
+// bf16 210, 199, 207 us to quantise and 226, 213, 211 back (fp16 the same);
+// fp32 382, 423, 419 and 543, 500, 582.  At most 2^20 workgroups, which stride
+// beyond
 constexpr int64_t kMxWideUnits = 256 * 8 * 16;
 unsigned grid_units(int64_t units, int per) {
     const int64_t g = (units + 8 * per - 1) / (8 * per);

@@ -11,8 +11,9 @@
 //
 // The gate/up epilogue quantises the hidden rows on the way out: a lane
 // holds 16 of a block's 32 features of one token, its partner lane + 32 the
-// others, so the block's maximum is 15 register maxima and one shuffle, and
-// the hidden rows cost 4.25 bits per element of memory traffic.
+// others, so the block's maximum is eight three-value maxima, a swap of the
+// halves and one more, and the hidden rows cost 4.25 bits per element of
+// memory traffic.
 #include <atomic>
 
 #include "rmoe_kloop.h"

@@ -10,20 +10,24 @@
 //
 // with silu'(g) = s + g s (1 - s), s = 1 / (1 + e^-g).  Everything between
 // the fp16 inputs and outputs is fp32; dg, du and hw are rounded to fp16
-// once, as operands of the products that follow.
+// once, as operands of the products that follow (a split into two fp16
+// operands would double those products).  That rounding and the results' own
+// put dx and the weight gradients 2.9e-4 of their norm from 64 bits on normal
+// inputs; the results' rounding alone, 2.1e-4.
 //
 // All three products run on the 256 x 256 tiles of rmoe_kloop.h with fp16
 // MFMA (v_mfma_f32_32x32x16_f16), bound by the matrix cores and by operand
-// delivery as the forward's tiles are (64 experts of 2048 x 1408, 49152 skewed
-// rows: hidden stage 465 us, 0.61 PFLOP/s, a third of it the epilogue's 690 MB;
-// dx 560 us, 1.01; weight gradients 1065 us, 0.80; 8 experts of 4096 x 14336,
-// 8192 rows: 0.98, 1.02 and 1.01 PFLOP/s at 1.5-1.7 GHz).  Their sums run along the row index of
-// a row-major matrix (Wd over H, Wg and Wu over I; for the weight gradients
-// both operands, over the tokens), so those operands lie k-major: an LDS slot
-// holds 64 k rows of 256 columns, and ds_read_b64_tr_b16 turns it into MFMA
-// operands: a group of 16 lanes reads 4 k rows of 16 columns and each lane
-// receives its column's 4 values.  DMA instructions move 8 k rows x 128
-// bytes, the pattern the L2 serves best.
+// delivery as the forward's tiles are (median dispatches on several cards; 64
+// experts of 2048 x 1408, 49152 skewed rows: hidden stage 490-505 us, 0.56-0.58
+// PFLOP/s, 36-42% of an item the epilogue's 690 MB; dx 561-577 us, 0.98-1.01;
+// weight gradients 1072-1119 us, 0.76-0.79; 8 experts of 4096 x 14336, 8192
+// rows: 0.92-0.96, 0.97-1.00 and 0.98 PFLOP/s at 1.5-1.7 GHz).  Their sums run
+// along the row index of a row-major matrix (Wd over H, Wg and Wu over I; for
+// the weight gradients both operands, over the tokens), so those operands lie
+// k-major: an LDS slot holds 64 k rows of 256 columns, and ds_read_b64_tr_b16
+// turns it into MFMA operands: a group of 16 lanes reads 4 k rows of 16 columns
+// and each lane receives its column's 4 values.  DMA instructions move 8 k rows
+// x 128 bytes, the pattern the L2 serves best.
 //
 // k-major slot: [4 column groups of 64][8 k groups of 8] blocks of 1 KB =
 // 8 rows x 128 bytes; 16-byte chunk c of row r sits at c ^ swz_k(r), which
