@@ -521,7 +521,7 @@ RMOE_API int rmoe_forward_mxfp4(const void *token_codes, const void *token_scale
                                 int32_t num_blocks_m, int32_t variant, void *stream);
 
 /* Its stages alone.  rmoe_gate_up_mxfp4 writes the hidden rows' codes and
- * scales, rmoe_down_mxfp4 reads them. */
+ * scales, rmoe_down_mxfp4 reads them; sizes, alignment and errors as there. */
 RMOE_API int rmoe_gate_up_mxfp4(const void *token_codes, const void *token_scales,
                                 const void *gate_codes, const void *gate_scales, const void *up_codes,
                                 const void *up_scales, const int32_t *group_sizes,

@@ -734,7 +734,7 @@ def forward_mxfp4(token_codes, token_scales, gate_codes, gate_scales, up_codes, 
     (``quantize_mxfp4`` of [E, I, H], [E, I, H] and [E, H, I]); the hidden
     rows between the two products are MXFP4 too.  ``workspace``: uint8, at
     least ``mxfp4_workspace_bytes(Tp, I)``; ``out`` [Tp, H] fp16, valid rows
-    written.  Asynchronous on ``stream``."""
+    written; Tp even.  Asynchronous on ``stream``."""
     torch = _torch()
     u8 = torch.uint8
     dev = _gpu(out, "out")
