@@ -32,7 +32,8 @@ constexpr int TILE_B = 32 * 128;     // 32 rows of a chunk
 constexpr int SCALE_B = 32 * 8;      // their scales
 constexpr int TILE_ALL = TILE_B + SCALE_B;
 
-// 256-byte DMA: lane i stores the dword at g to LDS byte lds + 4 i
+// 256-byte DMA: lane i stores the dword at g to LDS byte lds + 4 i (s_nop: as
+// in dma16)
 __device__ __forceinline__ void dma4(const void *g, unsigned lds) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(lds), "v"(g) : "memory", "m0");
 }
