@@ -539,6 +539,89 @@ RMOE_API int rmoe_down_mxfp4(const void *hidden_codes, const void *hidden_scales
                              int32_t num_blocks_m, int32_t variant, void *stream);
 
 /*
+ * 8-bit integers: a row of elements (one token, one output channel of a
+ * weight matrix, one hidden row) shares the scale s = amax / 127 rounded to
+ * fp32, amax the row's largest magnitude; its codes are the integers nearest
+ * to x / s, ties to the even one, within +-127, one byte each, row-major.  A
+ * row of zeros (or one so small that s underflows) has s = 0 and codes 0.  A
+ * row that holds an infinity or a NaN has s = NaN and codes 0: every product
+ * with it is NaN.
+ *
+ * Quantise x [rows, cols] of element type RMOE_TYPE_*: codes [rows, cols]
+ * int8, scales [rows] fp32.  Expert matrices [E, N, K] are E * N rows.  cols
+ * a positive multiple of 8.  x and codes 16-byte, scales 4-byte aligned; the
+ * three must not overlap.  One launch on `stream`.
+ */
+RMOE_API int rmoe_quantize_int8(const void *x, int32_t type, int64_t rows, int64_t cols, void *codes,
+                                float *scales, void *stream);
+
+/* The inverse: y [rows, cols] of element type RMOE_TYPE_* = code times scale
+ * in fp32, rounded to the type.  Sizes, alignment (y as x), errors as there. */
+RMOE_API int rmoe_dequantize_int8(const void *codes, const float *scales, int32_t type, int64_t rows,
+                                  int64_t cols, void *y, void *stream);
+
+/*
+ * rmoe_pack_f16 that quantises on the way: token t's row of x [num_tokens,
+ * hidden] fp16 is read and quantised once (as rmoe_quantize_int8) and written
+ * to its top_k padded rows of codes [Tp, hidden] int8 and scales [Tp] fp32, Tp
+ * = total_padded_tokens; w_compact as in rmoe_pack_f16.  Pairs with table
+ * entries out of range move nothing; other rows are not written.  hidden a
+ * multiple of 8; num_tokens at most 2^31 - 1.
+ */
+RMOE_API int rmoe_pack_int8_f16(const void *x, const float *topk_weights, const int32_t *padded_row_of_pair,
+                                const int32_t *compact_pos_of_pair, int64_t num_tokens, int32_t top_k,
+                                int64_t hidden, void *codes, float *scales, float *w_compact,
+                                int64_t total_padded_tokens, void *stream);
+
+/*
+ * The routed expert FFN on 8-bit tokens and weights, a scale for each token
+ * and channel:
+ *   gate = (sum of codes' products, exact in int32) * token scale * channel
+ *   scale, up likewise; hidden = silu(gate) * up in fp32, then quantised: one
+ *   scale per row over the whole row; out = fp16( sum * hidden row's scale *
+ *   channel scale * w ).
+ * Tokens: codes [Tp, H], scales [Tp] (rmoe_pack_int8_f16); gate_w, up_w [E,
+ * I, H] and down_w [E, H, I], each as codes and scales [E, I], [E, I], [E, H]
+ * (rmoe_quantize_int8); tables, routed weights, out and sizes as
+ * rmoe_forward_f16_variant; H and I at most 133120, so that the sums fit
+ * (RMOE_ERR_UNSUPPORTED_SHAPE).  workspace: rmoe_int8_workspace_bytes(Tp, I)
+ * bytes: the hidden rows' codes [Tp, I], the rows in fp32 [Tp, I], their
+ * scales [Tp]; contents irrelevant on entry.  Only valid rows of out and of
+ * the workspace are written.  variant: RMOE_VARIANT_STREAM or _TILE (equal
+ * results, bit for bit), or _AUTO for the choice of rmoe_pick_variant_int8.
+ * Codes, the weights' scales, workspace and out 16-byte aligned, the rest 4.
+ * Three launches on `stream`.
+ */
+RMOE_API size_t rmoe_int8_workspace_bytes(int64_t total_padded_tokens, int64_t intermediate);
+RMOE_API int rmoe_pick_variant_int8(int32_t variant, int64_t num_pairs, int32_t num_experts);
+RMOE_API int rmoe_forward_int8(const void *token_codes, const float *token_scales, const void *gate_codes,
+                               const float *gate_scales, const void *up_codes, const float *up_scales,
+                               const void *down_codes, const float *down_scales,
+                               const float *routed_expert_weights, const int32_t *group_sizes,
+                               const int32_t *group_offsets, const int32_t *group_padded_offsets,
+                               const int32_t *group_idx_for_bx, void *workspace, void *out, int64_t hidden,
+                               int64_t intermediate, int32_t num_experts, int64_t total_padded_tokens,
+                               int64_t total_valid_tokens, int32_t num_blocks_m, int32_t variant, void *stream);
+
+/* Its stages alone.  rmoe_gate_up_int8 writes the hidden rows in fp32 into
+ * hidden_rows [Tp, I] (scratch; 16-byte aligned), then their codes and scales
+ * (two launches); rmoe_down_int8 reads those. */
+RMOE_API int rmoe_gate_up_int8(const void *token_codes, const float *token_scales, const void *gate_codes,
+                               const float *gate_scales, const void *up_codes, const float *up_scales,
+                               const int32_t *group_sizes, const int32_t *group_padded_offsets,
+                               const int32_t *group_idx_for_bx, float *hidden_rows, void *hidden_codes,
+                               float *hidden_scales, int64_t hidden, int64_t intermediate, int32_t num_experts,
+                               int64_t total_padded_tokens, int64_t total_valid_tokens, int32_t num_blocks_m,
+                               int32_t variant, void *stream);
+RMOE_API int rmoe_down_int8(const void *hidden_codes, const float *hidden_scales, const void *down_codes,
+                            const float *down_scales, const float *routed_expert_weights,
+                            const int32_t *group_sizes, const int32_t *group_offsets,
+                            const int32_t *group_padded_offsets, const int32_t *group_idx_for_bx, void *out,
+                            int64_t hidden, int64_t intermediate, int32_t num_experts,
+                            int64_t total_padded_tokens, int64_t total_valid_tokens, int32_t num_blocks_m,
+                            int32_t variant, void *stream);
+
+/*
  * ---- Training: the forward that keeps its pre-activations, and the backward
  * pass.  fp16 tensors, fp32 in between; E = 1 is the dense gated block.
  *

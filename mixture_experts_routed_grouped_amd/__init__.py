@@ -75,6 +75,14 @@ _SIGS = {
     "rmoe_forward_mxfp4": ([_P] * 15 + [_I64, _I64, _I32, _I64, _I64, _I32, _I32, _P], ctypes.c_int),
     "rmoe_gate_up_mxfp4": ([_P] * 11 + [_I64, _I64, _I32, _I64, _I64, _I32, _I32, _P], ctypes.c_int),
     "rmoe_down_mxfp4": ([_P] * 10 + [_I64, _I64, _I32, _I64, _I64, _I32, _I32, _P], ctypes.c_int),
+    "rmoe_quantize_int8": ([_P, _I32, _I64, _I64, _P, _P, _P], ctypes.c_int),
+    "rmoe_dequantize_int8": ([_P, _P, _I32, _I64, _I64, _P, _P], ctypes.c_int),
+    "rmoe_pack_int8_f16": ([_P] * 4 + [_I64, _I32, _I64, _P, _P, _P, _I64, _P], ctypes.c_int),
+    "rmoe_int8_workspace_bytes": ([_I64, _I64], ctypes.c_size_t),
+    "rmoe_pick_variant_int8": ([_I32, _I64, _I32], ctypes.c_int),
+    "rmoe_forward_int8": ([_P] * 15 + [_I64, _I64, _I32, _I64, _I64, _I32, _I32, _P], ctypes.c_int),
+    "rmoe_gate_up_int8": ([_P] * 12 + [_I64, _I64, _I32, _I64, _I64, _I32, _I32, _P], ctypes.c_int),
+    "rmoe_down_int8": ([_P] * 10 + [_I64, _I64, _I32, _I64, _I64, _I32, _I32, _P], ctypes.c_int),
     "rmoe_gate_up_train_f16": ([_P] * 9 + [_I64, _I64, _I32, _I64, _I64, _I32, _P], ctypes.c_int),
     "rmoe_backward_scratch_bytes": ([_I64, _I64], ctypes.c_size_t),
     "rmoe_backward_f16": ([_P] * 21 + [_I64, _I64, _I32, _I64, _I64, _I32, _P], ctypes.c_int),
@@ -613,7 +621,7 @@ def _mx_type(dtype):
         return 1
     if dtype is torch.float32:
         return 2
-    raise TypeError(f"MXFP4 converts float16, bfloat16 and float32, not {dtype}")
+    raise TypeError(f"float16, bfloat16 and float32 are converted, not {dtype}")
 
 
 def mxfp4_row_bytes(cols: int) -> int:
@@ -791,6 +799,157 @@ def down_mxfp4(hidden_codes, hidden_scales, down_codes, down_scales, routed_expe
           _arg(dev, "hidden_codes", hidden_codes, u8, Tp, ri), _arg(dev, "hidden_scales", hidden_scales, u8, ci, Tp, 8),
           _arg(dev, "down_codes", down_codes, u8, E, H, ri), _arg(dev, "down_scales", down_scales, u8, E, ci, H, 8),
           _arg(dev, "routed_expert_weights", routed_expert_weights, torch.float32),
+          *_tables(dev, E, M, group_sizes, group_padded_offsets, group_idx_for_bx, group_offsets),
+          _arg(dev, "out", out, torch.float16), H, I, E, Tp, pairs, M, _VARIANTS[variant])
+
+
+# ------------------------------------------------------------- 8-bit integers
+def quantize_int8(x, codes=None, scales=None, stream=None):
+    """8-bit integer codes of the rows of ``x`` [.., cols] (fp16, bf16 or
+    fp32; cols a multiple of 8) and one fp32 scale per row: returns ``(codes,
+    scales)``, int8 of x's shape and float32 of its shape without the last
+    axis (allocated unless given)."""
+    torch = _torch()
+    dev = _gpu(x, "x")
+    ty, px = _mx_type(x.dtype), _arg(dev, "x", x, x.dtype)
+    shape = x.shape
+    if len(shape) < 1:
+        raise ValueError("x must have rows")
+    if codes is None:
+        codes = _empty(shape, torch.int8, dev, stream)
+        pc = codes.data_ptr()
+    else:
+        pc = _arg(dev, "codes", codes, torch.int8, *shape)
+    if scales is None:
+        scales = _empty(shape[:-1], torch.float32, dev, stream)
+        ps = scales.data_ptr()
+    else:
+        ps = _i8_scales(dev, "scales", scales, shape)
+    _call("rmoe_quantize_int8", dev, stream, px, ty, shape[:-1].numel(), shape[-1], pc, ps)
+    return codes, scales
+
+
+def _i8_scales(dev, name, scales, shape):
+    """Address of the scales of rows of this shape."""
+    address = _arg(dev, name, scales, _torch().float32)
+    if scales.shape != shape[:-1]:
+        raise ValueError(f"{name} must be {list(shape[:-1])}, got {list(scales.shape)}")
+    return address
+
+
+def dequantize_int8(codes, scales, dtype=None, out=None, stream=None):
+    """The values of 8-bit ``codes`` [.., cols] under their rows' ``scales``,
+    as ``dtype`` (default fp16), in ``out`` if given."""
+    torch = _torch()
+    if dtype is None:
+        dtype = torch.float16 if out is None else out.dtype
+    ty, dev = _mx_type(dtype), _gpu(codes, "codes")
+    shape = codes.shape
+    pc, ps = _arg(dev, "codes", codes, torch.int8), _i8_scales(dev, "scales", scales, shape)
+    if out is None:
+        out = _empty(shape, dtype, dev, stream)
+        po = out.data_ptr()
+    else:
+        po = _arg(dev, "out", out, dtype, *shape)
+    _call("rmoe_dequantize_int8", dev, stream, pc, ps, ty, shape[:-1].numel(), shape[-1], po)
+    return out
+
+
+def pack_int8(x, topk_weights, padded_row_of_pair, compact_pos_of_pair, codes, scales, w_compact, stream=None):
+    """``pack`` that quantises: each fp16 token row is quantised once and its
+    codes and scale are written to its padded rows of ``codes`` [Tp, H] int8
+    and ``scales`` [Tp] float32."""
+    torch = _torch()
+    i32, f32 = torch.int32, torch.float32
+    dev = _gpu(x, "x")
+    T, H = x.shape
+    pairs = topk_weights.numel()
+    k = pairs // T if T else 0
+    if k * T != pairs or padded_row_of_pair.numel() != pairs or compact_pos_of_pair.numel() != pairs or \
+            w_compact.numel() != pairs:
+        raise ValueError("topk_weights, the pair tables and w_compact must have num_tokens * top_k entries")
+    Tp = codes.shape[0]
+    _call("rmoe_pack_int8_f16", dev, stream, _arg(dev, "x", x, torch.float16),
+          _arg(dev, "topk_weights", topk_weights, f32), _arg(dev, "padded_row_of_pair", padded_row_of_pair, i32),
+          _arg(dev, "compact_pos_of_pair", compact_pos_of_pair, i32), T, k, H,
+          _arg(dev, "codes", codes, torch.int8, Tp, H), _arg(dev, "scales", scales, f32, Tp),
+          _arg(dev, "w_compact", w_compact, f32), Tp)
+
+
+def int8_workspace_bytes(total_padded_tokens: int, intermediate: int) -> int:
+    """Bytes of ``forward_int8``'s workspace (the hidden rows' codes, the rows
+    in fp32, the rows' scales)."""
+    return int(lib().rmoe_int8_workspace_bytes(int(total_padded_tokens), int(intermediate)))
+
+
+def pick_variant_int8(num_pairs: int, num_experts: int, variant="auto") -> str:
+    """The kernel family of the 8-bit forward for a batch."""
+    v = int(lib().rmoe_pick_variant_int8(_VARIANTS[variant], int(num_pairs), int(num_experts)))
+    _check(min(v, 0), "rmoe_pick_variant_int8")
+    return _VARIANT_NAMES[v]
+
+
+def forward_int8(token_codes, token_scales, gate_codes, gate_scales, up_codes, up_scales, down_codes, down_scales,
+                 routed_expert_weights, group_sizes, group_offsets, group_padded_offsets, group_idx_for_bx, workspace,
+                 out, variant="auto", stream=None):
+    """The routed expert FFN on 8-bit tokens (``pack_int8``) and weights
+    (``quantize_int8`` of [E, I, H], [E, I, H] and [E, H, I]), a scale for each
+    token and channel; the hidden rows between the two products are 8-bit too,
+    with a scale per row.  ``workspace``: uint8, at least
+    ``int8_workspace_bytes(Tp, I)``; ``out`` [Tp, H] fp16, valid rows written.
+    Asynchronous on ``stream``."""
+    torch = _torch()
+    i8, f32 = torch.int8, torch.float32
+    dev = _gpu(out, "out")
+    Tp, H = out.shape
+    E, I = gate_codes.shape[:2]
+    M, pairs = group_idx_for_bx.numel(), routed_expert_weights.numel()
+    if workspace.numel() < int8_workspace_bytes(Tp, I):
+        raise ValueError("workspace too small")
+    _call("rmoe_forward_int8", dev, stream,
+          _arg(dev, "token_codes", token_codes, i8, Tp, H), _arg(dev, "token_scales", token_scales, f32, Tp),
+          _arg(dev, "gate_codes", gate_codes, i8, E, I, H), _arg(dev, "gate_scales", gate_scales, f32, E, I),
+          _arg(dev, "up_codes", up_codes, i8, E, I, H), _arg(dev, "up_scales", up_scales, f32, E, I),
+          _arg(dev, "down_codes", down_codes, i8, E, H, I), _arg(dev, "down_scales", down_scales, f32, E, H),
+          _arg(dev, "routed_expert_weights", routed_expert_weights, f32),
+          *_tables(dev, E, M, group_sizes, group_padded_offsets, group_idx_for_bx, group_offsets),
+          _arg(dev, "workspace", workspace, torch.uint8), _arg(dev, "out", out, torch.float16), H, I, E, Tp, pairs, M,
+          _VARIANTS[variant])
+
+
+def gate_up_int8(token_codes, token_scales, gate_codes, gate_scales, up_codes, up_scales, group_sizes,
+                 group_padded_offsets, group_idx_for_bx, hidden_rows, hidden_codes, hidden_scales, num_pairs: int,
+                 variant="auto", stream=None):
+    """Stage 1 of ``forward_int8`` alone: the hidden rows in ``hidden_rows``
+    [Tp, I] float32 (scratch), then their codes [Tp, I] int8 and scales [Tp].
+    ``num_pairs`` feeds the family choice."""
+    torch = _torch()
+    i8, f32 = torch.int8, torch.float32
+    dev = _gpu(token_codes, "token_codes")
+    (Tp, H), (E, I) = token_codes.shape, gate_codes.shape[:2]
+    M = group_idx_for_bx.numel()
+    _call("rmoe_gate_up_int8", dev, stream,
+          _arg(dev, "token_codes", token_codes, i8, Tp, H), _arg(dev, "token_scales", token_scales, f32, Tp),
+          _arg(dev, "gate_codes", gate_codes, i8, E, I, H), _arg(dev, "gate_scales", gate_scales, f32, E, I),
+          _arg(dev, "up_codes", up_codes, i8, E, I, H), _arg(dev, "up_scales", up_scales, f32, E, I),
+          *_tables(dev, E, M, group_sizes, group_padded_offsets, group_idx_for_bx),
+          _arg(dev, "hidden_rows", hidden_rows, f32, Tp, I), _arg(dev, "hidden_codes", hidden_codes, i8, Tp, I),
+          _arg(dev, "hidden_scales", hidden_scales, f32, Tp), H, I, E, Tp, int(num_pairs), M, _VARIANTS[variant])
+
+
+def down_int8(hidden_codes, hidden_scales, down_codes, down_scales, routed_expert_weights, group_sizes, group_offsets,
+              group_padded_offsets, group_idx_for_bx, out, variant="auto", stream=None):
+    """Stage 2 of ``forward_int8`` alone: out = fp16((hidden Wd^T) * w) on
+    valid rows."""
+    torch = _torch()
+    i8, f32 = torch.int8, torch.float32
+    dev = _gpu(out, "out")
+    (Tp, H), (E, _, I) = out.shape, down_codes.shape
+    M, pairs = group_idx_for_bx.numel(), routed_expert_weights.numel()
+    _call("rmoe_down_int8", dev, stream,
+          _arg(dev, "hidden_codes", hidden_codes, i8, Tp, I), _arg(dev, "hidden_scales", hidden_scales, f32, Tp),
+          _arg(dev, "down_codes", down_codes, i8, E, H, I), _arg(dev, "down_scales", down_scales, f32, E, H),
+          _arg(dev, "routed_expert_weights", routed_expert_weights, f32),
           *_tables(dev, E, M, group_sizes, group_padded_offsets, group_idx_for_bx, group_offsets),
           _arg(dev, "out", out, torch.float16), H, I, E, Tp, pairs, M, _VARIANTS[variant])
 

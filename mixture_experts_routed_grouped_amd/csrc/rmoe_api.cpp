@@ -773,6 +773,192 @@ int rmoe_forward_mxfp4(const void *xc, const void *xs, const void *gc, const voi
 
 }  // extern "C"
 
+// ---- 8-bit integers --------------------------------------------------------
+
+namespace {
+
+// 127^2 K must not pass 2^31 - 1
+constexpr int64_t kMaxI8Sum = INT32_MAX / (127 * 127) / 128 * 128;
+
+// Sizes of a quantisation: RMOE_OK with *empty set where there is nothing to do.
+int check_i8_sizes(int32_t type, int64_t rows, int64_t cols, bool *empty) {
+    if (bad_type(type) || rows < 0 || cols <= 0) return RMOE_ERR_INVALID_ARGUMENT;
+    if (cols % 8 != 0) return RMOE_ERR_UNSUPPORTED_SHAPE;
+    int64_t n = 0;
+    if (__builtin_mul_overflow(rows, cols, &n) || n > (int64_t)1 << 56) return RMOE_ERR_UNSUPPORTED_SHAPE;
+    *empty = rows == 0;
+    return RMOE_OK;
+}
+
+int pick_variant_i8(int32_t variant, int64_t pairs, int32_t num_experts) {
+    return pick_variant(variant, pairs, num_experts);
+}
+
+int i8_gate_up_impl(const rmoe::I8Args &a, int32_t variant, int64_t pairs, void *stream) {
+    if (a.M == 0) return RMOE_OK;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    const int st = to_status(pick_variant_i8(variant, pairs, a.E) == RMOE_VARIANT_STREAM
+                                 ? rmoe::launch_i8_stream_gate_up(a, pairs, s)
+                                 : rmoe::launch_i8_tile_gate_up(a, s));
+    return st != RMOE_OK ? st : to_status(rmoe::launch_quantize_hidden_i8(a, pairs, s));
+}
+
+int i8_down_impl(const rmoe::I8Args &a, int32_t variant, int64_t pairs, void *stream) {
+    if (a.M == 0) return RMOE_OK;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (pick_variant_i8(variant, pairs, a.E) == RMOE_VARIANT_STREAM)
+        return to_status(rmoe::launch_i8_stream_down(a, pairs, s));
+    return to_status(rmoe::launch_i8_tile_down(a, s));
+}
+
+int check_i8_dims(int64_t hidden, int64_t intermediate, int32_t E, int64_t Tp, int64_t pairs, int32_t M,
+                  int32_t variant) {
+    const int st = check_dims(hidden, intermediate, E, Tp, M);
+    if (st != RMOE_OK) return st;
+    if (bad_variant(variant) || pairs < 0) return RMOE_ERR_INVALID_ARGUMENT;
+    return hidden > kMaxI8Sum || intermediate > kMaxI8Sum ? RMOE_ERR_UNSUPPORTED_SHAPE : RMOE_OK;
+}
+
+// The two stages' checked arguments.
+int i8_gate_up_args(rmoe::I8Args *a, const void *xc, const float *xs, const void *gc, const float *gsc, const void *uc,
+                    const float *us, const int32_t *gs, const int32_t *gpo, const int32_t *gidx, float *rows, void *hc,
+                    float *hs, int64_t hidden, int64_t intermediate, int32_t E, int32_t M) {
+    if (!xc || !xs || !gc || !gsc || !uc || !us || !gs || !gpo || (M > 0 && !gidx) || !rows || !hc || !hs)
+        return RMOE_ERR_INVALID_ARGUMENT;
+    if (!aligned16(xc) || !aligned16(gc) || !aligned16(uc) || !aligned16(gsc) || !aligned16(us) || !aligned16(rows) ||
+        !aligned16(hc) || !aligned4(xs) || !aligned4(hs) || !aligned4(gs) || !aligned4(gpo) || !aligned4(gidx))
+        return RMOE_ERR_MISALIGNED;
+    a->x = bytes(xc), a->xs = xs, a->w0 = bytes(gc), a->w0s = gsc, a->w1 = bytes(uc), a->w1s = us;
+    a->gs = gs, a->gpo = gpo, a->gidx = gidx;
+    a->rows = rows, a->yc = bytes(hc), a->ys = hs;
+    a->N = intermediate, a->K = hidden, a->E = E, a->M = M;
+    return RMOE_OK;
+}
+
+int i8_down_args(rmoe::I8Args *a, const void *hc, const float *hs, const void *dc, const float *ds, const float *rw,
+                 const int32_t *gs, const int32_t *go, const int32_t *gpo, const int32_t *gidx, void *out,
+                 int64_t hidden, int64_t intermediate, int32_t E, int64_t pairs, int32_t M) {
+    if (!hc || !hs || !dc || !ds || !gs || !go || !gpo || (M > 0 && !gidx) || !out || (pairs > 0 && !rw))
+        return RMOE_ERR_INVALID_ARGUMENT;
+    if (!aligned16(hc) || !aligned16(dc) || !aligned16(ds) || !aligned16(out) || !aligned4(hs) || !aligned4(rw) ||
+        !aligned4(gs) || !aligned4(go) || !aligned4(gpo) || !aligned4(gidx))
+        return RMOE_ERR_MISALIGNED;
+    a->x = bytes(hc), a->xs = hs, a->w0 = bytes(dc), a->w0s = ds, a->rw = rw;
+    a->gs = gs, a->go = go, a->gpo = gpo, a->gidx = gidx;
+    a->y = static_cast<_Float16 *>(out);
+    a->N = hidden, a->K = intermediate, a->E = E, a->M = M;
+    return RMOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int rmoe_quantize_int8(const void *x, int32_t type, int64_t rows, int64_t cols, void *codes, float *scales,
+                       void *stream) {
+    bool empty = false;
+    const int st = check_i8_sizes(type, rows, cols, &empty);
+    if (st != RMOE_OK) return st;
+    if (empty) return RMOE_OK;
+    if (!x || !codes || !scales) return RMOE_ERR_INVALID_ARGUMENT;
+    if (!aligned16(x) || !aligned16(codes) || !aligned4(scales)) return RMOE_ERR_MISALIGNED;
+    return to_status(rmoe::launch_quantize_i8(x, mx_type(type), rows, cols, bytes(codes), scales,
+                                              static_cast<hipStream_t>(stream)));
+}
+
+int rmoe_dequantize_int8(const void *codes, const float *scales, int32_t type, int64_t rows, int64_t cols, void *y,
+                         void *stream) {
+    bool empty = false;
+    const int st = check_i8_sizes(type, rows, cols, &empty);
+    if (st != RMOE_OK) return st;
+    if (empty) return RMOE_OK;
+    if (!codes || !scales || !y) return RMOE_ERR_INVALID_ARGUMENT;
+    if (!aligned16(y) || !aligned16(codes) || !aligned4(scales)) return RMOE_ERR_MISALIGNED;
+    return to_status(rmoe::launch_dequantize_i8(bytes(codes), scales, mx_type(type), rows, cols, y,
+                                                static_cast<hipStream_t>(stream)));
+}
+
+int rmoe_pack_int8_f16(const void *x, const float *topk_weights, const int32_t *prow, const int32_t *cpos,
+                       int64_t num_tokens, int32_t top_k, int64_t hidden, void *codes, float *scales, float *w_compact,
+                       int64_t total_padded_tokens, void *stream) {
+    if (top_k < 0 || total_padded_tokens < 0) return RMOE_ERR_INVALID_ARGUMENT;
+    bool empty = false;
+    const int st = check_i8_sizes(RMOE_TYPE_F16, num_tokens, hidden, &empty);
+    if (st != RMOE_OK) return st;
+    if (num_tokens > INT32_MAX) return RMOE_ERR_UNSUPPORTED_SHAPE;
+    if (empty || top_k == 0) return RMOE_OK;
+    if (!x || !topk_weights || !prow || !cpos || !codes || !scales || !w_compact) return RMOE_ERR_INVALID_ARGUMENT;
+    if (!aligned16(x) || !aligned16(codes) || !aligned4(scales) || !aligned4(topk_weights) || !aligned4(prow) ||
+        !aligned4(cpos) || !aligned4(w_compact))
+        return RMOE_ERR_MISALIGNED;
+    return to_status(rmoe::launch_pack_i8(static_cast<const _Float16 *>(x), topk_weights, prow, cpos, num_tokens,
+                                          top_k, hidden, total_padded_tokens, bytes(codes), scales, w_compact,
+                                          static_cast<hipStream_t>(stream)));
+}
+
+size_t rmoe_int8_workspace_bytes(int64_t total_padded_tokens, int64_t intermediate) {
+    if (total_padded_tokens <= 0 || intermediate <= 0) return 0;
+    return (size_t)total_padded_tokens * (5u * (size_t)intermediate + 4u);
+}
+
+int rmoe_pick_variant_int8(int32_t variant, int64_t num_pairs, int32_t num_experts) {
+    if (bad_variant(variant) || num_pairs < 0 || num_experts < 1) return RMOE_ERR_INVALID_ARGUMENT;
+    return pick_variant_i8(variant, num_pairs, num_experts);
+}
+
+int rmoe_gate_up_int8(const void *xc, const float *xs, const void *gc, const float *gsc, const void *uc,
+                      const float *us, const int32_t *gs, const int32_t *gpo, const int32_t *gidx, float *rows,
+                      void *hc, float *hs, int64_t hidden, int64_t intermediate, int32_t num_experts,
+                      int64_t total_padded_tokens, int64_t total_valid_tokens, int32_t num_blocks_m, int32_t variant,
+                      void *stream) {
+    int st = check_i8_dims(hidden, intermediate, num_experts, total_padded_tokens, total_valid_tokens, num_blocks_m,
+                           variant);
+    if (st != RMOE_OK) return st;
+    rmoe::I8Args a{};
+    st = i8_gate_up_args(&a, xc, xs, gc, gsc, uc, us, gs, gpo, gidx, rows, hc, hs, hidden, intermediate, num_experts,
+                         num_blocks_m);
+    return st != RMOE_OK ? st : i8_gate_up_impl(a, variant, total_valid_tokens, stream);
+}
+
+int rmoe_down_int8(const void *hc, const float *hs, const void *dc, const float *ds, const float *rw,
+                   const int32_t *gs, const int32_t *go, const int32_t *gpo, const int32_t *gidx, void *out,
+                   int64_t hidden, int64_t intermediate, int32_t num_experts, int64_t total_padded_tokens,
+                   int64_t total_valid_tokens, int32_t num_blocks_m, int32_t variant, void *stream) {
+    int st = check_i8_dims(hidden, intermediate, num_experts, total_padded_tokens, total_valid_tokens, num_blocks_m,
+                           variant);
+    if (st != RMOE_OK) return st;
+    rmoe::I8Args a{};
+    st = i8_down_args(&a, hc, hs, dc, ds, rw, gs, go, gpo, gidx, out, hidden, intermediate, num_experts,
+                      total_valid_tokens, num_blocks_m);
+    return st != RMOE_OK ? st : i8_down_impl(a, variant, total_valid_tokens, stream);
+}
+
+int rmoe_forward_int8(const void *xc, const float *xs, const void *gc, const float *gsc, const void *uc,
+                      const float *us, const void *dc, const float *ds, const float *rw, const int32_t *gs,
+                      const int32_t *go, const int32_t *gpo, const int32_t *gidx, void *workspace, void *out,
+                      int64_t hidden, int64_t intermediate, int32_t num_experts, int64_t total_padded_tokens,
+                      int64_t total_valid_tokens, int32_t num_blocks_m, int32_t variant, void *stream) {
+    int st = check_i8_dims(hidden, intermediate, num_experts, total_padded_tokens, total_valid_tokens, num_blocks_m,
+                           variant);
+    if (st != RMOE_OK) return st;
+    if (!workspace) return RMOE_ERR_INVALID_ARGUMENT;
+    // codes, rows in fp32, scales: rows of 128 bytes and more keep the alignment
+    unsigned char *hc = bytes(workspace);
+    const size_t n = (size_t)total_padded_tokens * (size_t)intermediate;
+    float *rows = reinterpret_cast<float *>(hc + n), *hs = rows + n;
+    rmoe::I8Args gu{}, dn{};
+    st = i8_gate_up_args(&gu, xc, xs, gc, gsc, uc, us, gs, gpo, gidx, rows, hc, hs, hidden, intermediate, num_experts,
+                         num_blocks_m);
+    if (st != RMOE_OK) return st;
+    st = i8_down_args(&dn, hc, hs, dc, ds, rw, gs, go, gpo, gidx, out, hidden, intermediate, num_experts,
+                      total_valid_tokens, num_blocks_m);
+    if (st != RMOE_OK) return st;
+    st = i8_gate_up_impl(gu, variant, total_valid_tokens, stream);
+    return st != RMOE_OK ? st : i8_down_impl(dn, variant, total_valid_tokens, stream);
+}
+
+}  // extern "C"
+
 // ---- training --------------------------------------------------------------
 
 namespace {

@@ -1,0 +1,288 @@
+// Tiled grouped GEMM on 8-bit integer tokens and weights, for blocks with
+// many rows.
+//
+// v_mfma_i32_32x32x32_i8 takes 16 bytes per lane and operand, as
+// v_mfma_f32_32x32x16_f16 does, and the same time: a K step of 128 bytes per
+// row holds 128 elements instead of 64, so the 256 x 256 tile, its DMAs and
+// its LDS traffic are those of the fp16 tiled kernels at twice the products.
+// The sums are exact 32-bit integers (K is limited so that they fit); the
+// token's and the channel's scale enter in the epilogue.
+//
+// A hidden row's scale needs the whole row, whose slices are spread over
+// workgroups: the gate/up epilogue writes the rows in fp32 and a second
+// launch turns them into codes.
+#include <atomic>
+
+#include "rmoe_i8.h"
+#include "rmoe_kloop.h"
+
+namespace rmoe {
+namespace {
+
+constexpr int BK = 128;             // K per step
+constexpr int SLOT = 256 * BK;      // 32 KB: a K step of 256 rows
+constexpr int NAS = 3, NBS = 2;     // A (weight) and B (token) slots: A runs two steps ahead, B one
+constexpr int B_OFF = NAS * SLOT;
+constexpr int LDS_BYTES = (NAS + NBS) * SLOT;
+static_assert(LDS_BYTES <= 160 * 1024, "LDS");
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x16 __attribute__((ext_vector_type(16)));
+
+struct I8Ops {
+    typedef i32x4 Frag;
+    static constexpr int AR = 1, BR = 1;
+    static constexpr int DMAS = 16, LATE = 8, PARTS = 4, PRE = 3, FILL = 0;
+
+    unsigned char *smem;
+    unsigned dwave;                      // LDS address of this wave's 64 rows of a slot
+    const unsigned char *tbase, *wbase;  // uniform: token rows, weight rows
+    unsigned row16;                      // bytes of 16 rows
+    unsigned off[2];                     // lane offsets of instructions 0 and 1 of a slot; j: 16 rows past j - 2
+    unsigned to[2], wo[2];
+    int nk;
+    int lane, lr, lh, arow, trow0;  // arow: first A row of this wave's tile 0; tile t at arow + 32 (t & 1) + astep (t / 2)
+    int astep;
+
+    __device__ __forceinline__ void begin() {
+        const int l = fresh(lane);
+        lr = l & 31;
+        lh = l >> 5;
+    }
+    __device__ __forceinline__ void dma(int d, int j) {
+        if (d < 8) {
+            const unsigned o = row_off(to, d);
+            dma16_sb(tbase + (int64_t)min(j + NBS, nk - 1) * BK, o, dwave + B_OFF + ((j + NBS) % NBS) * SLOT + 1024 * d);
+        } else {
+            const unsigned o = row_off(wo, d - 8);
+            dma16_sb(wbase + (int64_t)min(j + NAS, nk - 1) * BK, o, dwave + ((j + NAS) % NAS) * SLOT + 1024 * (d - 8));
+        }
+    }
+    // lane offset of instruction j of a slot, whose instructions go out in order
+    __device__ __forceinline__ unsigned row_off(unsigned (&o)[2], int j) {
+        o[j & 1] = j < 2 ? (unsigned)fresh((int)off[j]) : o[j & 1] + row16;
+        return o[j & 1];
+    }
+    __device__ __forceinline__ int row_a(int t) const { return arow + 32 * (t & 1) + astep * (t >> 1); }
+    __device__ __forceinline__ void read(int k, int s, int i, Frag *a, Frag *b) {
+        const int ch = 2 * s + lh;
+        if (i < 4)
+            a[i] = *(const Frag *)(smem + (k % NAS) * SLOT + lds_off(row_a(i) + lr, ch));
+        else
+            b[i - 4] = *(const Frag *)(smem + B_OFF + (k % NBS) * SLOT + lds_off(trow0 + 32 * (i - 4) + lr, ch));
+    }
+    __device__ __forceinline__ void step(int) {}
+    __device__ __forceinline__ void next() {}
+    // the accumulators are integers held in the K loop's fp32 registers
+    template <int S>
+    __device__ __forceinline__ void mma(const Frag &x, const Frag &y, f16x &c, int, int) {
+        c = __builtin_bit_cast(f16x, __builtin_amdgcn_mfma_i32_32x32x32_i8(x, y, __builtin_bit_cast(i32x16, c), 0, 0, 0));
+    }
+    __device__ __forceinline__ void publish(int) {}
+};
+
+__device__ __forceinline__ float sum_of(float c) { return (float)__builtin_bit_cast(int, c); }
+
+// What a lane and a wave hold for the whole launch, and the item's bases.
+template <bool DUAL>
+struct Tile {
+    const I8Args &a;
+    unsigned char *smem;
+    int wave, lane, ww, wt;  // ww: weight half, wt: token half (= block bx + wt)
+    int64_t N, K;
+    I8Ops p;
+
+    __device__ __forceinline__ Tile(const I8Args &args, unsigned char *s) : a(args), smem(s) {
+        wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        lane = threadIdx.x & 63;
+        ww = wave & 1;
+        wt = wave >> 1;
+        N = a.N;
+        K = a.K;
+        p.smem = smem;
+        p.nk = (int)(K / BK);
+        p.lane = lane;
+        p.trow0 = 128 * wt;
+        p.arow = DUAL ? 64 * ww : 128 * ww;  // gate/up: tiles 0, 1 gate rows, 2, 3 the same up rows
+        p.astep = DUAL ? 128 : 64;
+        // instruction j moves rows 64 w + 8 j + lane / 8 of a slot, physical
+        // chunk lane % 8; the rows' swizzle repeats with j's parity
+        p.row16 = (unsigned)(16 * K);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int r = 8 * j + (lane >> 3);
+            p.off[j] = (unsigned)(r * K + 16 * ((lane & 7) ^ lds_swz(r)));
+        }
+        p.dwave = (unsigned)(uintptr_t)smem + 64 * wave * BK;
+    }
+    __device__ __forceinline__ void set(const TileItem &it) {
+        const int64_t n0 = (int64_t)it.nt * (DUAL ? 128 : 256);
+        // weight rows 64 w .. of the slot: gate rows for waves 0, 1, up rows for 2, 3
+        int64_t wrow0 = n0 + (DUAL ? (64 * wave) & 127 : 64 * wave);
+        wrow0 = wrow0 < N ? wrow0 : N - 64;  // a narrow last slice: idle rows read valid rows
+        p.wbase = uniform((DUAL && wave >= 2 ? a.w1 : a.w0) + ((int64_t)it.e * N + wrow0) * K);
+        // an absent second block: its half reads the first block's rows
+        p.tbase = uniform(a.x + ((int64_t)it.bx * kBlockM + (it.rows1 > 0 ? 64 * wave : (64 * wave) & 127)) * K);
+    }
+    // valid rows and live token tiles of this wave
+    __device__ __forceinline__ int rows(const TileItem &it) const { return wt ? it.rows1 : it.rows0; }
+    __device__ __forceinline__ int tiles(const TileItem &it) const {
+        return DUAL || (int64_t)it.nt * 256 + 128 * ww < N ? (rows(it) + 31) / 32 : 0;
+    }
+    // Pieces of this wave's LDS for staging: 8 KB each in A's slot 2 and B's
+    // slot 1, which only its own DMAs fill (all landed after the K loop; no
+    // wave reads the ring after the last barrier, and the next item's first
+    // step goes to the other slots).
+    __device__ __forceinline__ unsigned char *piece(int i) const {
+        return smem + (i ? B_OFF + SLOT : 2 * SLOT) + wave * 8192;
+    }
+
+    // gate/up: hidden rows in fp32, 32 tokens of 64 features per piece (256
+    // bytes per row, 16-byte chunks XOR-swizzled by row), whole lines out.
+    // Register 4q + r of tile t holds feature 32 t + 8q + 4lh + r.
+    template <int NTT, class F>
+    __device__ __forceinline__ void hidden(const TileItem &it, f16x (&acc)[4][4], F &&fill) const {
+        const int ln = fresh(lane), lr = ln & 31, lh = ln >> 5, c = ln & 15;
+        const int64_t n0 = (int64_t)it.nt * 128 + 64 * ww, row0 = (int64_t)(it.bx + wt) * kBlockM;
+        const int myrows = rows(it);
+        f4 gs[2][4], us[2][4];
+        float xs[4];
+        if constexpr (NTT > 0) {
+            const int64_t so = (int64_t)it.e * N + n0 + 4 * lh;
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    gs[t][q] = *(const f4 *)(a.w0s + so + 32 * t + 8 * q);
+                    us[t][q] = *(const f4 *)(a.w1s + so + 32 * t + 8 * q);
+                }
+#pragma unroll
+            for (int u = 0; u < NTT; ++u) xs[u] = a.xs[row0 + 32 * u + lr];
+            wait_vm<0>();  // the scales landed: a later wait for them would wait for the next item's DMAs too
+        }
+        fill();
+        float *ybase = a.rows + row0 * N + n0 + 4 * c;
+#pragma unroll
+        for (int u = 0; u < NTT; ++u) {
+            unsigned char *st = piece(u & 1);
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    f4 h;
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const float g = sum_of(acc[t][u][4 * q + r]) * (xs[u] * gs[t][q][r]);
+                        const float v = sum_of(acc[t + 2][u][4 * q + r]) * (xs[u] * us[t][q][r]);
+                        h[r] = silu(g) * v;
+                    }
+                    *(f4 *)(st + lr * 256 + (((8 * t + 2 * q + lh) ^ (lr & 15)) << 4)) = h;
+                }
+            __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): this wave's staging writes are done
+            f4 v[8];  // read together: one LDS round trip, not eight
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int r = 4 * j + (ln >> 4);
+                v[j] = *(const f4 *)(st + r * 256 + ((c ^ (r & 15)) << 4));
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int row = 32 * u + 4 * j + (ln >> 4);
+                if (row < myrows) *(f4 *)(ybase + (int64_t)row * N) = v[j];
+            }
+        }
+    }
+
+    // down: out rows, 64 at a time staged through LDS for whole-line stores:
+    // 128 columns per row, 16-byte chunks XOR-swizzled by row.
+    template <int NTT, class F>
+    __device__ __forceinline__ void out(const TileItem &it, f16x (&acc)[4][4], F &&fill) const {
+        const int ln = fresh(lane), lr = ln & 31, lh = ln >> 5;
+        const int64_t row0 = (int64_t)(it.bx + wt) * kBlockM, n0 = (int64_t)it.nt * 256 + 128 * ww;
+        const int myrows = rows(it);
+        f4 ds[4][4];
+        float w[4];
+        if constexpr (NTT > 0) {
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    ds[t][q] = *(const f4 *)(a.w0s + (int64_t)it.e * N + n0 + 32 * t + 8 * q + 4 * lh);
+            const float *rwe = a.rw + table(a.go)[it.e] + it.off + kBlockM * wt;
+#pragma unroll
+            for (int u = 0; u < NTT; ++u) {
+                w[u] = 0.f;
+                if (32 * u + lr < myrows) w[u] = a.xs[row0 + 32 * u + lr] * rwe[32 * u + lr];
+            }
+            wait_vm<0>();  // as in hidden()
+        }
+        fill();
+        _Float16 *ybase = a.y + row0 * N + n0;
+        const int c = ln & 15;
+#pragma unroll
+        for (int u0 = 0; u0 < NTT; u0 += 2) {
+            __builtin_amdgcn_sched_barrier(0);  // no accumulator is copied out early: registers
+#pragma unroll
+            for (int u = u0; u < u0 + 2 && u < NTT; ++u)
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const f16x &o = acc[t][u];
+                        const f4 d = ds[t][q];
+                        *(h4 *)(piece(u - u0) + lr * 256 + (((4 * t + q) ^ (lr & 15)) << 4) + 8 * lh) =
+                            to_h4(sum_of(o[4 * q + 0]) * (w[u] * d[0]), sum_of(o[4 * q + 1]) * (w[u] * d[1]),
+                                  sum_of(o[4 * q + 2]) * (w[u] * d[2]), sum_of(o[4 * q + 3]) * (w[u] * d[3]));
+                    }
+            __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): this wave's staging writes are done
+#pragma unroll
+            for (int u = u0; u < u0 + 2 && u < NTT; ++u) {
+                h8 v[8];  // read together: one LDS round trip, not eight
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int r = 4 * j + (ln >> 4);
+                    v[j] = *(const h8 *)(piece(u - u0) + r * 256 + ((c ^ (r & 15)) << 4));
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int row = 32 * u + 4 * j + (ln >> 4);
+                    if (row < myrows) *(h8 *)(ybase + (int64_t)row * N + 8 * c) = v[j];
+                }
+            }
+        }
+    }
+
+    template <int NTT, class F>
+    __device__ __forceinline__ bool finish(const TileItem &it, f16x (&acc)[4][4], F &&fill) const {
+        if constexpr (DUAL)
+            hidden<NTT>(it, acc, fill);
+        else
+            out<NTT>(it, acc, fill);
+        return NTT == 4 && rows(it) == kBlockM;  // a whole block of rows: 32 stores
+    }
+};
+
+template <bool DUAL>
+__global__ __launch_bounds__(256) void i8_tile_kernel(I8Args a, int NT) {
+    extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
+    Tile<DUAL> tile(a, smem);
+    run_items(tile, a.gs, a.gpo, a.gidx, a.E, NT);
+}
+
+template <bool DUAL>
+hipError_t launch(const I8Args &a, int NT, hipStream_t s) {
+    unsigned grid = 0;
+    hipError_t e = cu_grid(grid);
+    if (e != hipSuccess) return e;
+    static std::atomic<uint64_t> lds_set{0};
+    e = lds_opt_in_once((const void *)i8_tile_kernel<DUAL>, LDS_BYTES, lds_set);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(i8_tile_kernel<DUAL>, dim3(grid), dim3(256), LDS_BYTES, s, a, NT);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_i8_tile_gate_up(const I8Args &a, hipStream_t s) { return launch<true>(a, (int)(a.N / 128), s); }
+hipError_t launch_i8_tile_down(const I8Args &a, hipStream_t s) { return launch<false>(a, (int)((a.N + 255) / 256), s); }
+
+}  // namespace rmoe

@@ -125,6 +125,38 @@ hipError_t launch_mx_tile_down(const MxArgs &a, hipStream_t s);
 hipError_t launch_mx_stream_gate_up(const MxArgs &a, int64_t pairs, hipStream_t s);
 hipError_t launch_mx_stream_down(const MxArgs &a, int64_t pairs, hipStream_t s);
 
+// ---- 8-bit integers (rmoe_i8.h)
+
+hipError_t launch_quantize_i8(const void *x, MxType type, int64_t rows, int64_t cols, unsigned char *codes,
+                              float *scales, hipStream_t s);
+hipError_t launch_dequantize_i8(const unsigned char *codes, const float *scales, MxType type, int64_t rows,
+                                int64_t cols, void *y, hipStream_t s);
+hipError_t launch_pack_i8(const _Float16 *x, const float *topk_w, const int32_t *prow, const int32_t *cpos, int64_t T,
+                          int32_t k, int64_t H, int64_t Tp, unsigned char *codes, float *scales, float *w_compact,
+                          hipStream_t s);
+
+// One stage of the routed FFN on 8-bit rows, as StageArgs.
+struct I8Args {
+    const unsigned char *x;                    // token codes [Tp, K]
+    const float *xs;                           // their scales [Tp]
+    const unsigned char *w0, *w1;              // weight codes [E, N, K]; w1 gate/up only
+    const float *w0s, *w1s;                    // their scales [E, N]
+    const float *rw;                           // [pairs] compact order (down only)
+    const int32_t *gs, *go, *gpo, *gidx;
+    float *rows;                               // gate/up: hidden rows [Tp, N] in fp32
+    unsigned char *yc;                         // gate/up: their codes [Tp, N]
+    float *ys;                                 // and scales [Tp]
+    _Float16 *y;                               // down: out [Tp, N]
+    int64_t K, N;
+    int32_t E, M;
+};
+// The products of the gate/up stage write rows, the quantisation yc and ys.
+hipError_t launch_i8_tile_gate_up(const I8Args &a, hipStream_t s);
+hipError_t launch_i8_tile_down(const I8Args &a, hipStream_t s);
+hipError_t launch_i8_stream_gate_up(const I8Args &a, int64_t pairs, hipStream_t s);
+hipError_t launch_i8_stream_down(const I8Args &a, int64_t pairs, hipStream_t s);
+hipError_t launch_quantize_hidden_i8(const I8Args &a, int64_t pairs, hipStream_t s);
+
 // ---- training (rmoe_train.hip)
 
 struct TrainArgs {
