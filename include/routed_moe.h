@@ -424,6 +424,65 @@ RMOE_API int rmoe_router_f16(const void *x, const void *router_w, int64_t num_to
                              int32_t *topk_ids, float *topk_weights, void *stream);
 
 /*
+ * The router of a training batch: rmoe_router_f16 (the same ids and scores,
+ * bit for bit) that also keeps what its backward pass needs, counts the pairs
+ * per expert and gives the two losses that keep a router in balance:
+ *   probs [num_tokens, E] fp32, lse [num_tokens] fp32: softmax(logits[t]) and
+ *     log(sum_e exp(logits[t, e]));
+ *   counts [E + 1] int32: the pairs that chose each expert, then n, the
+ *     tokens that count;
+ *   losses [2] fp32: balance = E / (top_k n) * sum_e counts[e] * P[e], P[e]
+ *     the mean of probs[t, e] over the n tokens (1 where all experts are
+ *     equally likely), and z = mean of lse^2; both 0 if n = 0.
+ * token_mask [num_tokens] uint8 or NULL: tokens whose byte is 0 are left out
+ * (the padding of a batch; their rows may hold anything): ids -1, weights,
+ * probs and lse 0, in no count and no loss.  The contract builder leaves
+ * pairs with id -1 out of its tables.  A token with a NaN logit gets the id
+ * 2^31 - 1 (left out likewise), NaN probabilities and NaN losses.
+ * scratch: rmoe_router_train_scratch_bytes(num_tokens, E) bytes, contents
+ * irrelevant on entry.  Sums run in an order fixed by the sizes: equal calls
+ * give equal bits.  Shapes: as rmoe_router_f16 with top_k >= 1, hidden at
+ * most 2^20, num_tokens * top_k at most 2^31 - 1.  fp16 tensors 16-byte, the
+ * rest (but the mask) 4-byte aligned.  Two launches on `stream`.
+ */
+RMOE_API size_t rmoe_router_train_scratch_bytes(int64_t num_tokens, int32_t num_experts);
+RMOE_API int rmoe_router_train_f16(const void *x, const void *router_w, const uint8_t *token_mask,
+                                   int64_t num_tokens, int64_t hidden, int32_t num_experts, int32_t top_k,
+                                   int32_t *topk_ids, float *topk_weights, float *probs, float *lse,
+                                   int32_t *counts, float *losses, void *scratch, void *stream);
+
+/*
+ * Backward of rmoe_router_train_f16.  g[t, j]: the gradient of routed weight
+ * j of token t; drw [num_tokens * top_k] fp32 holds it in pair order, or,
+ * with compact_pos_of_pair (the contract's, not NULL), in compact order, as
+ * rmoe_backward_f16 leaves it: g = drw[compact_pos_of_pair[pair]], 0 for a
+ * position outside [0, num_tokens * top_k).  dlosses [2] fp32 (device) or
+ * NULL: the gradients a and b of the balance and the z loss.  With n =
+ * counts[E] (counts are constants here: a caller may sum them over ranks),
+ *   dp[t, e] = sum_{j: ids[t, j] = e} g[t, j] + a E counts[e] / (top_k n^2)
+ *   dl[t, e] = p (dp - sum_i p[t, i] dp[t, i]) + 2 b lse[t] p / n, p = probs[t, e];
+ *     0 for tokens left out by token_mask; ids outside [0, E) add nothing
+ *   dx = fp16( dl . router_w + dx_add )         [num_tokens, hidden]
+ *   drouter_w[e] = sum_t dl[t, e] x[t]          [E, hidden] fp32
+ * dx_add [num_tokens, hidden] fp16 or NULL: the gradient that reached the
+ * tokens through the experts (rmoe_combine_f16); it may be dx itself.  dl is
+ * fp32; for the products it is split into two fp16 values (22 bits).  Every
+ * row of dx is written; rows of x that are left out are not read.
+ * scratch: rmoe_router_backward_scratch_bytes(num_tokens, hidden, E) bytes,
+ * 16-byte aligned, contents irrelevant on entry.  Sums run in a fixed order.
+ * Shapes and alignment as rmoe_router_train_f16 (drouter_w and dx_add 16).
+ * At most five launches on `stream`.
+ */
+RMOE_API size_t rmoe_router_backward_scratch_bytes(int64_t num_tokens, int64_t hidden, int32_t num_experts);
+RMOE_API int rmoe_router_backward_f16(const void *x, const void *router_w, const uint8_t *token_mask,
+                                      const int32_t *topk_ids, const float *probs, const float *lse,
+                                      const int32_t *counts, const float *drw,
+                                      const int32_t *compact_pos_of_pair, const float *dlosses,
+                                      const void *dx_add, void *dx, float *drouter_w, void *scratch,
+                                      int64_t num_tokens, int64_t hidden, int32_t num_experts, int32_t top_k,
+                                      void *stream);
+
+/*
  * MXFP4: microscaled 4-bit floating point.  A row of `cols` elements is cut
  * into blocks of 32; a block shares the scale 2^(b - 127), held as its
  * exponent byte b, and each element is an E2M1 code (sign bit, then the

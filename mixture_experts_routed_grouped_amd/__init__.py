@@ -61,6 +61,10 @@ _SIGS = {
     "rmoe_combine_f16": ([_P, _P, _I64, _I32, _I64, _P, _I64, _P], ctypes.c_int),
     "rmoe_contract_workspace_bytes": ([_I64, _I32], ctypes.c_size_t),
     "rmoe_router_f16": ([_P, _P, _I64, _I64, _I32, _I32, _P, _P, _P], ctypes.c_int),
+    "rmoe_router_train_scratch_bytes": ([_I64, _I32], ctypes.c_size_t),
+    "rmoe_router_train_f16": ([_P] * 3 + [_I64, _I64, _I32, _I32] + [_P] * 8, ctypes.c_int),
+    "rmoe_router_backward_scratch_bytes": ([_I64, _I64, _I32], ctypes.c_size_t),
+    "rmoe_router_backward_f16": ([_P] * 14 + [_I64, _I64, _I32, _I32, _P], ctypes.c_int),
     "rmoe_build_contract_device": ([_P, _I64, _I32, _I32, _P, _P, _P, _P, _I64, _P, _P, _P, _P, _P,
                                     _P, ctypes.c_size_t, _P], ctypes.c_int),
     "rmoe_mxfp4_chunks": ([_I64], _I64),
@@ -473,6 +477,86 @@ def router(x, router_w, top_k: int, topk_ids=None, topk_weights=None, stream=Non
                                _dev(topk_weights, torch.float32, "topk_weights"), _stream(x, stream))
     _check(st, "rmoe_router_f16")
     return topk_ids, topk_weights
+
+
+_ROUTER_OUT = ("topk_ids", "topk_weights", "probs", "lse", "counts", "losses")
+
+
+def router_train(x, router_w, top_k: int, token_mask=None, out=None, stream=None) -> dict:
+    """The router of a training batch (rmoe_router_train_f16): ``router`` that
+    also keeps what ``router_backward`` needs.  ``token_mask`` [T] (uint8 or
+    bool, or None): tokens where it is 0 are left out (ids -1, weights 0, in no
+    count and no loss).  Returns device tensors ``topk_ids`` [T, k] int32,
+    ``topk_weights`` [T, k], ``probs`` [T, E] and ``lse`` [T] float32,
+    ``counts`` [E + 1] int32 (pairs per expert, then the tokens that count) and
+    ``losses`` [2] float32 (balance, z).  ``out``: the result of an earlier
+    call for the same T, E and k, to be written instead of new tensors."""
+    torch = _torch()
+    i32, f32 = torch.int32, torch.float32
+    dev = _gpu(x, "x")
+    T, H = x.shape
+    E, k = router_w.shape[0], int(top_k)
+    px, pw = _arg(dev, "x", x, torch.float16), _arg(dev, "router_w", router_w, torch.float16, E, H)
+    mask = _mask(dev, token_mask, T)
+    words = int(lib().rmoe_router_train_scratch_bytes(T, E)) // 4
+    if out is None:
+        shapes = ((T, k), (T, k), (T, E), (T,), (E + 1,), (2,))
+        types = (i32, f32, f32, f32, i32, f32)
+        out = {n: _empty(s, t, dev, stream) for n, s, t in zip(_ROUTER_OUT, shapes, types)}
+        out["_scratch"] = _empty((words,), f32, dev, stream)  # kept alive until the stream has used it
+    elif out["_scratch"].numel() < words:
+        raise ValueError("out was made for another shape")
+    _call("rmoe_router_train_f16", dev, stream, px, pw, mask, T, H, E, k,
+          _arg(dev, "topk_ids", out["topk_ids"], i32, T, k), _arg(dev, "topk_weights", out["topk_weights"], f32, T, k),
+          _arg(dev, "probs", out["probs"], f32, T, E), _arg(dev, "lse", out["lse"], f32, T),
+          _arg(dev, "counts", out["counts"], i32, E + 1), _arg(dev, "losses", out["losses"], f32, 2),
+          _arg(dev, "_scratch", out["_scratch"], f32))
+    return out
+
+
+def _mask(dev, token_mask, T):
+    """Address of a token mask, None for none."""
+    if token_mask is None:
+        return None
+    torch = _torch()
+    return _arg(dev, "token_mask", token_mask, torch.bool if token_mask.dtype is torch.bool else torch.uint8, T)
+
+
+def router_backward_scratch_bytes(num_tokens: int, hidden: int, num_experts: int) -> int:
+    """Bytes of the scratch that ``router_backward`` needs."""
+    return int(lib().rmoe_router_backward_scratch_bytes(int(num_tokens), int(hidden), int(num_experts)))
+
+
+def router_backward(x, router_w, topk_ids, probs, lse, counts, drw, dlosses, dx, drouter_w, scratch,
+                    compact_pos_of_pair=None, token_mask=None, dx_add=None, stream=None):
+    """Backward pass of ``router_train`` (rmoe_router_backward_f16).  ``drw``:
+    the gradients of the routed weights, one per pair, in pair order or, with
+    the contract's ``compact_pos_of_pair``, in compact order as ``backward``
+    leaves them; ``dlosses`` [2] float32 (or None): the gradients of the two
+    losses.  Writes ``dx`` [T, H] float16, the tokens' gradient through the
+    router plus ``dx_add`` [T, H] (their gradient through the experts; it may
+    be ``dx`` itself), and ``drouter_w`` [E, H] float32.  ``scratch``: at least
+    ``router_backward_scratch_bytes(T, H, E)`` bytes."""
+    torch = _torch()
+    f16, i32, f32 = torch.float16, torch.int32, torch.float32
+    dev = _gpu(x, "x")
+    (T, H), E = x.shape, router_w.shape[0]
+    k = topk_ids.shape[-1]
+    work = _arg(dev, "scratch", scratch, scratch.dtype)
+    if scratch.numel() * scratch.element_size() < router_backward_scratch_bytes(T, H, E):
+        raise ValueError("scratch too small")
+    if compact_pos_of_pair is not None and compact_pos_of_pair.numel() != T * k:
+        raise ValueError("compact_pos_of_pair must have num_tokens * top_k entries")
+    if drw.numel() != T * k:
+        raise ValueError("drw must have num_tokens * top_k entries")
+    _call("rmoe_router_backward_f16", dev, stream, _arg(dev, "x", x, f16),
+          _arg(dev, "router_w", router_w, f16, E, H), _mask(dev, token_mask, T),
+          _arg(dev, "topk_ids", topk_ids, i32, T, k), _arg(dev, "probs", probs, f32, T, E),
+          _arg(dev, "lse", lse, f32, T), _arg(dev, "counts", counts, i32, E + 1), _arg(dev, "drw", drw, f32),
+          None if compact_pos_of_pair is None else _arg(dev, "compact_pos_of_pair", compact_pos_of_pair, i32),
+          None if dlosses is None else _arg(dev, "dlosses", dlosses, f32, 2),
+          None if dx_add is None else _arg(dev, "dx_add", dx_add, f16, T, H), _arg(dev, "dx", dx, f16, T, H),
+          _arg(dev, "drouter_w", drouter_w, f32, E, H), work, T, H, E, k)
 
 
 def contract_workspace_bytes(num_pairs: int, num_experts: int) -> int:

@@ -21,7 +21,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "librmoe.so")
 PHASE_LIB = os.path.join(PKG, "librmoe_phase.so")
 SOURCES = ["rmoe_api.cpp", "rmoe_stream.hip", "rmoe_tile.hip", "rmoe_pack.hip", "rmoe_contract.hip", "rmoe_router.hip",
-           "rmoe_mx.hip", "rmoe_mx_tile.hip", "rmoe_mx_stream.hip", "rmoe_i8.hip", "rmoe_i8_tile.hip", "rmoe_i8_stream.hip", "rmoe_train.hip"]
+           "rmoe_mx.hip", "rmoe_mx_tile.hip", "rmoe_mx_stream.hip", "rmoe_i8.hip", "rmoe_i8_tile.hip", "rmoe_i8_stream.hip", "rmoe_train.hip", "rmoe_router_train.hip"]
 ARCH = "gfx950"
 
 # -packed-fp32-ops: keep the compiler from forming packed fp32 VALU ops.

@@ -562,6 +562,71 @@ int rmoe_router_f16(const void *x, const void *router_w, int64_t num_tokens, int
                                          static_cast<hipStream_t>(stream)));
 }
 
+// Sizes of the training router, forward and backward.
+static int check_router_train(int64_t num_tokens, int64_t hidden, int32_t num_experts, int32_t top_k) {
+    if (num_tokens < 0 || hidden <= 0 || num_experts < 1 || top_k < 1 || top_k > num_experts)
+        return RMOE_ERR_INVALID_ARGUMENT;
+    if (num_experts > 256 || top_k > 32 || hidden % 64 != 0 || hidden > (int64_t)1 << 20 ||
+        num_tokens > INT32_MAX / top_k)
+        return RMOE_ERR_UNSUPPORTED_SHAPE;
+    return RMOE_OK;
+}
+
+size_t rmoe_router_train_scratch_bytes(int64_t num_tokens, int32_t num_experts) {
+    if (num_tokens <= 0 || num_experts < 1 || num_experts > 256 || num_tokens > INT32_MAX) return 0;
+    return (size_t)rmoe::router_train_parts(num_tokens) * (2u * (size_t)num_experts + 2u) * 4u;
+}
+
+int rmoe_router_train_f16(const void *x, const void *router_w, const uint8_t *token_mask, int64_t num_tokens,
+                          int64_t hidden, int32_t num_experts, int32_t top_k, int32_t *topk_ids, float *topk_weights,
+                          float *probs, float *lse, int32_t *counts, float *losses, void *scratch, void *stream) {
+    const int st = check_router_train(num_tokens, hidden, num_experts, top_k);
+    if (st != RMOE_OK) return st;
+    if (!router_w || !counts || !losses ||
+        (num_tokens > 0 && (!x || !topk_ids || !topk_weights || !probs || !lse || !scratch)))
+        return RMOE_ERR_INVALID_ARGUMENT;
+    if (!aligned16(x) || !aligned16(router_w) || !aligned4(topk_ids) || !aligned4(topk_weights) || !aligned4(probs) ||
+        !aligned4(lse) || !aligned4(counts) || !aligned4(losses) || !aligned4(scratch))
+        return RMOE_ERR_MISALIGNED;
+    rmoe::RouterTrainArgs a{};
+    a.x = static_cast<const _Float16 *>(x), a.w = static_cast<const _Float16 *>(router_w), a.mask = token_mask;
+    a.T = num_tokens, a.H = hidden, a.E = num_experts, a.k = top_k;
+    a.ids = topk_ids, a.vals = topk_weights, a.probs = probs, a.lse = lse, a.counts = counts, a.losses = losses;
+    const int64_t parts = rmoe::router_train_parts(num_tokens);
+    a.part_p = static_cast<float *>(scratch);
+    a.part_c = reinterpret_cast<int32_t *>(a.part_p + parts * num_experts);
+    a.part_z = reinterpret_cast<float *>(a.part_c + parts * (num_experts + 1));
+    return to_status(rmoe::launch_router_train(a, static_cast<hipStream_t>(stream)));
+}
+
+size_t rmoe_router_backward_scratch_bytes(int64_t num_tokens, int64_t hidden, int32_t num_experts) {
+    if (check_router_train(num_tokens, hidden, num_experts, 1) != RMOE_OK) return 0;
+    return (size_t)rmoe::router_backward_scratch(num_tokens, hidden, num_experts);
+}
+
+int rmoe_router_backward_f16(const void *x, const void *router_w, const uint8_t *token_mask, const int32_t *topk_ids,
+                             const float *probs, const float *lse, const int32_t *counts, const float *drw,
+                             const int32_t *compact_pos_of_pair, const float *dlosses, const void *dx_add, void *dx,
+                             float *drouter_w, void *scratch, int64_t num_tokens, int64_t hidden, int32_t num_experts,
+                             int32_t top_k, void *stream) {
+    const int st = check_router_train(num_tokens, hidden, num_experts, top_k);
+    if (st != RMOE_OK) return st;
+    if (!router_w || !counts || !drouter_w || !scratch ||
+        (num_tokens > 0 && (!x || !topk_ids || !probs || !lse || !drw || !dx)))
+        return RMOE_ERR_INVALID_ARGUMENT;
+    if (!aligned16(x) || !aligned16(router_w) || !aligned16(dx_add) || !aligned16(dx) || !aligned16(drouter_w) ||
+        !aligned16(scratch) || !aligned4(topk_ids) || !aligned4(probs) || !aligned4(lse) || !aligned4(counts) ||
+        !aligned4(drw) || !aligned4(compact_pos_of_pair) || !aligned4(dlosses))
+        return RMOE_ERR_MISALIGNED;
+    rmoe::RouterBackArgs a{};
+    a.x = static_cast<const _Float16 *>(x), a.w = static_cast<const _Float16 *>(router_w), a.mask = token_mask;
+    a.ids = topk_ids, a.probs = probs, a.lse = lse, a.counts = counts, a.drw = drw, a.cpos = compact_pos_of_pair;
+    a.dlosses = dlosses, a.add = static_cast<const _Float16 *>(dx_add), a.dx = static_cast<_Float16 *>(dx);
+    a.dw = drouter_w, a.scratch = static_cast<unsigned char *>(scratch);
+    a.T = num_tokens, a.H = hidden, a.E = num_experts, a.k = top_k;
+    return to_status(rmoe::launch_router_backward(a, static_cast<hipStream_t>(stream)));
+}
+
 }  // extern "C"
 
 // ---- MXFP4 -----------------------------------------------------------------

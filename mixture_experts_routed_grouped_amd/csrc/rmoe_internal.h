@@ -88,6 +88,44 @@ hipError_t launch_combine(const _Float16 *out, const int32_t *prow, int64_t T, i
 hipError_t launch_router(const _Float16 *x, const _Float16 *w, int64_t T, int64_t H, int32_t E,
                          int32_t k, int32_t *ids, float *vals, hipStream_t s);
 
+// The training router: what the forward keeps, and the losses.
+struct RouterTrainArgs {
+    const _Float16 *x, *w;  // [T, H], [E, H]
+    const uint8_t *mask;    // [T], 0: the token is left out; null: none is
+    int64_t T, H;
+    int32_t E, k;
+    int32_t *ids;           // [T, k]
+    float *vals;            // [T, k]
+    float *probs, *lse;     // [T, E], [T]
+    int32_t *counts;        // [E + 1]: pairs per expert, tokens that count
+    float *losses;          // [2]: balance, z
+    float *part_p;          // [parts, E] sums of probabilities
+    int32_t *part_c;        // [parts, E + 1] counts
+    float *part_z;          // [parts] sums of lse^2
+};
+int64_t router_train_parts(int64_t T);  // at most
+hipError_t launch_router_train(const RouterTrainArgs &a, hipStream_t s);
+
+// Its backward pass (rmoe_router_train.hip).
+struct RouterBackArgs {
+    const _Float16 *x, *w;  // [T, H], [E, H]
+    const uint8_t *mask;
+    const int32_t *ids;     // [T, k]
+    const float *probs, *lse;
+    const int32_t *counts;  // [E + 1]
+    const float *drw;       // [pairs]: in pair order, or in compact order with cpos
+    const int32_t *cpos;    // [T, k] or null
+    const float *dlosses;   // [2] or null
+    const _Float16 *add;    // [T, H] or null
+    _Float16 *dx;           // [T, H]
+    float *dw;              // [E, H]
+    unsigned char *scratch;
+    int64_t T, H;
+    int32_t E, k;
+};
+int64_t router_backward_scratch(int64_t T, int64_t H, int32_t E);
+hipError_t launch_router_backward(const RouterBackArgs &a, hipStream_t s);
+
 // Device-side check of the contract tables: writes the number of violated
 // rules to *violations (one workgroup, no memset needed).
 hipError_t launch_validate(const int32_t *gs, const int32_t *go, const int32_t *gpo,

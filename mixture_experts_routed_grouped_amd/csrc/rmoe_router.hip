@@ -53,12 +53,13 @@ __device__ __forceinline__ bool better(float s, int e, float s2, int e2) {
     return s > s2 || (s == s2 && e < e2);
 }
 
-template <int EP, int TOK>
-__global__ __launch_bounds__(256) void router_kernel(const _Float16 *__restrict__ x,
-                                                     const _Float16 *__restrict__ w, int64_t T,
-                                                     int64_t H, int32_t E, int32_t k,
-                                                     int32_t *__restrict__ ids,
-                                                     float *__restrict__ vals) {
+// TRAIN: the training forward, which also keeps the probabilities and each
+// token's logsumexp, leaves out masked tokens and sums what the losses need
+// over the workgroup's tokens.
+template <int EP, int TOK, bool TRAIN>
+__device__ __forceinline__ void router_body(const _Float16 *__restrict__ x, const _Float16 *__restrict__ w, int64_t T,
+                                            int64_t H, int32_t E, int32_t k, int32_t *__restrict__ ids,
+                                            float *__restrict__ vals, const RouterTrainArgs &tr) {
     using C = RouterCfg<EP, TOK>;
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
     const int64_t t0 = (int64_t)blockIdx.x * TOK;
@@ -177,6 +178,26 @@ __global__ __launch_bounds__(256) void router_kernel(const _Float16 *__restrict_
     const float inv = 1.0f / sum;
     uint64_t taken = 0;  // bit i: expert sub + 4i already chosen
     const bool live = tok < TOK && t0 + tok < T;
+    // behind the logits: 1 / sum of each token (0: left out), the
+    // workgroup's pairs per expert, and its tokens and their lse^2
+    static_assert(!TRAIN || C::LDS_BYTES >= C::TROWS * EP * 4 + (TOK + EP + 2 * TOK) * 4, "LDS behind the logits");
+    float *invs = L + C::TROWS * EP;
+    int32_t *cnt = reinterpret_cast<int32_t *>(invs + TOK);
+    float *zs = reinterpret_cast<float *>(cnt + EP), *on = zs + TOK;
+    bool counts = live;
+    if constexpr (TRAIN) {
+        __syncthreads();  // idle threads (tok >= TOK) wrote rows there too
+        counts = live && (tr.mask == nullptr || tr.mask[t0 + tok] != 0);
+        for (int e = tid; e < EP; e += 256) cnt[e] = 0;
+        if (tok < TOK && sub == 0) {
+            const float lse = counts ? m + __builtin_amdgcn_logf(sum) * 0.6931471805599453f : 0.f;
+            invs[tok] = counts ? inv : 0.f;
+            zs[tok] = lse * lse;
+            on[tok] = counts ? 1.f : 0.f;
+            if (live) tr.lse[t0 + tok] = lse;
+        }
+        __syncthreads();
+    }
     for (int j = 0; j < k; ++j) {
         float bs = -1.f;
         int be = 0x7fffffff;
@@ -199,9 +220,116 @@ __global__ __launch_bounds__(256) void router_kernel(const _Float16 *__restrict_
         }
         if ((be & 3) == sub) taken |= 1ull << (be >> 2);
         if (live && sub == 0) {
-            ids[(t0 + tok) * k + j] = be;
-            vals[(t0 + tok) * k + j] = bs;
+            if constexpr (TRAIN) {
+                ids[(t0 + tok) * k + j] = counts ? be : -1;
+                vals[(t0 + tok) * k + j] = counts ? bs : 0.f;
+                // a row of NaN picks no expert (be past E)
+                if (counts && be < E) atomicAdd(&cnt[be], 1);
+            } else {
+                ids[(t0 + tok) * k + j] = be;
+                vals[(t0 + tok) * k + j] = bs;
+            }
         }
+    }
+    if constexpr (TRAIN) {
+        __syncthreads();
+        const int nt = T - t0 < TOK ? (int)(T - t0) : TOK;
+        // probabilities: the workgroup's tokens are one contiguous piece
+        for (int i = tid; i < nt * E; i += 256) {
+            const int t = i / E, e = i - t * E;
+            tr.probs[t0 * E + i] = invs[t] > 0.f ? L[t * EP + e] * invs[t] : on[t] * invs[t];
+        }
+        // sums over the workgroup's tokens, in a fixed order
+        if (tid < E) {
+            float s = 0.f;
+#pragma unroll 8
+            for (int t = 0; t < nt; ++t) s += invs[t] > 0.f ? L[t * EP + tid] * invs[t] : on[t] * invs[t];
+            tr.part_p[(int64_t)blockIdx.x * E + tid] = s;
+            tr.part_c[(int64_t)blockIdx.x * (E + 1) + tid] = cnt[tid];
+        }
+        if (wave == 3) {  // zs and on hold TOK entries, zeros past the last token
+            float z = lane < TOK ? zs[lane] : 0.f, n = lane < TOK ? on[lane] : 0.f;
+#pragma unroll
+            for (int d = 1; d < 64; d <<= 1) {
+                z += __shfl_xor(z, d);
+                n += __shfl_xor(n, d);
+            }
+            if (lane == 0) {
+                tr.part_z[blockIdx.x] = z;
+                tr.part_c[(int64_t)blockIdx.x * (E + 1) + E] = (int)n;
+            }
+        }
+    }
+}
+
+template <int EP, int TOK>
+__global__ __launch_bounds__(256) void router_kernel(const _Float16 *__restrict__ x,
+                                                     const _Float16 *__restrict__ w, int64_t T,
+                                                     int64_t H, int32_t E, int32_t k,
+                                                     int32_t *__restrict__ ids,
+                                                     float *__restrict__ vals) {
+    router_body<EP, TOK, false>(x, w, T, H, E, k, ids, vals, RouterTrainArgs{});
+}
+
+template <int EP, int TOK>
+__global__ __launch_bounds__(256) void router_train_kernel(RouterTrainArgs a) {
+    router_body<EP, TOK, true>(a.x, a.w, a.T, a.H, a.E, a.k, a.ids, a.vals, a);
+}
+
+// Sums of the workgroups' parts and the losses: one workgroup, a slice of
+// the parts per 1024 / EP threads, then the slices in order.
+__global__ __launch_bounds__(1024) void router_losses_kernel(RouterTrainArgs a, int parts) {
+    __shared__ double ps[1024], zsum[16];
+    __shared__ int32_t cs[1024], nsum[16];
+    const int EP = (a.E + 31) / 32 * 32, slices = 1024 / EP, e = threadIdx.x % EP, sl = threadIdx.x / EP;
+    double p = 0.0;
+    int32_t c = 0;
+    if (e < a.E && sl < slices)
+        for (int b = sl; b < parts; b += slices) {
+            p += a.part_p[(int64_t)b * a.E + e];
+            c += a.part_c[(int64_t)b * (a.E + 1) + e];
+        }
+    ps[threadIdx.x] = p;
+    cs[threadIdx.x] = c;
+    double z = 0.0;
+    int32_t n = 0;
+    for (int b = threadIdx.x; b < parts; b += 1024) {
+        z += a.part_z[b];
+        n += a.part_c[(int64_t)b * (a.E + 1) + a.E];
+    }
+    for (int d = 1; d < 64; d <<= 1) {
+        z += __shfl_xor(z, d);
+        n += __shfl_xor(n, d);
+    }
+    if ((threadIdx.x & 63) == 0) {
+        zsum[threadIdx.x >> 6] = z;
+        nsum[threadIdx.x >> 6] = n;
+    }
+    __syncthreads();
+    z = 0.0;
+    n = 0;
+    for (int i = 0; i < 16; ++i) {
+        z += zsum[i];
+        n += nsum[i];
+    }
+    double term = 0.0;
+    if (sl == 0 && e < a.E) {
+        for (int i = 1; i < slices; ++i) {
+            p += ps[i * EP + e];
+            c += cs[i * EP + e];
+        }
+        a.counts[e] = c;
+        term = p * c;
+    }
+    __syncthreads();
+    ps[threadIdx.x] = term;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        double s = 0.0;
+        for (int i = 0; i < a.E; ++i) s += ps[i];
+        a.counts[a.E] = n;
+        a.losses[0] = n > 0 ? (float)(s * a.E / ((double)a.k * n * n)) : 0.f;
+        a.losses[1] = n > 0 ? (float)(z / n) : 0.f;
     }
 }
 
@@ -215,6 +343,17 @@ hipError_t launch_ep(const _Float16 *x, const _Float16 *w, int64_t T, int64_t H,
     const unsigned grid = (unsigned)((T + TOK - 1) / TOK);
     hipLaunchKernelGGL((router_kernel<EP, TOK>), dim3(grid), dim3(256), C::LDS_BYTES, s, x, w, T, H,
                        E, k, ids, vals);
+    return hipGetLastError();
+}
+
+template <int EP, int TOK>
+hipError_t launch_train_ep(const RouterTrainArgs &a, hipStream_t s) {
+    using C = RouterCfg<EP, TOK>;
+    static std::atomic<uint64_t> lds_set{0};
+    hipError_t e = lds_opt_in_once((const void *)router_train_kernel<EP, TOK>, C::LDS_BYTES, lds_set);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((router_train_kernel<EP, TOK>), dim3((unsigned)((a.T + TOK - 1) / TOK)), dim3(256), C::LDS_BYTES,
+                       s, a);
     return hipGetLastError();
 }
 
@@ -241,16 +380,42 @@ hipError_t cu_count(int &n) {
     return hipSuccess;
 }
 
+// 64 once that still gives two workgroups per CU
+hipError_t tokens_per_workgroup(int64_t T, int &tok) {
+    int cus = 0;
+    hipError_t e = cu_count(cus);
+    tok = T >= (int64_t)64 * 2 * cus ? 64 : 32;
+    return e;
+}
+
 }  // namespace
+
+int64_t router_train_parts(int64_t T) { return (T + 31) / 32; }
+
+hipError_t launch_router_train(const RouterTrainArgs &a, hipStream_t s) {
+    int tok = 0;
+    hipError_t e = tokens_per_workgroup(a.T, tok);
+    if (e != hipSuccess) return e;
+    if (a.T > 0) {
+#define RMOE_R(N) \
+    case N: e = tok == 64 ? launch_train_ep<32 * N, 64>(a, s) : launch_train_ep<32 * N, 32>(a, s); break;
+        switch ((a.E + 31) / 32) {
+            RMOE_R(1) RMOE_R(2) RMOE_R(3) RMOE_R(4) RMOE_R(5) RMOE_R(6) RMOE_R(7) RMOE_R(8)
+            default: return hipErrorInvalidValue;
+        }
+#undef RMOE_R
+        if (e != hipSuccess) return e;
+    }
+    hipLaunchKernelGGL(router_losses_kernel, dim3(1), dim3(1024), 0, s, a, (int)((a.T + tok - 1) / tok));
+    return hipGetLastError();
+}
 
 hipError_t launch_router(const _Float16 *x, const _Float16 *w, int64_t T, int64_t H, int32_t E,
                          int32_t k, int32_t *ids, float *vals, hipStream_t s) {
     if (T == 0 || k == 0) return hipSuccess;
-    // tokens per workgroup: 64 once that still gives two workgroups per CU
-    int cus = 0;
-    hipError_t e = cu_count(cus);
+    int tok = 0;
+    hipError_t e = tokens_per_workgroup(T, tok);
     if (e != hipSuccess) return e;
-    const int tok = T >= (int64_t)64 * 2 * cus ? 64 : 32;
     switch ((E + 31) / 32) {
         case 1: return launch_tok<32>(tok, x, w, T, H, E, k, ids, vals, s);
         case 2: return launch_tok<64>(tok, x, w, T, H, E, k, ids, vals, s);

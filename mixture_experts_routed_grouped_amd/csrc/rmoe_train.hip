@@ -35,6 +35,7 @@
 #include <atomic>
 
 #include "rmoe_kloop.h"
+#include "rmoe_kmajor.h"
 
 namespace rmoe {
 namespace {
@@ -45,23 +46,6 @@ constexpr int NAS = 3, NBS = 2;      // A (weight) and B (token) slots: A runs t
 constexpr int B_OFF = NAS * SLOT;
 constexpr int LDS_BYTES = (NAS + NBS) * SLOT;
 static_assert(LDS_BYTES <= 160 * 1024, "LDS");
-typedef short s4 __attribute__((ext_vector_type(4)));
-
-__device__ __forceinline__ int swz_k(int r) { return ((r >> 1) & 1) * 4 | ((r >> 2) & 1) * 2; }
-
-// Lane offset in a k-major slot of read half h of a 32-column tile of parity
-// tp: rows 4h .. 4h+3 of k group lane / 32 (sub-step s: + 2048 s; column
-// group nb: + 8192 nb).
-__device__ __forceinline__ unsigned tr_off(int lane, int tp, int h) {
-    const int i = lane & 15, n16 = (lane >> 4) & 1, lh = lane >> 5;
-    const int r = 4 * h + (i >> 2), c = 4 * tp + 2 * n16 + ((i & 3) >> 1);
-    return lh * 1024 + r * 128 + ((c ^ swz_k(r)) << 4) + (i & 1) * 8;
-}
-__device__ __forceinline__ h4 tr_read(const unsigned char *p) {
-    return __builtin_bit_cast(
-        h4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4 *)p));
-}
-
 // Lane offsets of a slot's instructions, which go out in order: a row-major
 // slot's rows 8 j .. 8 j + 7 (the swizzle repeats with j's parity), a k-major
 // slot's k rows 8 j ...  One vector add per instruction (from a fresh first
