@@ -442,8 +442,8 @@ RMOE_API int rmoe_router_f16(const void *x, const void *router_w, int64_t num_to
  * scratch: rmoe_router_train_scratch_bytes(num_tokens, E) bytes, contents
  * irrelevant on entry.  Sums run in an order fixed by the sizes: equal calls
  * give equal bits.  Shapes: as rmoe_router_f16 with top_k >= 1, hidden at
- * most 2^20, num_tokens * top_k at most 2^31 - 1.  fp16 tensors 16-byte, the
- * rest (but the mask) 4-byte aligned.  Two launches on `stream`.
+ * most 2^20, num_tokens * top_k at most 2^31 - 1.  fp16 tensors 16-byte,
+ * scratch 8-byte, the rest (but the mask) 4-byte aligned.  Two launches on `stream`.
  */
 RMOE_API size_t rmoe_router_train_scratch_bytes(int64_t num_tokens, int32_t num_experts);
 RMOE_API int rmoe_router_train_f16(const void *x, const void *router_w, const uint8_t *token_mask,

@@ -586,16 +586,15 @@ int rmoe_router_train_f16(const void *x, const void *router_w, const uint8_t *to
         (num_tokens > 0 && (!x || !topk_ids || !topk_weights || !probs || !lse || !scratch)))
         return RMOE_ERR_INVALID_ARGUMENT;
     if (!aligned16(x) || !aligned16(router_w) || !aligned4(topk_ids) || !aligned4(topk_weights) || !aligned4(probs) ||
-        !aligned4(lse) || !aligned4(counts) || !aligned4(losses) || !aligned4(scratch))
+        !aligned4(lse) || !aligned4(counts) || !aligned4(losses) || (reinterpret_cast<uintptr_t>(scratch) & 7u))
         return RMOE_ERR_MISALIGNED;
     rmoe::RouterTrainArgs a{};
     a.x = static_cast<const _Float16 *>(x), a.w = static_cast<const _Float16 *>(router_w), a.mask = token_mask;
     a.T = num_tokens, a.H = hidden, a.E = num_experts, a.k = top_k;
     a.ids = topk_ids, a.vals = topk_weights, a.probs = probs, a.lse = lse, a.counts = counts, a.losses = losses;
     const int64_t parts = rmoe::router_train_parts(num_tokens);
-    a.part_p = static_cast<float *>(scratch);
-    a.part_c = reinterpret_cast<int32_t *>(a.part_p + parts * num_experts);
-    a.part_z = reinterpret_cast<float *>(a.part_c + parts * (num_experts + 1));
+    a.parts = static_cast<rmoe::RouterPart *>(scratch);
+    a.tokens = a.parts + parts * num_experts;
     return to_status(rmoe::launch_router_train(a, static_cast<hipStream_t>(stream)));
 }
 

@@ -88,6 +88,12 @@ hipError_t launch_combine(const _Float16 *out, const int32_t *prow, int64_t T, i
 hipError_t launch_router(const _Float16 *x, const _Float16 *w, int64_t T, int64_t H, int32_t E,
                          int32_t k, int32_t *ids, float *vals, hipStream_t s);
 
+// A workgroup's sum and count.
+struct alignas(8) RouterPart {
+    float sum;
+    int32_t count;
+};
+
 // The training router: what the forward keeps, and the losses.
 struct RouterTrainArgs {
     const _Float16 *x, *w;  // [T, H], [E, H]
@@ -99,9 +105,8 @@ struct RouterTrainArgs {
     float *probs, *lse;     // [T, E], [T]
     int32_t *counts;        // [E + 1]: pairs per expert, tokens that count
     float *losses;          // [2]: balance, z
-    float *part_p;          // [parts, E] sums of probabilities
-    int32_t *part_c;        // [parts, E + 1] counts
-    float *part_z;          // [parts] sums of lse^2
+    RouterPart *parts;      // [parts, E] probabilities, pairs
+    RouterPart *tokens;     // [parts] lse^2, tokens
 };
 int64_t router_train_parts(int64_t T);  // at most
 hipError_t launch_router_train(const RouterTrainArgs &a, hipStream_t s);

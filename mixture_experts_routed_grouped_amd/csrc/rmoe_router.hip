@@ -28,25 +28,27 @@ namespace rmoe {
 namespace {
 
 constexpr int RT_CK = 64;   // K per chunk
-constexpr int RT_NST = 4;   // LDS ring stages: DMA runs 3 chunks ahead
+constexpr int RT_XST = 8;   // LDS ring stages of the tokens: from HBM, 7 chunks ahead
+constexpr int RT_WST = 3;   // and of the gate rows, from the L2
 
 template <int EP, int TOK>
 struct RouterCfg {
     static constexpr int TROWS = TOK;             // LDS token rows
-    static constexpr int ROWS = TROWS + EP;       // LDS rows per chunk: tokens, then gate rows
-    static constexpr int STAGE = ROWS * 128;
-    static constexpr int NI = ROWS / 8;           // DMA instructions per chunk
-    static_assert(NI % 4 == 0, "DMA split over 4 waves");
-    static constexpr int NIW = NI / 4;            // per wave
+    static constexpr int XSTAGE = TROWS * 128, WSTAGE = EP * 128;  // bytes of a chunk: tokens, gate rows
+    static constexpr int W_OFF = RT_XST * XSTAGE;
+    static constexpr int NIX = TROWS / 8;         // DMA instructions per chunk: tokens, by the fifth wave,
+    static constexpr int NIW = EP / 32;           // gate rows, by each of the others
     static constexpr int NT = EP / 32;            // 32-expert tiles
     static constexpr int EW = TOK == 64 ? 2 : 4;  // waves sharing the expert tiles
     static constexpr int TPW = (NT + EW - 1) / EW;  // tiles per wave
     // waves per expert tile that split a chunk's 4 K-steps (TOK = 32 only)
     static constexpr int KSW = TOK == 32 && NT == 1 ? 4 : TOK == 32 && NT == 2 ? 2 : 1;
-    static constexpr int LDS_BYTES = RT_NST * STAGE;  // >= the TROWS x EP fp32 logits
+    static constexpr int LD = EP + 4;             // words per row of logits
+    static constexpr int LDS_BYTES = W_OFF + RT_WST * WSTAGE;  // >= the TROWS x LD fp32 logits
     static_assert(TOK == 64 || TOK == 32, "tokens per workgroup: whole 32-token tiles");
-    static_assert(LDS_BYTES >= KSW * TROWS * EP * 4, "partial logits fit in the ring");
+    static_assert(LDS_BYTES >= KSW * TROWS * LD * 4 && LDS_BYTES >= 64 * LD * 4, "partial logits fit in the rings");
     static_assert(LDS_BYTES <= 160 * 1024, "LDS");
+    static_assert((RT_XST - 2) * NIX < 64 && (RT_WST - 2) * NIW < 64, "vmcnt range");
 };
 
 __device__ __forceinline__ bool better(float s, int e, float s2, int e2) {
@@ -72,34 +74,55 @@ __device__ __forceinline__ void router_body(const _Float16 *__restrict__ x, cons
     const int th = TOK == 64 ? (wave & 1) : 0;
     const int eh = TOK == 64 ? (wave >> 1) : C::KSW > 1 ? wave % C::NT : wave;
 
-    // DMA sources: instruction j = wave*NIW + i moves rows 8j .. 8j+7 of the
-    // chunk (rows < TOK: tokens, clamped to the last token; the rest: gate
-    // rows, clamped to the last expert -- padding rows feed outputs nobody reads)
-    const _Float16 *src[C::NIW];
-#pragma unroll
-    for (int i = 0; i < C::NIW; ++i) {
-        const int r = 8 * (wave * C::NIW + i) + (lane >> 3);
-        const int c = (lane & 7) ^ lds_swz(r);
-        if (r < C::TROWS) {
-            const int64_t row = t0 + r < T ? t0 + r : T - 1;
-            src[i] = x + row * H + 8 * c;
-        } else {
-            const int e = r - C::TROWS < E ? r - C::TROWS : E - 1;
-            src[i] = w + (int64_t)e * H + 8 * c;
-        }
-    }
-    const unsigned sbase = (unsigned)(uintptr_t)smem + wave * C::NIW * 1024;
     // every workgroup reads the same gate rows: each starts its K sweep at a
     // different chunk, so that concurrent workgroups do not ask the L2 for
     // the same lines at the same moment (a token's sum order stays fixed)
     const int nk = (int)(H / RT_CK);
     const int kofs = (int)((blockIdx.x * 7u) % (unsigned)nk);
-    auto dma_chunk = [&](int kc, int stage) {
-        const int kk = kc + kofs < nk ? kc + kofs : kc + kofs - nk;
+    auto chunk = [&](int kc) -> int64_t {  // element offset; clamped at the end: repeats land in stages no later chunk reads
+        kc = kc < nk ? kc : nk - 1;
+        return (int64_t)(kc + kofs < nk ? kc + kofs : kc + kofs - nk) * RT_CK;
+    };
+    const unsigned lds0 = (unsigned)(uintptr_t)smem;
+    // DMA instruction j moves rows 8j .. 8j+7 of a chunk (tokens clamped to
+    // the last one, gate rows to the last expert: padding rows feed outputs
+    // nobody reads)
+    if (wave == 4) {
+        const _Float16 *src[C::NIX];
 #pragma unroll
-        for (int i = 0; i < C::NIW; ++i) dma16(src[i] + (int64_t)kk * RT_CK, sbase + stage * C::STAGE + i * 1024);
+        for (int i = 0; i < C::NIX; ++i) {
+            const int r = 8 * i + (lane >> 3);
+            src[i] = x + (t0 + r < T ? t0 + r : T - 1) * H + 8 * ((lane & 7) ^ lds_swz(r));
+        }
+        auto dma = [&](int kc) {
+#pragma unroll
+            for (int i = 0; i < C::NIX; ++i)
+                dma16(src[i] + chunk(kc), lds0 + (kc % RT_XST) * C::XSTAGE + i * 1024);
+        };
+#pragma unroll
+        for (int p = 0; p < RT_XST - 1; ++p) dma(p);
+        for (int kc = 0; kc < nk; ++kc) {
+            wait_vm<(RT_XST - 2) * C::NIX>();  // chunk kc landed
+            bar();
+            dma(kc + RT_XST - 1);
+        }
+        wait_vm<0>();
+        bar();
+        return;
+    }
+    const _Float16 *src[C::NIW];
+#pragma unroll
+    for (int i = 0; i < C::NIW; ++i) {
+        const int e = 8 * (wave * C::NIW + i) + (lane >> 3);
+        src[i] = w + (int64_t)(e < E ? e : E - 1) * H + 8 * ((lane & 7) ^ lds_swz(e));
+    }
+    auto dma = [&](int kc) {
+#pragma unroll
+        for (int i = 0; i < C::NIW; ++i)
+            dma16(src[i] + chunk(kc), lds0 + C::W_OFF + (kc % RT_WST) * C::WSTAGE + (wave * C::NIW + i) * 1024);
     };
 
+    constexpr bool whole = C::KSW > 1 || C::NT % C::EW == 0;  // every wave has TPW expert tiles
     f16x acc[C::TPW];
 #pragma unroll
     for (int t = 0; t < C::TPW; ++t)
@@ -107,108 +130,123 @@ __device__ __forceinline__ void router_body(const _Float16 *__restrict__ x, cons
         for (int i = 0; i < 16; ++i) acc[t][i] = 0.f;
 
 #pragma unroll
-    for (int p = 0; p < RT_NST - 1; ++p) dma_chunk(p < nk ? p : nk - 1, p);
+    for (int p = 0; p < RT_WST - 1; ++p) dma(p);
     for (int kc = 0; kc < nk; ++kc) {
-        wait_vm<(RT_NST - 2) * C::NIW>();  // chunk kc landed (own DMAs) ...
-        bar();  // ... and everyone's; and every wave is done with chunk kc-1's stage
-        // refill that stage (clamped at the end: repeats land in stages no
-        // later chunk reads)
-        dma_chunk(kc + RT_NST - 1 < nk ? kc + RT_NST - 1 : nk - 1, (kc + RT_NST - 1) % RT_NST);
-        const unsigned char *base = smem + (kc % RT_NST) * C::STAGE;
+        wait_vm<(RT_WST - 2) * C::NIW>();    // chunk kc landed (own DMAs) ...
+        __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): this wave's reads of chunk kc-1
+        bar();  // ... and everyone's; and every wave is done with chunk kc-1's stages
+        // the wave's operands of the chunk, all requested before the first MFMA
+        const unsigned char *bx = smem + (kc % RT_XST) * C::XSTAGE;
+        const unsigned char *bw = smem + C::W_OFF + (kc % RT_WST) * C::WSTAGE;
+        constexpr int NS = 4 / C::KSW;  // K-steps of this wave: s = KSW i + ks
+        h8 b[NS], a[C::TPW][NS];
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            if (s % C::KSW != ks) continue;
-            const h8 b = *(const h8 *)(base + lds_off(32 * th + lr, 2 * s + lh));
+        for (int i = 0; i < NS; ++i) {
+            const int ch = 2 * (C::KSW * i + ks) + lh;
+            b[i] = *(const h8 *)(bx + lds_off(32 * th + lr, ch));
 #pragma unroll
             for (int t = 0; t < C::TPW; ++t) {
-                const int et = eh + C::EW * t;
-                if (et < C::NT) {
-                    const h8 a = *(const h8 *)(base + lds_off(C::TROWS + 32 * et + lr, 2 * s + lh));
-                    acc[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, acc[t], 0, 0, 0);
-                }
+                // an idle last tile reads the tile before it
+                const int et = whole || eh + C::EW * t < C::NT ? eh + C::EW * t : C::NT - 1;
+                a[t][i] = *(const h8 *)(bw + lds_off(32 * et + lr, ch));
             }
         }
+        dma(kc + RT_WST - 1);
+#pragma unroll
+        for (int i = 0; i < NS; ++i)
+#pragma unroll
+            for (int t = 0; t < C::TPW; ++t) acc[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a[t][i], b[i], acc[t], 0, 0, 0);
     }
     wait_vm<0>();
     bar();
 
     // ---- logits -> LDS [TROWS tokens][EP experts] fp32 (partial logits of
-    //      K-split ks at L + ks * TROWS * EP, then added in order of ks).
+    //      K-split ks at L + ks * TROWS * LD, then added in order of ks).
     //      32x32 accumulator layout: register 4q + r holds expert row
-    //      8q + 4lh + r, token lr.
+    //      8q + 4lh + r, token lr.  Rows are 4 words apart modulo the banks:
+    //      the 16 tokens x 4 lanes that read together touch all 64 (at a
+    //      stride of EP they shared 4 of them).
     float *L = reinterpret_cast<float *>(smem);
+    constexpr int LD = C::LD;
 #pragma unroll
     for (int t = 0; t < C::TPW; ++t) {
         const int et = eh + C::EW * t;
-        if (et < C::NT) {
+        if (whole || et < C::NT) {
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    L[ks * C::TROWS * EP + (32 * th + lr) * EP + 32 * et + 8 * q + 4 * lh + r] = acc[t][4 * q + r];
+                *(f4 *)(L + ks * C::TROWS * LD + (32 * th + lr) * LD + 32 * et + 8 * q + 4 * lh) =
+                    f4{acc[t][4 * q], acc[t][4 * q + 1], acc[t][4 * q + 2], acc[t][4 * q + 3]};
         }
     }
     __syncthreads();
     if constexpr (C::KSW > 1) {
-        for (int i = tid; i < C::TROWS * EP; i += 256) {
+        for (int i = tid; i < C::TROWS * LD; i += 256) {
             float v = L[i];
 #pragma unroll
-            for (int j = 1; j < C::KSW; ++j) v += L[j * C::TROWS * EP + i];
+            for (int j = 1; j < C::KSW; ++j) v += L[j * C::TROWS * LD + i];
             L[i] = v;
         }
         __syncthreads();
     }
 
     // ---- softmax and top-k: 4 consecutive lanes per token, lane `sub` owns
-    //      experts sub, sub + 4, ...
+    //      experts sub, sub + 4, ..., in registers
+    constexpr int NE = EP / 4;
     const int tok = tid >> 2, sub = tid & 3;
-    float *row = L + tok * EP;
-    float m = -__builtin_inff();
-    for (int e = sub; e < E; e += 4) m = fmaxf(m, row[e]);
+    float *row = L + tok * LD;
+    float v[NE], m = -__builtin_inff();
+#pragma unroll
+    for (int i = 0; i < NE; ++i) {
+        v[i] = sub + 4 * i < E ? row[sub + 4 * i] : -__builtin_inff();
+        m = fmaxf(m, v[i]);
+    }
     m = fmaxf(m, __shfl_xor(m, 1));
     m = fmaxf(m, __shfl_xor(m, 2));
     float sum = 0.f;
-    for (int e = sub; e < E; e += 4) {
-        const float p = __builtin_amdgcn_exp2f((row[e] - m) * 1.4426950408889634f);
-        row[e] = p;
-        sum += p;
+#pragma unroll
+    for (int i = 0; i < NE; ++i) {
+        v[i] = __builtin_amdgcn_exp2f((v[i] - m) * 1.4426950408889634f);
+        sum += v[i];
     }
     sum += __shfl_xor(sum, 1);
     sum += __shfl_xor(sum, 2);
     const float inv = 1.0f / sum;
-    uint64_t taken = 0;  // bit i: expert sub + 4i already chosen
+#pragma unroll
+    for (int i = 0; i < NE; ++i) v[i] *= inv;
     const bool live = tok < TOK && t0 + tok < T;
-    // behind the logits: 1 / sum of each token (0: left out), the
-    // workgroup's pairs per expert, and its tokens and their lse^2
-    static_assert(!TRAIN || C::LDS_BYTES >= C::TROWS * EP * 4 + (TOK + EP + 2 * TOK) * 4, "LDS behind the logits");
-    float *invs = L + C::TROWS * EP;
-    int32_t *cnt = reinterpret_cast<int32_t *>(invs + TOK);
+    // behind the logits: the workgroup's pairs per expert, and of each token
+    // lse^2 and whether it counts
+    static_assert(!TRAIN || C::LDS_BYTES >= (C::TROWS * LD + EP + 2 * TOK) * 4, "LDS behind the logits");
+    int32_t *cnt = reinterpret_cast<int32_t *>(L + C::TROWS * LD);
     float *zs = reinterpret_cast<float *>(cnt + EP), *on = zs + TOK;
     bool counts = live;
     if constexpr (TRAIN) {
-        __syncthreads();  // idle threads (tok >= TOK) wrote rows there too
         counts = live && (tr.mask == nullptr || tr.mask[t0 + tok] != 0);
+        __syncthreads();  // idle threads (tok >= TOK) have read their rows there
         for (int e = tid; e < EP; e += 256) cnt[e] = 0;
-        if (tok < TOK && sub == 0) {
-            const float lse = counts ? m + __builtin_amdgcn_logf(sum) * 0.6931471805599453f : 0.f;
-            invs[tok] = counts ? inv : 0.f;
-            zs[tok] = lse * lse;
-            on[tok] = counts ? 1.f : 0.f;
-            if (live) tr.lse[t0 + tok] = lse;
+        if (tok < TOK) {
+#pragma unroll
+            for (int i = 0; i < NE; ++i) row[sub + 4 * i] = counts ? v[i] : 0.f;
+            if (sub == 0) {
+                const float lse = counts ? m + __builtin_amdgcn_logf(sum) * 0.6931471805599453f : 0.f;
+                zs[tok] = lse * lse;
+                on[tok] = counts ? 1.f : 0.f;
+                if (live) tr.lse[t0 + tok] = lse;
+            }
         }
         __syncthreads();
     }
+#pragma unroll
+    for (int i = 0; i < NE; ++i) v[i] = sub + 4 * i < E ? v[i] : -2.f;
     for (int j = 0; j < k; ++j) {
         float bs = -1.f;
         int be = 0x7fffffff;
-        for (int e = sub, i = 0; e < E; e += 4, ++i) {
-            if ((taken >> i) & 1) continue;
-            const float s = row[e] * inv;
-            if (better(s, e, bs, be)) {
-                bs = s;
-                be = e;
+#pragma unroll
+        for (int i = 0; i < NE; ++i)
+            if (v[i] > bs) {  // in ascending order: the first of equal scores stays
+                bs = v[i];
+                be = sub + 4 * i;
             }
-        }
 #pragma unroll
         for (int d = 1; d <= 2; d <<= 1) {
             const float os = __shfl_xor(bs, d);
@@ -218,7 +256,8 @@ __device__ __forceinline__ void router_body(const _Float16 *__restrict__ x, cons
                 be = oe;
             }
         }
-        if ((be & 3) == sub) taken |= 1ull << (be >> 2);
+#pragma unroll
+        for (int i = 0; i < NE; ++i) v[i] = be == sub + 4 * i ? -2.f : v[i];  // taken
         if (live && sub == 0) {
             if constexpr (TRAIN) {
                 ids[(t0 + tok) * k + j] = counts ? be : -1;
@@ -234,18 +273,14 @@ __device__ __forceinline__ void router_body(const _Float16 *__restrict__ x, cons
     if constexpr (TRAIN) {
         __syncthreads();
         const int nt = T - t0 < TOK ? (int)(T - t0) : TOK;
-        // probabilities: the workgroup's tokens are one contiguous piece
-        for (int i = tid; i < nt * E; i += 256) {
-            const int t = i / E, e = i - t * E;
-            tr.probs[t0 * E + i] = invs[t] > 0.f ? L[t * EP + e] * invs[t] : on[t] * invs[t];
-        }
+        for (int t = wave; t < nt; t += 4)
+            for (int e = lane; e < E; e += 64) tr.probs[(t0 + t) * E + e] = L[t * LD + e];
         // sums over the workgroup's tokens, in a fixed order
         if (tid < E) {
             float s = 0.f;
 #pragma unroll 8
-            for (int t = 0; t < nt; ++t) s += invs[t] > 0.f ? L[t * EP + tid] * invs[t] : on[t] * invs[t];
-            tr.part_p[(int64_t)blockIdx.x * E + tid] = s;
-            tr.part_c[(int64_t)blockIdx.x * (E + 1) + tid] = cnt[tid];
+            for (int t = 0; t < nt; ++t) s += L[t * LD + tid];
+            tr.parts[(int64_t)blockIdx.x * E + tid] = RouterPart{s, cnt[tid]};
         }
         if (wave == 3) {  // zs and on hold TOK entries, zeros past the last token
             float z = lane < TOK ? zs[lane] : 0.f, n = lane < TOK ? on[lane] : 0.f;
@@ -255,15 +290,14 @@ __device__ __forceinline__ void router_body(const _Float16 *__restrict__ x, cons
                 n += __shfl_xor(n, d);
             }
             if (lane == 0) {
-                tr.part_z[blockIdx.x] = z;
-                tr.part_c[(int64_t)blockIdx.x * (E + 1) + E] = (int)n;
+                tr.tokens[blockIdx.x] = RouterPart{z, (int)n};
             }
         }
     }
 }
 
 template <int EP, int TOK>
-__global__ __launch_bounds__(256) void router_kernel(const _Float16 *__restrict__ x,
+__global__ __launch_bounds__(320) void router_kernel(const _Float16 *__restrict__ x,
                                                      const _Float16 *__restrict__ w, int64_t T,
                                                      int64_t H, int32_t E, int32_t k,
                                                      int32_t *__restrict__ ids,
@@ -272,7 +306,7 @@ __global__ __launch_bounds__(256) void router_kernel(const _Float16 *__restrict_
 }
 
 template <int EP, int TOK>
-__global__ __launch_bounds__(256) void router_train_kernel(RouterTrainArgs a) {
+__global__ __launch_bounds__(320) void router_train_kernel(RouterTrainArgs a) {
     router_body<EP, TOK, true>(a.x, a.w, a.T, a.H, a.E, a.k, a.ids, a.vals, a);
 }
 
@@ -285,17 +319,20 @@ __global__ __launch_bounds__(1024) void router_losses_kernel(RouterTrainArgs a, 
     double p = 0.0;
     int32_t c = 0;
     if (e < a.E && sl < slices)
+#pragma unroll 32
         for (int b = sl; b < parts; b += slices) {
-            p += a.part_p[(int64_t)b * a.E + e];
-            c += a.part_c[(int64_t)b * (a.E + 1) + e];
+            const RouterPart r = a.parts[(int64_t)b * a.E + e];
+            p += r.sum;
+            c += r.count;
         }
     ps[threadIdx.x] = p;
     cs[threadIdx.x] = c;
     double z = 0.0;
     int32_t n = 0;
     for (int b = threadIdx.x; b < parts; b += 1024) {
-        z += a.part_z[b];
-        n += a.part_c[(int64_t)b * (a.E + 1) + a.E];
+        const RouterPart r = a.tokens[b];
+        z += r.sum;
+        n += r.count;
     }
     for (int d = 1; d < 64; d <<= 1) {
         z += __shfl_xor(z, d);
@@ -321,12 +358,13 @@ __global__ __launch_bounds__(1024) void router_losses_kernel(RouterTrainArgs a, 
         a.counts[e] = c;
         term = p * c;
     }
+    for (int d = 1; d < 64; d <<= 1) term += __shfl_xor(term, d);
     __syncthreads();
-    ps[threadIdx.x] = term;
+    if ((threadIdx.x & 63) == 0) ps[threadIdx.x >> 6] = term;
     __syncthreads();
     if (threadIdx.x == 0) {
         double s = 0.0;
-        for (int i = 0; i < a.E; ++i) s += ps[i];
+        for (int i = 0; i < 4; ++i) s += ps[i];  // experts: the first 256 threads
         a.counts[a.E] = n;
         a.losses[0] = n > 0 ? (float)(s * a.E / ((double)a.k * n * n)) : 0.f;
         a.losses[1] = n > 0 ? (float)(z / n) : 0.f;
@@ -341,7 +379,7 @@ hipError_t launch_ep(const _Float16 *x, const _Float16 *w, int64_t T, int64_t H,
     hipError_t e = lds_opt_in_once((const void *)router_kernel<EP, TOK>, C::LDS_BYTES, lds_set);
     if (e != hipSuccess) return e;
     const unsigned grid = (unsigned)((T + TOK - 1) / TOK);
-    hipLaunchKernelGGL((router_kernel<EP, TOK>), dim3(grid), dim3(256), C::LDS_BYTES, s, x, w, T, H,
+    hipLaunchKernelGGL((router_kernel<EP, TOK>), dim3(grid), dim3(320), C::LDS_BYTES, s, x, w, T, H,
                        E, k, ids, vals);
     return hipGetLastError();
 }
@@ -352,7 +390,7 @@ hipError_t launch_train_ep(const RouterTrainArgs &a, hipStream_t s) {
     static std::atomic<uint64_t> lds_set{0};
     hipError_t e = lds_opt_in_once((const void *)router_train_kernel<EP, TOK>, C::LDS_BYTES, lds_set);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((router_train_kernel<EP, TOK>), dim3((unsigned)((a.T + TOK - 1) / TOK)), dim3(256), C::LDS_BYTES,
+    hipLaunchKernelGGL((router_train_kernel<EP, TOK>), dim3((unsigned)((a.T + TOK - 1) / TOK)), dim3(320), C::LDS_BYTES,
                        s, a);
     return hipGetLastError();
 }

@@ -18,8 +18,10 @@
 // Bound by memory: x is read once for dW, dx written once (and added to what
 // came through the experts, read once).
 #include <atomic>
+#include <type_traits>
 
 #include "rmoe_internal.h"
+#include "rmoe_kloop.h"
 #include "rmoe_kmajor.h"
 
 namespace rmoe {
@@ -97,75 +99,103 @@ __device__ __forceinline__ void store_split(unsigned char *p, const float (&v)[8
     *(h8 *)(p + FRAG) = lo;
 }
 
-// ---- dl: one workgroup per block of 64 tokens, 4 lanes per token.
-__global__ __launch_bounds__(256) void dlogits_kernel(RouterBackArgs a, Scratch s) {
+// ---- dl: one workgroup per block of 64 tokens.  Thread (token, lane, part):
+// a token's experts are cut into 4 parts of EP / 4, each taken by 4 lanes.
+__global__ __launch_bounds__(1024) void dlogits_kernel(RouterBackArgs a, Scratch s) {
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
     const int EP = 32 * s.et, ld = EP + 4;  // row stride: 16 tokens x 4 lanes on 64 banks
-    float *L = reinterpret_cast<float *>(smem);  // [64][ld]
-    __shared__ float up_x[BT], up_w[256];
-    const int tid = threadIdx.x, tok = tid >> 2, sub = tid & 3;
-    const int64_t b = blockIdx.x, t = b * BT + tok;
+    float *L = reinterpret_cast<float *>(smem);            // [64][ld] dl
+    float *pg = L + BT * ld;                               // [64 k] a routed weight's gradient times its probability
+    int *pid = reinterpret_cast<int *>(pg + BT * a.k);     // [64 k] its expert, -1: none
+    __shared__ float red[4][BT], up_x[BT], up_w[256];
+    __shared__ uint16_t on[4];
+    const int tid = threadIdx.x, sub = tid & 3, tok = (tid >> 2) & 63, part = tid >> 8;
+    const int64_t b = blockIdx.x, t0 = b * BT, t = t0 + tok;
     const bool live = t < a.T && (a.mask == nullptr || a.mask[t] != 0);
     const float n = (float)a.counts[a.E];
     const float ca = a.dlosses && n > 0.f ? a.dlosses[0] * (float)a.E / ((float)a.k * n * n) : 0.f;
     const float cz = a.dlosses && n > 0.f ? a.dlosses[1] * 2.0f / n : 0.f;
     float *row = L + tok * ld;
     const float *p = a.probs + t * a.E;
+    const int e0 = part * (EP / 4) + sub, ne = EP / 16;  // this thread's experts: e0 + 4 i, i < ne
+    float pv[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) pv[i] = i < ne && live && e0 + 4 * i < a.E ? p[e0 + 4 * i] : 0.f;
 
-    auto gradient = [&](int j) {  // of routed weight j of this token
-        const int64_t i = t * a.k + j, q = a.cpos ? a.cpos[i] : i;
-        return q >= 0 && q < a.T * a.k ? a.drw[q] : 0.f;
-    };
+    // the block's pairs are one contiguous piece
+    const int64_t np = (a.T - t0 < BT ? a.T - t0 : BT) * a.k;
+    for (int i = tid; i < np; i += 1024) {
+        const int tk = i / a.k, id = a.ids[t0 * a.k + i];
+        const bool use = id >= 0 && id < a.E && (a.mask == nullptr || a.mask[t0 + tk] != 0);
+        const int64_t q = a.cpos ? (int64_t)a.cpos[t0 * a.k + i] : t0 * a.k + i;
+        const float g = use && q >= 0 && q < a.T * a.k ? a.drw[q] : 0.f;
+        pg[i] = use ? g * a.probs[(t0 + tk) * a.E + id] : 0.f;
+        pid[i] = use ? id : -1;
+    }
     float dot = 0.f;
-    if (live) {
-        for (int e = sub; e < a.E; e += 4) dot += p[e] * (ca * (float)a.counts[e]);
-        for (int j = sub; j < a.k; j += 4) {
-            const int id = a.ids[t * a.k + j];
-            if (id >= 0 && id < a.E) dot += p[id] * gradient(j);
-        }
+    float dv[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        dv[i] = i < ne && e0 + 4 * i < a.E ? pv[i] * (ca * (float)a.counts[e0 + 4 * i]) : 0.f;
+        dot += dv[i];
     }
     dot += __shfl_xor(dot, 1);
     dot += __shfl_xor(dot, 2);
-    const float z = live ? cz * a.lse[t] - dot : 0.f;
-    for (int e = sub; e < EP; e += 4) row[e] = live && e < a.E ? p[e] * (ca * (float)a.counts[e] + z) : 0.f;
+    if (sub == 0) red[part][tok] = dot;
+    if (tid < 256) {  // 16 tokens per wave, 4 equal bits each
+        const uint64_t bits = __ballot(live);
+        if ((tid & 63) == 0) {
+            unsigned w = 0;
+            for (int i = 0; i < 16; ++i) w |= (unsigned)(bits >> (4 * i) & 1) << i;
+            on[tid >> 6] = (uint16_t)w;
+        }
+    }
     __syncthreads();
-    if (live && sub == 0)
+    if (tid == 0)
+        s.live[b] = (uint64_t)on[0] | (uint64_t)on[1] << 16 | (uint64_t)on[2] << 32 | (uint64_t)on[3] << 48;
+    if (b == 0 && tid < 8) ((h8 *)s.zeros)[tid] = h8{0, 0, 0, 0, 0, 0, 0, 0};
+    dot = (red[0][tok] + red[1][tok]) + (red[2][tok] + red[3][tok]);
+    if (live)
+        for (int j = 0; j < a.k; ++j) dot += pg[tok * a.k + j];
+    const float z = live ? cz * a.lse[t] - dot : 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        if (i < ne) row[e0 + 4 * i] = dv[i] + pv[i] * z;
+    __syncthreads();
+    if (live && tid < 256 && sub == 0)
         for (int j = 0; j < a.k; ++j) {
-            const int id = a.ids[t * a.k + j];
-            if (id >= 0 && id < a.E) row[id] += p[id] * gradient(j);
+            const int id = pid[tok * a.k + j];
+            if (id >= 0) row[id] += pg[tok * a.k + j];
         }
     __syncthreads();
-    // scales: of a token, over its 4 lanes; of an expert
+    // scales: of a token, over its lanes and parts; of an expert
     float m = 0.f;
-    for (int e = sub; e < EP; e += 4) m = __builtin_elementwise_maximum(m, __builtin_fabsf(row[e]));
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        if (i < ne) m = __builtin_elementwise_maximum(m, __builtin_fabsf(row[e0 + 4 * i]));
     m = __builtin_elementwise_maximum(m, __shfl_xor(m, 1));
     m = __builtin_elementwise_maximum(m, __shfl_xor(m, 2));
-    if (sub == 0) {
-        const Scale c = scale_of(m);
-        up_x[tok] = c.up;
-        s.sx[t] = c.down;
-    }
+    if (sub == 0) red[part][tok] = m;
     if (tid < EP) {
         float w = 0.f;
-#pragma unroll 8
+#pragma unroll 16
         for (int i = 0; i < BT; ++i) w = __builtin_elementwise_maximum(w, __builtin_fabsf(L[i * ld + tid]));
         const Scale c = scale_of(w);
         up_w[tid] = c.up;
         s.sw[b * EP + tid] = c.down;
     }
-    const uint64_t bits = __ballot(live);  // 16 tokens per wave, 4 equal bits each
-    __shared__ uint16_t on[4];
-    if ((tid & 63) == 0) {
-        unsigned w = 0;
-        for (int i = 0; i < 16; ++i) w |= (unsigned)(bits >> (4 * i) & 1) << i;
-        on[tid >> 6] = (uint16_t)w;
-    }
-    if (b == 0 && tid < 8) ((h8 *)s.zeros)[tid] = h8{0, 0, 0, 0, 0, 0, 0, 0};
     __syncthreads();
-    if (tid == 0)
-        s.live[b] = (uint64_t)on[0] | (uint64_t)on[1] << 16 | (uint64_t)on[2] << 32 | (uint64_t)on[3] << 48;
+    if (tid < BT) {
+        m = red[0][tid];
+#pragma unroll
+        for (int i = 1; i < 4; ++i) m = __builtin_elementwise_maximum(m, red[i][tid]);
+        const Scale c = scale_of(m);
+        up_x[tid] = c.up;
+        s.sx[t0 + tid] = c.down;
+    }
+    __syncthreads();
     // operands of dx: lane = token % 32 + 32 (octet of experts % 2)
-    for (int i = tid; i < BT * EP / 8; i += 256) {
+    for (int i = tid; i < BT * EP / 8; i += 1024) {
         const int tk = i & 63, o = i >> 6;  // token, octet of experts
         float v[8];
 #pragma unroll
@@ -174,7 +204,7 @@ __global__ __launch_bounds__(256) void dlogits_kernel(RouterBackArgs a, Scratch 
         store_split(f + ((tk & 31) + 32 * (o & 1)) * 16, v, up_x[tk]);
     }
     // operands of dW: lane = expert % 32 + 32 (octet of tokens % 2)
-    for (int i = tid; i < EP * 8; i += 256) {
+    for (int i = tid; i < EP * 8; i += 1024) {
         const int o = i / EP, e = i - o * EP;  // octet of tokens, expert
         float v[8];
 #pragma unroll
@@ -186,10 +216,30 @@ __global__ __launch_bounds__(256) void dlogits_kernel(RouterBackArgs a, Scratch 
 
 // ---- dx: a workgroup takes 256 columns; its 4 waves hold the gate matrix's
 // 64 columns each as MFMA operands in registers and run over tiles of 32
-// tokens, whose operands come from the caches.
+// tokens.  A tile's operands travel through a ring in LDS that all four read;
+// the rows to be added go to a piece of each wave's own, where the sum
+// replaces them (fp16, its one rounding) before it leaves as whole lines.
+// Everything that is read in the loop comes by DMA, one tile ahead: the waits
+// count memory instructions and leave the stores of the tile before in flight.
 template <int ET>
+struct DxCfg {
+    static constexpr int KS = 2 * ET;                // steps of 16 experts
+    static constexpr int OPS = KS * 2 * FRAG;        // operands of a tile of tokens
+    static constexpr int PIECE = 32 * 128;           // 32 tokens x 64 columns of fp16
+    static constexpr int WAVE = PIECE + 256;         // and the tokens' scales, twice
+    static constexpr int SLOT = OPS + 4 * WAVE, D = 2;
+    static constexpr int W = ET * 16 * FRAG;         // the gate matrix's 256 columns, before the loop
+    static constexpr int LDS = W > D * SLOT ? W : D * SLOT;
+};
+// 256-byte DMA: lane i stores the dword at g to LDS byte lds + 4 i (s_nop: as
+// in dma16)
+__device__ __forceinline__ void dma4(const void *g, unsigned lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(lds), "v"(g) : "memory", "m0");
+}
+template <int ET, bool ADD>
 __global__ __launch_bounds__(256) void dx_kernel(RouterBackArgs a, Scratch s, int chunks) {
-    constexpr int KS = 2 * ET;  // steps of 16 experts
+    using C = DxCfg<ET>;
+    constexpr int KS = C::KS;
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
     const int lr = lane & 31, lh = lane >> 5;
@@ -199,17 +249,18 @@ __global__ __launch_bounds__(256) void dx_kernel(RouterBackArgs a, Scratch s, in
     if ((int)(blockIdx.x >> 3) >= per || at >= total) return;
     const int chunk = at / s.slices, slice = at - chunk * s.slices;
     const int64_t c0 = (int64_t)slice * HS + 64 * wave;  // this wave's columns
-    const int64_t cl = c0 < a.H ? c0 : a.H - 64;         // idle waves read valid ones
-    const unsigned lds = (unsigned)(uintptr_t)smem + wave * ET * 4 * FRAG;
-    const int r8 = lane >> 3;
+    const bool mine = c0 < a.H;
+    const int64_t cl = mine ? c0 : a.H - 64;             // idle waves read valid ones
+    const unsigned lds0 = (unsigned)(uintptr_t)smem;
+    const int r8 = lane >> 3, c8 = lane & 7;
 #pragma unroll
     for (int g = 0; g < 4 * ET; ++g) {
-        const int e = 8 * g + r8, c = (lane & 7) ^ swz_k(r8);
+        const int e = 8 * g + r8, c = c8 ^ swz_k(r8);
         const void *src = e < a.E ? (const void *)(a.w + e * a.H + cl + 8 * c) : (const void *)(s.zeros + 16 * c);
-        dma16(src, lds + g * FRAG);
+        dma16(src, lds0 + (wave * ET * 4 + g) * FRAG);
     }
     wait_vm<0>();
-    bar();
+    __syncthreads();
     h8 w[2][KS];
     const unsigned char *slot = smem + wave * ET * 4 * FRAG;
 #pragma unroll
@@ -219,20 +270,46 @@ __global__ __launch_bounds__(256) void dx_kernel(RouterBackArgs a, Scratch s, in
             w[ht][k].lo = tr_read(slot + 2048 * k + tr_off(lane, ht, 0));
             w[ht][k].hi = tr_read(slot + 2048 * k + tr_off(lane, ht, 1));
         }
-    __syncthreads();  // the slots become staging pieces: 32 tokens x 64 columns of fp32 per wave
-    unsigned char *st = smem + wave * 8192;
+    __syncthreads();  // the gate matrix is in registers: its LDS becomes the ring
     const int64_t tiles = (a.T + 31) / 32, lo = tiles * chunk / chunks, hi = tiles * (chunk + 1) / chunks;
-    const int c8 = lane & 7;
-    for (int64_t i = lo; i < hi; ++i) {
-        const unsigned char *f = s.dlx + i * KS * 2 * FRAG + lane * 16;
-        h8 add[4];
-        if (a.add && c0 < a.H) {
+    // a tile's 4 ET operands, ET per wave; its scales; its rows to be added,
+    // whose 16-byte chunks are XOR-swizzled by row pair (lds_swz)
+    const unsigned char *ops = uniform(s.dlx + wave * ET * FRAG);
+    const _Float16 *addbase = uniform(a.add + cl);
+    unsigned aoff[2];  // lane offset of rows 8 j ..: their swizzle repeats with j's parity
+#pragma unroll
+    for (int j = 0; j < 2; ++j) aoff[j] = (unsigned)((8 * j + r8) * a.H * 2) + 16 * (c8 ^ lds_swz(8 * j + r8));
+    const unsigned row16 = (unsigned)(32 * a.H);
+    auto fill = [&](int64_t i) {
+        const unsigned d = lds0 + (unsigned)(i & 1) * C::SLOT, mypiece = d + C::OPS + wave * C::WAVE;
+#pragma unroll
+        for (int g = 0; g < ET; ++g) dma16_sb(ops + i * C::OPS + g * FRAG, 16 * lane, d + (wave * ET + g) * FRAG);
+        dma4(s.sx + 32 * i + lr, mypiece + C::PIECE);
+        if constexpr (ADD) {
+            const _Float16 *rows = addbase + 32 * i * a.H;
+            const int left = a.T - 32 * i < 32 ? (int)(a.T - 32 * i) : 32;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int64_t t = 32 * i + 8 * j + r8;
-                if (t < a.T) add[j] = *(const h8 *)(a.add + t * a.H + c0 + 8 * c8);
+                unsigned o = aoff[j & 1] + (j >> 1) * row16;
+                // behind the last token: its row again
+                if (left < 32 && 8 * j + r8 >= left) o = (unsigned)((left - 1) * a.H * 2) + 16 * c8;
+                dma16_sb(rows, o, mypiece + 1024 * j);
             }
         }
+    };
+    _Float16 *out = a.dx + c0;
+    const unsigned yoff = (unsigned)(r8 * a.H * 2) + 16 * c8, row8 = (unsigned)(16 * a.H);
+    if (lo < hi) fill(lo);
+    for (int64_t i = lo; i < hi; ++i) {
+        // all but the stores of the tile before, which is a whole one
+        if (i > lo && mine)
+            wait_vm<4>();
+        else
+            wait_vm<0>();
+        bar();  // tile i is there; everyone is done with the other slot
+        if (i + 1 < hi) fill(i + 1);
+        const unsigned char *f = smem + (i & 1) * C::SLOT + lane * 16;
+        unsigned char *st = smem + (i & 1) * C::SLOT + C::OPS + wave * C::WAVE;
         f16x acc[2];
 #pragma unroll
         for (int ht = 0; ht < 2; ++ht)
@@ -242,78 +319,109 @@ __global__ __launch_bounds__(256) void dx_kernel(RouterBackArgs a, Scratch s, in
         for (int k = 0; k < KS; ++k) {
             const h8 dh = *(const h8 *)(f + (2 * k) * FRAG), dl = *(const h8 *)(f + (2 * k + 1) * FRAG);
 #pragma unroll
-            for (int ht = 0; ht < 2; ++ht) {
-                acc[ht] = __builtin_amdgcn_mfma_f32_32x32x16_f16(w[ht][k], dh, acc[ht], 0, 0, 0);
-                acc[ht] = __builtin_amdgcn_mfma_f32_32x32x16_f16(w[ht][k], dl, acc[ht], 0, 0, 0);
-            }
+            for (int ht = 0; ht < 2; ++ht) acc[ht] = __builtin_amdgcn_mfma_f32_32x32x16_f16(w[ht][k], dh, acc[ht], 0, 0, 0);
+#pragma unroll
+            for (int ht = 0; ht < 2; ++ht) acc[ht] = __builtin_amdgcn_mfma_f32_32x32x16_f16(w[ht][k], dl, acc[ht], 0, 0, 0);
         }
         // register 4q + r of tile ht: column 32 ht + 8q + 4lh + r of token lr
-        const float down = s.sx[32 * i + lr];
+        const float down = *(const float *)(st + C::PIECE + 4 * lr);
+        unsigned char *row = st + lr * 128 + 8 * lh;
 #pragma unroll
         for (int ht = 0; ht < 2; ++ht)
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-                *(f4 *)(st + lr * 256 + (((8 * ht + 2 * q + lh) ^ (lr & 15)) << 4)) =
-                    f4{acc[ht][4 * q] * down, acc[ht][4 * q + 1] * down, acc[ht][4 * q + 2] * down, acc[ht][4 * q + 3] * down};
-        __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+            for (int q = 0; q < 4; ++q) {
+                h4 *at4 = (h4 *)(row + (((4 * ht + q) ^ lds_swz(lr)) << 4));
+                float v[4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) v[r] = acc[ht][4 * q + r] * down;
+                if constexpr (ADD) {
+                    const h4 add = *at4;
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) v[r] += (float)add[r];
+                }
+                *at4 = to_h4(v[0], v[1], v[2], v[3]);
+            }
+        __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): this wave's rows are written
         asm volatile("" ::: "memory");
+        h8 y[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[j] = *(const h8 *)(st + (8 * j + r8) * 128 + ((c8 ^ lds_swz(8 * j + r8)) << 4));
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int r = 8 * j + r8;
-            const f4 v0 = *(const f4 *)(st + r * 256 + (((2 * c8) ^ (r & 15)) << 4));
-            const f4 v1 = *(const f4 *)(st + r * 256 + (((2 * c8 + 1) ^ (r & 15)) << 4));
-            const int64_t t = 32 * i + r;
-            if (t < a.T && c0 < a.H) {
-                h8 y;
-#pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    float v = q < 4 ? v0[q & 3] : v1[q & 3];
-                    if (a.add) v += (float)add[j][q];
-                    y[q] = (_Float16)v;
-                }
-                *(h8 *)(a.dx + t * a.H + c0 + 8 * c8) = y;
-            }
+            const int64_t t = 32 * i + 8 * j + r8;
+            if (t < a.T && mine) *(h8 *)((unsigned char *)(out + 32 * i * a.H) + yoff + j * row8) = y[j];
         }
         asm volatile("" ::: "memory");
     }
 }
 
 // ---- dW: a workgroup takes 256 columns of H, up to 4 expert tiles and a
-// part of the blocks of tokens; x travels as a k-major slot, the operands of
-// dl as they are.  A block's sums are scaled back and added up in fp32.
+// part of the blocks of tokens, which it runs through in steps of 32 tokens: x
+// as a k-major slot, the operands of dl as they are, and the experts' scales,
+// all by DMA three steps ahead.  8 waves, 4 groups of 64 columns x 2 halves of
+// the expert tiles: two per SIMD, one's scaling and addresses beside the
+// other's MFMAs.  A block's sums are scaled back and added up in fp32 after
+// its second step.
 template <int ET>
-__global__ __launch_bounds__(256) void dw_kernel(RouterBackArgs a, Scratch s, int tile0) {
-    constexpr int XB = BT * HS * 2, DB = ET * 8 * FRAG, SLOT = XB + DB;
+struct DwCfg {
+    static constexpr int XB = 32 * HS * 2, DB = ET * 4 * FRAG, SB = 8 * 256;  // bytes of a step: tokens, operands, scales
+    static constexpr int SLOT = XB + DB + SB, D = 4;
+    static constexpr int TPW = (ET + 1) / 2;     // expert tiles per wave
+    static constexpr int OPW = (4 * ET + 7) / 8;  // operands moved per wave
+    static constexpr int DMAS = 2 + OPW + 1;     // per wave and step
+    static constexpr int LDS = D * SLOT;
+};
+template <int ET>
+__global__ __launch_bounds__(512) void dw_kernel(RouterBackArgs a, Scratch s, int tile0) {
+    using C = DwCfg<ET>;
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
     const int lr = lane & 31, lh = lane >> 5, r8 = lane >> 3;
+    const int cg = wave & 3, t0 = (wave >> 2) * C::TPW;  // this wave's columns, its first tile
     const int total = s.slices * s.splits, per = (total + 7) / 8;
     const int at = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
     if ((int)(blockIdx.x >> 3) >= per || at >= total) return;
     const int split = at / s.slices, slice = at - split * s.slices;
-    const int64_t c0 = (int64_t)slice * HS + 64 * wave, cl = c0 < a.H ? c0 : a.H - 64;
-    const int64_t b0 = s.nb * split / s.splits, b1 = s.nb * (split + 1) / s.splits;
+    const int64_t b0 = s.nb * split / s.splits, n = 2 * (s.nb * (split + 1) / s.splits - b0);  // first block, steps
     const unsigned lds = (unsigned)(uintptr_t)smem;
-    const int c = (lane & 7) ^ swz_k(r8);
-    // x: this wave's column group, 8 instructions of 8 tokens; dl: 2 ET of its 8 ET operands
-    auto fill = [&](int64_t b, int slot) {
-        const uint64_t on = s.live[b];
+    // the kernel before wrote it: scalar loads (the waits below count the
+    // vector memory instructions)
+    typedef const __attribute__((address_space(4))) uint64_t *Words;
+    const Words live = (Words)(uintptr_t)s.live;
+    // x: this wave moves 16 tokens of column group wave / 2, two instructions
+    const int64_t cx = (int64_t)slice * HS + 64 * (wave >> 1);
+    const _Float16 *xbase = uniform(a.x + (cx < a.H ? cx : a.H - 64));  // idle columns read valid ones
+    const int tx = 16 * (wave & 1) + r8;
+    const unsigned xstep = (unsigned)(16 * a.H), xoff = (unsigned)(tx * a.H * 2) + 16 * ((lane & 7) ^ swz_k(r8));
+    // step i; past the last one the last again, so that every wait counts the same
+    auto fill = [&](int64_t i) {
+        const unsigned d = lds + (unsigned)(i % C::D) * C::SLOT;
+        const int64_t j = i < n ? i : n - 1, b = b0 + (j >> 1);
+        const int half = (int)(j & 1);
+        const unsigned on = (unsigned)(live[b] >> (32 * half));
+        const _Float16 *src = xbase + (b * BT + 32 * half) * a.H;
+        if (on == ~0u) {
+            dma16_sb(src, xoff, d + (2 * wave) * FRAG);
+            dma16_sb(src, xoff + xstep, d + (2 * wave + 1) * FRAG);
+        } else {
 #pragma unroll
-        for (int g = 0; g < 8; ++g) {
-            const int t = 8 * g + r8;
-            const void *src = on >> t & 1 ? (const void *)(a.x + (b * BT + t) * a.H + cl + 8 * c) : (const void *)(s.zeros + 16 * c);
-            dma16(src, lds + slot * SLOT + wave * 8 * FRAG + g * FRAG);
+            for (int g = 0; g < 2; ++g) {
+                const unsigned char *row = (const unsigned char *)src + xoff + g * xstep;
+                dma16(on >> (tx + 8 * g) & 1 ? row : s.zeros + 16 * (lane & 7), d + (2 * wave + g) * FRAG);
+            }
         }
-        const unsigned char *d = s.dlw + (b * s.et + tile0) * 8 * FRAG + lane * 16;
+        // the step's operands: tile o / 4, of its 8 the half's 4 (some moved twice)
+        const unsigned char *f = s.dlw + (b * s.et + tile0) * 8 * FRAG + half * 4 * FRAG;
 #pragma unroll
-        for (int g = 0; g < 2 * ET; ++g) {
-            const int o = wave * 2 * ET + g;
-            dma16(d + o * FRAG, lds + slot * SLOT + XB + o * FRAG);
+        for (int g = 0; g < C::OPW; ++g) {
+            const int o = (wave * C::OPW + g) % (4 * ET);
+            dma16_sb(uniform(f + ((o >> 2) * 8 + (o & 3)) * FRAG), 16 * lane, d + C::XB + o * FRAG);
         }
+        dma4(s.sw + b * 32 * s.et + 32 * (tile0 + (wave < ET ? wave : 0)) + lr, d + C::XB + C::DB + wave * 256);
     };
-    f16x sum[ET][2];
+    f16x sum[C::TPW][2], acc[C::TPW][2];
 #pragma unroll
-    for (int et = 0; et < ET; ++et)
+    for (int et = 0; et < C::TPW; ++et)
 #pragma unroll
         for (int ht = 0; ht < 2; ++ht)
 #pragma unroll
@@ -321,52 +429,63 @@ __global__ __launch_bounds__(256) void dw_kernel(RouterBackArgs a, Scratch s, in
     unsigned off[2][2];
 #pragma unroll
     for (int i = 0; i < 4; ++i) off[i >> 1][i & 1] = tr_off(lane, i >> 1, i & 1);
-    if (b0 < b1) fill(b0, 0);
-    for (int64_t b = b0; b < b1; ++b) {
-        const int slot = (int)(b - b0) & 1;
-        float down[ET];
-#pragma unroll
-        for (int et = 0; et < ET; ++et) down[et] = s.sw[b * 32 * s.et + 32 * (tile0 + et) + lr];
-        wait_vm<0>();
-        __syncthreads();  // block b is there; everyone is done with the other slot
-        if (b + 1 < b1) fill(b + 1, slot ^ 1);
-        const unsigned char *xs = smem + slot * SLOT + wave * 8 * FRAG, *ds = smem + slot * SLOT + XB + lane * 16;
-        h8 xa[2][4];
+    auto step = [&](int64_t i, auto second) __attribute__((always_inline)) {
+        wait_vm<2 * C::DMAS>();              // all but the two steps after this one
+        __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): this wave's reads of the step before
+        bar();                               // step i is there; everyone is done with the slot of the one before
+        fill(i + 3);
+        const unsigned char *slot = smem + (i % C::D) * C::SLOT, *xs = slot + cg * 4 * FRAG;
+        const unsigned char *ds = slot + C::XB + t0 * 4 * FRAG + lane * 16;
+        h8 xa[2][2];
 #pragma unroll
         for (int ht = 0; ht < 2; ++ht)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
+            for (int k = 0; k < 2; ++k) {
                 xa[ht][k].lo = tr_read(xs + 2048 * k + off[ht][0]);
                 xa[ht][k].hi = tr_read(xs + 2048 * k + off[ht][1]);
             }
 #pragma unroll
-        for (int et = 0; et < ET; ++et) {
-            f16x acc[2];
+        for (int et = 0; et < C::TPW; ++et) {
+            if (ET % 2 && t0 + et >= ET) continue;  // an odd count's idle tile
+            if constexpr (!second) {
 #pragma unroll
-            for (int ht = 0; ht < 2; ++ht)
+                for (int ht = 0; ht < 2; ++ht)
 #pragma unroll
-                for (int r = 0; r < 16; ++r) acc[ht][r] = 0.f;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const h8 dh = *(const h8 *)(ds + ((et * 4 + k) * 2) * FRAG), dl = *(const h8 *)(ds + ((et * 4 + k) * 2 + 1) * FRAG);
-#pragma unroll
-                for (int ht = 0; ht < 2; ++ht) {
-                    acc[ht] = __builtin_amdgcn_mfma_f32_32x32x16_f16(xa[ht][k], dh, acc[ht], 0, 0, 0);
-                    acc[ht] = __builtin_amdgcn_mfma_f32_32x32x16_f16(xa[ht][k], dl, acc[ht], 0, 0, 0);
-                }
+                    for (int r = 0; r < 16; ++r) acc[et][ht][r] = 0.f;
             }
 #pragma unroll
-            for (int ht = 0; ht < 2; ++ht)
+            for (int k = 0; k < 2; ++k) {
+                const h8 dh = *(const h8 *)(ds + (et * 4 + k * 2) * FRAG), dl = *(const h8 *)(ds + (et * 4 + k * 2 + 1) * FRAG);
 #pragma unroll
-                for (int r = 0; r < 16; ++r) sum[et][ht][r] = __builtin_fmaf(acc[ht][r], down[et], sum[et][ht][r]);
+                for (int ht = 0; ht < 2; ++ht) acc[et][ht] = __builtin_amdgcn_mfma_f32_32x32x16_f16(xa[ht][k], dh, acc[et][ht], 0, 0, 0);
+#pragma unroll
+                for (int ht = 0; ht < 2; ++ht) acc[et][ht] = __builtin_amdgcn_mfma_f32_32x32x16_f16(xa[ht][k], dl, acc[et][ht], 0, 0, 0);
+            }
+            if constexpr (second) {
+                const float down = *(const float *)(slot + C::XB + C::DB + (t0 + et) * 256 + 4 * lr);
+#pragma unroll
+                for (int ht = 0; ht < 2; ++ht)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) sum[et][ht][r] = __builtin_fmaf(acc[et][ht][r], down, sum[et][ht][r]);
+            }
         }
+    };
+    if (n > 0) {
+#pragma unroll
+        for (int i = 0; i < 3; ++i) fill(i);
+        for (int64_t i = 0; i < n; i += 2) {
+            step(i, std::integral_constant<bool, false>{});
+            step(i + 1, std::integral_constant<bool, true>{});
+        }
+        wait_vm<0>();  // no DMA is left in flight
     }
+    const int64_t c0 = (int64_t)slice * HS + 64 * cg;
     if (c0 >= a.H) return;
     float *y = s.splits > 1 ? s.parts + (int64_t)split * a.E * a.H : a.dw;
 #pragma unroll
-    for (int et = 0; et < ET; ++et) {
-        const int e = 32 * (tile0 + et) + lr;
-        if (e >= a.E) continue;
+    for (int et = 0; et < C::TPW; ++et) {
+        const int e = 32 * (tile0 + t0 + et) + lr;
+        if (e >= a.E || t0 + et >= ET) continue;
 #pragma unroll
         for (int ht = 0; ht < 2; ++ht)
 #pragma unroll
@@ -377,37 +496,39 @@ __global__ __launch_bounds__(256) void dw_kernel(RouterBackArgs a, Scratch s, in
 }
 
 // The parts' sum, in order.
-__global__ __launch_bounds__(256) void dw_sum_kernel(const f4 *__restrict__ parts, int splits, int64_t n, f4 *__restrict__ y) {
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+__global__ __launch_bounds__(64) void dw_sum_kernel(const f4 *__restrict__ parts, int splits, int64_t n, f4 *__restrict__ y) {
+    for (int64_t i = (int64_t)blockIdx.x * 64 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 64) {
         f4 v = parts[i];
+#pragma unroll 8
         for (int p = 1; p < splits; ++p) v += parts[p * n + i];
         y[i] = v;
     }
 }
 
-template <int ET>
+template <int ET, bool ADD>
 hipError_t launch_dx(const RouterBackArgs &a, const Scratch &s, hipStream_t st) {
-    constexpr int LDS = ET * 16 * FRAG > 32768 ? ET * 16 * FRAG : 32768;
+    constexpr int LDS = DxCfg<ET>::LDS;
+    static_assert(LDS <= 160 * 1024, "LDS");
     static std::atomic<uint64_t> lds_set{0};
-    hipError_t e = lds_opt_in_once((const void *)dx_kernel<ET>, LDS, lds_set);
+    hipError_t e = lds_opt_in_once((const void *)dx_kernel<ET, ADD>, LDS, lds_set);
     if (e != hipSuccess) return e;
     const int64_t tiles = (a.T + 31) / 32;
     int64_t chunks = s.slices >= 512 ? 1 : (512 + s.slices - 1) / s.slices;
     if (chunks > tiles) chunks = tiles;
     const int64_t total = (s.slices * chunks + 7) / 8 * 8;
-    hipLaunchKernelGGL(dx_kernel<ET>, dim3((unsigned)total), dim3(256), LDS, st, a, s, (int)chunks);
+    hipLaunchKernelGGL((dx_kernel<ET, ADD>), dim3((unsigned)total), dim3(256), LDS, st, a, s, (int)chunks);
     return hipGetLastError();
 }
 
 template <int ET>
 hipError_t launch_dw(const RouterBackArgs &a, const Scratch &s, int tile0, hipStream_t st) {
-    constexpr int LDS = 2 * (BT * HS * 2 + ET * 8 * FRAG);
+    constexpr int LDS = DwCfg<ET>::LDS;
     static_assert(LDS <= 160 * 1024, "LDS");
     static std::atomic<uint64_t> lds_set{0};
     hipError_t e = lds_opt_in_once((const void *)dw_kernel<ET>, LDS, lds_set);
     if (e != hipSuccess) return e;
     const int total = (s.slices * s.splits + 7) / 8 * 8;
-    hipLaunchKernelGGL(dw_kernel<ET>, dim3((unsigned)total), dim3(256), LDS, st, a, s, tile0);
+    hipLaunchKernelGGL(dw_kernel<ET>, dim3((unsigned)total), dim3(512), LDS, st, a, s, tile0);
     return hipGetLastError();
 }
 
@@ -418,14 +539,14 @@ int64_t router_backward_scratch(int64_t T, int64_t H, int32_t E) { return scratc
 hipError_t launch_router_backward(const RouterBackArgs &a, hipStream_t st) {
     const Scratch s = scratch_of(a.scratch, a.T, a.H, a.E);
     if (s.nb > 0) {
-        const int lds = BT * (32 * s.et + 4) * 4;
+        const int lds = BT * (32 * s.et + 4 + 2 * a.k) * 4;
         static std::atomic<uint64_t> lds_set{0};
-        hipError_t e = lds_opt_in_once((const void *)dlogits_kernel, BT * (256 + 4) * 4, lds_set);
+        hipError_t e = lds_opt_in_once((const void *)dlogits_kernel, BT * (256 + 4 + 2 * 32) * 4, lds_set);
         if (e != hipSuccess) return e;
-        hipLaunchKernelGGL(dlogits_kernel, dim3((unsigned)s.nb), dim3(256), lds, st, a, s);
+        hipLaunchKernelGGL(dlogits_kernel, dim3((unsigned)s.nb), dim3(1024), lds, st, a, s);
         e = hipGetLastError();
         if (e != hipSuccess) return e;
-#define RMOE_X(N) case N: e = launch_dx<N>(a, s, st); break;
+#define RMOE_X(N) case N: e = a.add ? launch_dx<N, true>(a, s, st) : launch_dx<N, false>(a, s, st); break;
         switch (s.et) {
             RMOE_X(1) RMOE_X(2) RMOE_X(3) RMOE_X(4) RMOE_X(5) RMOE_X(6) RMOE_X(7) RMOE_X(8)
             default: return hipErrorInvalidValue;
@@ -445,9 +566,9 @@ hipError_t launch_router_backward(const RouterBackArgs &a, hipStream_t st) {
     }
     if (s.splits > 1) {
         const int64_t n = a.E * a.H / 4;
-        int64_t g = (n + 255) / 256;
-        if (g > 256 * 16) g = 256 * 16;
-        hipLaunchKernelGGL(dw_sum_kernel, dim3((unsigned)g), dim3(256), 0, st, (const f4 *)s.parts, s.splits, n, (f4 *)a.dw);
+        int64_t g = (n + 63) / 64;
+        if (g > 256 * 32) g = 256 * 32;  // strides beyond
+        hipLaunchKernelGGL(dw_sum_kernel, dim3((unsigned)g), dim3(64), 0, st, (const f4 *)s.parts, s.splits, n, (f4 *)a.dw);
         return hipGetLastError();
     }
     return hipSuccess;
