@@ -90,6 +90,12 @@ struct Tile {
     int wave, lane, ww, wt;  // ww: weight half, wt: token half (= block bx + wt)
     int64_t N, K;
     I8Ops p;
+    // The scales of the item whose products run: of the wave's 128 weight rows
+    // (gate/up: 64 gate, 64 up rows) and of its 128 tokens (down: times the
+    // routed weight), two of each per lane.  Requested with the item's first
+    // step, under the epilogue before it: a request at the epilogue's start
+    // would hold up the next item's first step by its own round trip.
+    float fs[2], ts[2];
 
     __device__ __forceinline__ Tile(const I8Args &args, unsigned char *s) : a(args), smem(s) {
         wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -122,62 +128,73 @@ struct Tile {
         p.wbase = uniform((DUAL && wave >= 2 ? a.w1 : a.w0) + ((int64_t)it.e * N + wrow0) * K);
         // an absent second block: its half reads the first block's rows
         p.tbase = uniform(a.x + ((int64_t)it.bx * kBlockM + (it.rows1 > 0 ? 64 * wave : (64 * wave) & 127)) * K);
+        // an idle wave (a narrow last slice, an absent second block) reads valid ones
+        const int64_t c0 = n0 + (DUAL ? 64 : 128) * ww, f = (int64_t)it.e * N + (c0 < N ? c0 : N - 128) + lane;
+        const int64_t row = ((int64_t)it.bx + (rows(it) > 0 ? wt : 0)) * kBlockM + lane;
+        fs[0] = a.w0s[f];
+        fs[1] = DUAL ? a.w1s[f] : a.w0s[f + 64];
+        ts[0] = a.xs[row];
+        ts[1] = a.xs[row + 64];
+        if constexpr (!DUAL) {
+            const float *rwe = a.rw + table(a.go)[it.e] + it.off + kBlockM * wt;
+            const int n = rows(it);
+            ts[0] *= lane < n ? rwe[lane] : 0.f;
+            ts[1] *= lane + 64 < n ? rwe[lane + 64] : 0.f;
+        }
     }
     // valid rows and live token tiles of this wave
     __device__ __forceinline__ int rows(const TileItem &it) const { return wt ? it.rows1 : it.rows0; }
     __device__ __forceinline__ int tiles(const TileItem &it) const {
         return DUAL || (int64_t)it.nt * 256 + 128 * ww < N ? (rows(it) + 31) / 32 : 0;
     }
-    // Pieces of this wave's LDS for staging: 8 KB each in A's slot 2 and B's
-    // slot 1, which only its own DMAs fill (all landed after the K loop; no
-    // wave reads the ring after the last barrier, and the next item's first
-    // step goes to the other slots).
+    // Two pieces of 8 KB of this wave's LDS: in A's slot 2 and B's slot 1,
+    // which only its own DMAs fill (all landed after the K loop; no wave reads
+    // the ring after the last barrier, and the next item's first step goes to
+    // the other slots).  Rows are staged in the first; the second takes the
+    // scales, 128 of weight rows and 128 of tokens.  A wave's LDS accesses
+    // happen in their order, so rows may follow rows without waiting.
     __device__ __forceinline__ unsigned char *piece(int i) const {
         return smem + (i ? B_OFF + SLOT : 2 * SLOT) + wave * 8192;
     }
+    __device__ __forceinline__ void keep_scales() const {
+        float *sc = (float *)piece(1);
+        sc[lane] = fs[0];
+        sc[64 + lane] = fs[1];
+        sc[128 + lane] = ts[0];
+        sc[192 + lane] = ts[1];
+    }
 
-    // gate/up: hidden rows in fp32, 32 tokens of 64 features per piece (256
+    // gate/up: hidden rows in fp32, 32 tokens of 64 features at a time (256
     // bytes per row, 16-byte chunks XOR-swizzled by row), whole lines out.
     // Register 4q + r of tile t holds feature 32 t + 8q + 4lh + r.
     template <int NTT, class F>
-    __device__ __forceinline__ void hidden(const TileItem &it, f16x (&acc)[4][4], F &&fill) const {
+    __device__ __forceinline__ void hidden(const TileItem &it, f16x (&acc)[4][4], F &&fill) {
         const int ln = fresh(lane), lr = ln & 31, lh = ln >> 5, c = ln & 15;
         const int64_t n0 = (int64_t)it.nt * 128 + 64 * ww, row0 = (int64_t)(it.bx + wt) * kBlockM;
         const int myrows = rows(it);
-        f4 gs[2][4], us[2][4];
-        float xs[4];
-        if constexpr (NTT > 0) {
-            const int64_t so = (int64_t)it.e * N + n0 + 4 * lh;
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    gs[t][q] = *(const f4 *)(a.w0s + so + 32 * t + 8 * q);
-                    us[t][q] = *(const f4 *)(a.w1s + so + 32 * t + 8 * q);
-                }
-#pragma unroll
-            for (int u = 0; u < NTT; ++u) xs[u] = a.xs[row0 + 32 * u + lr];
-            wait_vm<0>();  // the scales landed: a later wait for them would wait for the next item's DMAs too
-        }
+        keep_scales();
         fill();
+        const float *sc = (const float *)piece(1);
+        unsigned char *st = piece(0);
         float *ybase = a.rows + row0 * N + n0 + 4 * c;
 #pragma unroll
         for (int u = 0; u < NTT; ++u) {
-            unsigned char *st = piece(u & 1);
+            __builtin_amdgcn_sched_barrier(0);  // no accumulator is copied out early: registers
+            const float xs = sc[128 + 32 * u + lr];
 #pragma unroll
             for (int t = 0; t < 2; ++t)
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
+                    const f4 gs = *(const f4 *)(sc + 32 * t + 8 * q + 4 * lh), us = *(const f4 *)(sc + 64 + 32 * t + 8 * q + 4 * lh);
                     f4 h;
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        const float g = sum_of(acc[t][u][4 * q + r]) * (xs[u] * gs[t][q][r]);
-                        const float v = sum_of(acc[t + 2][u][4 * q + r]) * (xs[u] * us[t][q][r]);
+                        const float g = sum_of(acc[t][u][4 * q + r]) * (xs * gs[r]);
+                        const float v = sum_of(acc[t + 2][u][4 * q + r]) * (xs * us[r]);
                         h[r] = silu(g) * v;
                     }
                     *(f4 *)(st + lr * 256 + (((8 * t + 2 * q + lh) ^ (lr & 15)) << 4)) = h;
                 }
-            __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): this wave's staging writes are done
             f4 v[8];  // read together: one LDS round trip, not eight
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
@@ -192,67 +209,47 @@ struct Tile {
         }
     }
 
-    // down: out rows, 64 at a time staged through LDS for whole-line stores:
-    // 128 columns per row, 16-byte chunks XOR-swizzled by row.
+    // down: out rows, 32 tokens of 128 columns at a time, staged as above.
     template <int NTT, class F>
-    __device__ __forceinline__ void out(const TileItem &it, f16x (&acc)[4][4], F &&fill) const {
-        const int ln = fresh(lane), lr = ln & 31, lh = ln >> 5;
+    __device__ __forceinline__ void out(const TileItem &it, f16x (&acc)[4][4], F &&fill) {
+        const int ln = fresh(lane), lr = ln & 31, lh = ln >> 5, c = ln & 15;
         const int64_t row0 = (int64_t)(it.bx + wt) * kBlockM, n0 = (int64_t)it.nt * 256 + 128 * ww;
         const int myrows = rows(it);
-        f4 ds[4][4];
-        float w[4];
-        if constexpr (NTT > 0) {
+        keep_scales();
+        fill();
+        const float *sc = (const float *)piece(1);
+        unsigned char *st = piece(0);
+        _Float16 *ybase = a.y + row0 * N + n0 + 8 * c;
+#pragma unroll
+        for (int u = 0; u < NTT; ++u) {
+            __builtin_amdgcn_sched_barrier(0);  // no accumulator is copied out early: registers
+            const float w = sc[128 + 32 * u + lr];
 #pragma unroll
             for (int t = 0; t < 4; ++t)
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    ds[t][q] = *(const f4 *)(a.w0s + (int64_t)it.e * N + n0 + 32 * t + 8 * q + 4 * lh);
-            const float *rwe = a.rw + table(a.go)[it.e] + it.off + kBlockM * wt;
+                for (int q = 0; q < 4; ++q) {
+                    const f16x &o = acc[t][u];
+                    const f4 d = *(const f4 *)(sc + 32 * t + 8 * q + 4 * lh);
+                    *(h4 *)(st + lr * 256 + (((4 * t + q) ^ (lr & 15)) << 4) + 8 * lh) =
+                        to_h4(sum_of(o[4 * q + 0]) * (w * d[0]), sum_of(o[4 * q + 1]) * (w * d[1]),
+                              sum_of(o[4 * q + 2]) * (w * d[2]), sum_of(o[4 * q + 3]) * (w * d[3]));
+                }
+            h8 v[8];  // read together: one LDS round trip, not eight
 #pragma unroll
-            for (int u = 0; u < NTT; ++u) {
-                w[u] = 0.f;
-                if (32 * u + lr < myrows) w[u] = a.xs[row0 + 32 * u + lr] * rwe[32 * u + lr];
+            for (int j = 0; j < 8; ++j) {
+                const int r = 4 * j + (ln >> 4);
+                v[j] = *(const h8 *)(st + r * 256 + ((c ^ (r & 15)) << 4));
             }
-            wait_vm<0>();  // as in hidden()
-        }
-        fill();
-        _Float16 *ybase = a.y + row0 * N + n0;
-        const int c = ln & 15;
 #pragma unroll
-        for (int u0 = 0; u0 < NTT; u0 += 2) {
-            __builtin_amdgcn_sched_barrier(0);  // no accumulator is copied out early: registers
-#pragma unroll
-            for (int u = u0; u < u0 + 2 && u < NTT; ++u)
-#pragma unroll
-                for (int t = 0; t < 4; ++t)
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const f16x &o = acc[t][u];
-                        const f4 d = ds[t][q];
-                        *(h4 *)(piece(u - u0) + lr * 256 + (((4 * t + q) ^ (lr & 15)) << 4) + 8 * lh) =
-                            to_h4(sum_of(o[4 * q + 0]) * (w[u] * d[0]), sum_of(o[4 * q + 1]) * (w[u] * d[1]),
-                                  sum_of(o[4 * q + 2]) * (w[u] * d[2]), sum_of(o[4 * q + 3]) * (w[u] * d[3]));
-                    }
-            __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): this wave's staging writes are done
-#pragma unroll
-            for (int u = u0; u < u0 + 2 && u < NTT; ++u) {
-                h8 v[8];  // read together: one LDS round trip, not eight
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int r = 4 * j + (ln >> 4);
-                    v[j] = *(const h8 *)(piece(u - u0) + r * 256 + ((c ^ (r & 15)) << 4));
-                }
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int row = 32 * u + 4 * j + (ln >> 4);
-                    if (row < myrows) *(h8 *)(ybase + (int64_t)row * N + 8 * c) = v[j];
-                }
+            for (int j = 0; j < 8; ++j) {
+                const int row = 32 * u + 4 * j + (ln >> 4);
+                if (row < myrows) *(h8 *)(ybase + (int64_t)row * N) = v[j];
             }
         }
     }
 
     template <int NTT, class F>
-    __device__ __forceinline__ bool finish(const TileItem &it, f16x (&acc)[4][4], F &&fill) const {
+    __device__ __forceinline__ bool finish(const TileItem &it, f16x (&acc)[4][4], F &&fill) {
         if constexpr (DUAL)
             hidden<NTT>(it, acc, fill);
         else
