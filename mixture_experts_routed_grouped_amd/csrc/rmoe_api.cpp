@@ -854,8 +854,19 @@ int check_i8_sizes(int32_t type, int64_t rows, int64_t cols, bool *empty) {
     return RMOE_OK;
 }
 
+// Streaming reads an expert's weights once per 64 rows of each of its blocks.
+// Forward times of both families (one MI355X, the tiled one's over the
+// streaming one's; equal groups, then Zipf 1.2): E=1 (4096, 14336) 1.74 at 64
+// rows per expert, 1.23 at 128; E=2 1.90 and 1.03; E=8 (4096, 14336) 1.22 and
+// 0.91 at 48, 1.17 and 0.77 at 64; E=8 (2048, 5632) 1.48 and 1.19, 1.34 and
+// 1.03; E=16 (4096, 14336) 1.04 and 0.88 at 32, 0.98 and 0.81 at 40; E=32
+// (4096, 2048) 1.23 and 1.34 at 40, 1.17 and 1.05 at 64; E=64 (2048, 1408)
+// 1.10 and 1.12, 1.09 and 1.04; E=128 (7168, 2048) 1.00 and 0.97, 0.96 and
+// 0.81.
 int pick_variant_i8(int32_t variant, int64_t pairs, int32_t num_experts) {
-    return pick_variant(variant, pairs, num_experts);
+    if (variant == RMOE_VARIANT_STREAM || variant == RMOE_VARIANT_TILE) return variant;
+    const int64_t rows = num_experts <= 4 ? 128 : num_experts <= 8 ? 56 : num_experts < 32 ? 32 : 40;
+    return pairs <= rows * num_experts ? RMOE_VARIANT_STREAM : RMOE_VARIANT_TILE;
 }
 
 int i8_gate_up_impl(const rmoe::I8Args &a, int32_t variant, int64_t pairs, void *stream) {
