@@ -900,12 +900,14 @@ def quantize_int8(x, codes=None, scales=None, stream=None):
     if len(shape) < 1:
         raise ValueError("x must have rows")
     if codes is None:
-        codes = _empty(shape, torch.int8, dev, stream)
+        # empty_like is the quickest way to memory on the current stream
+        codes = torch.empty_like(x, dtype=torch.int8) if stream is None else _empty(shape, torch.int8, dev, stream)
         pc = codes.data_ptr()
     else:
         pc = _arg(dev, "codes", codes, torch.int8, *shape)
     if scales is None:
-        scales = _empty(shape[:-1], torch.float32, dev, stream)
+        scales = x.new_empty(shape[:-1], dtype=torch.float32) if stream is None else \
+            _empty(shape[:-1], torch.float32, dev, stream)
         ps = scales.data_ptr()
     else:
         ps = _i8_scales(dev, "scales", scales, shape)
@@ -931,7 +933,7 @@ def dequantize_int8(codes, scales, dtype=None, out=None, stream=None):
     shape = codes.shape
     pc, ps = _arg(dev, "codes", codes, torch.int8), _i8_scales(dev, "scales", scales, shape)
     if out is None:
-        out = _empty(shape, dtype, dev, stream)
+        out = torch.empty_like(codes, dtype=dtype) if stream is None else _empty(shape, dtype, dev, stream)
         po = out.data_ptr()
     else:
         po = _arg(dev, "out", out, dtype, *shape)

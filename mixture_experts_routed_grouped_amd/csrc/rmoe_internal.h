@@ -107,6 +107,7 @@ struct RouterTrainArgs {
     float *losses;          // [2]: balance, z
     RouterPart *parts;      // [parts, E] probabilities, pairs
     RouterPart *tokens;     // [parts] lse^2, tokens
+    int32_t lag;            // set by the launcher
 };
 int64_t router_train_parts(int64_t T);  // at most
 hipError_t launch_router_train(const RouterTrainArgs &a, hipStream_t s);

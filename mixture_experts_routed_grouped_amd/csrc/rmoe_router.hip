@@ -60,7 +60,7 @@ __device__ __forceinline__ bool better(float s, int e, float s2, int e2) {
 // over the workgroup's tokens.
 template <int EP, int TOK, bool TRAIN>
 __device__ __forceinline__ void router_body(const _Float16 *__restrict__ x, const _Float16 *__restrict__ w, int64_t T,
-                                            int64_t H, int32_t E, int32_t k, int32_t *__restrict__ ids,
+                                            int64_t H, int32_t E, int32_t k, int32_t lag_, int32_t *__restrict__ ids,
                                             float *__restrict__ vals, const RouterTrainArgs &tr) {
     using C = RouterCfg<EP, TOK>;
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
@@ -76,12 +76,18 @@ __device__ __forceinline__ void router_body(const _Float16 *__restrict__ x, cons
 
     // every workgroup reads the same gate rows: each starts its K sweep at a
     // different chunk, so that concurrent workgroups do not ask the L2 for
-    // the same lines at the same moment (a token's sum order stays fixed)
+    // the same lines at the same moment (a token's sum order stays fixed).
+    // With a lag the two halves of 64 tokens are sums of two workgroups of 32:
+    // the second half joins the sweep lag chunks after the first, where its
+    // own workgroup would have started, and goes on as long after the first's
+    // end (the same sums, the gate rows read once for both).
     const int nk = (int)(H / RT_CK);
-    const int kofs = (int)((blockIdx.x * 7u) % (unsigned)nk);
+    const int lag = TOK == 64 ? lag_ : 0, sweep = nk + lag;
+    const int kofs = (int)((blockIdx.x * (TOK == 64 && lag ? 14u : 7u)) % (unsigned)nk);
     auto chunk = [&](int kc) -> int64_t {  // element offset; clamped at the end: repeats land in stages no later chunk reads
-        kc = kc < nk ? kc : nk - 1;
-        return (int64_t)(kc + kofs < nk ? kc + kofs : kc + kofs - nk) * RT_CK;
+        kc = (kc < sweep ? kc : sweep - 1) + kofs;
+        kc = kc < nk ? kc : kc - nk;
+        return (int64_t)(kc < nk ? kc : kc - nk) * RT_CK;
     };
     const unsigned lds0 = (unsigned)(uintptr_t)smem;
     // DMA instruction j moves rows 8j .. 8j+7 of a chunk (tokens clamped to
@@ -101,7 +107,7 @@ __device__ __forceinline__ void router_body(const _Float16 *__restrict__ x, cons
         };
 #pragma unroll
         for (int p = 0; p < RT_XST - 1; ++p) dma(p);
-        for (int kc = 0; kc < nk; ++kc) {
+        for (int kc = 0; kc < sweep; ++kc) {
             wait_vm<(RT_XST - 2) * C::NIX>();  // chunk kc landed
             bar();
             dma(kc + RT_XST - 1);
@@ -131,10 +137,14 @@ __device__ __forceinline__ void router_body(const _Float16 *__restrict__ x, cons
 
 #pragma unroll
     for (int p = 0; p < RT_WST - 1; ++p) dma(p);
-    for (int kc = 0; kc < nk; ++kc) {
+    for (int kc = 0; kc < sweep; ++kc) {
         wait_vm<(RT_WST - 2) * C::NIW>();    // chunk kc landed (own DMAs) ...
         __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): this wave's reads of chunk kc-1
         bar();  // ... and everyone's; and every wave is done with chunk kc-1's stages
+        if (lag && (th ? kc < lag : kc >= nk)) {  // the other half's part of the sweep
+            dma(kc + RT_WST - 1);
+            continue;
+        }
         // the wave's operands of the chunk, all requested before the first MFMA
         const unsigned char *bx = smem + (kc % RT_XST) * C::XSTAGE;
         const unsigned char *bw = smem + C::W_OFF + (kc % RT_WST) * C::WSTAGE;
@@ -221,6 +231,7 @@ __device__ __forceinline__ void router_body(const _Float16 *__restrict__ x, cons
     float *zs = reinterpret_cast<float *>(cnt + EP), *on = zs + TOK;
     bool counts = live;
     if constexpr (TRAIN) {
+        if (blockIdx.x == 0 && tid == 0) tr.losses[0] = 0.f;  // the next kernel counts there
         counts = live && (tr.mask == nullptr || tr.mask[t0 + tok] != 0);
         __syncthreads();  // idle threads (tok >= TOK) have read their rows there
         for (int e = tid; e < EP; e += 256) cnt[e] = 0;
@@ -299,37 +310,46 @@ __device__ __forceinline__ void router_body(const _Float16 *__restrict__ x, cons
 template <int EP, int TOK>
 __global__ __launch_bounds__(320) void router_kernel(const _Float16 *__restrict__ x,
                                                      const _Float16 *__restrict__ w, int64_t T,
-                                                     int64_t H, int32_t E, int32_t k,
+                                                     int64_t H, int32_t E, int32_t k, int32_t lag,
                                                      int32_t *__restrict__ ids,
                                                      float *__restrict__ vals) {
-    router_body<EP, TOK, false>(x, w, T, H, E, k, ids, vals, RouterTrainArgs{});
+    router_body<EP, TOK, false>(x, w, T, H, E, k, lag, ids, vals, RouterTrainArgs{});
 }
 
 template <int EP, int TOK>
 __global__ __launch_bounds__(320) void router_train_kernel(RouterTrainArgs a) {
-    router_body<EP, TOK, true>(a.x, a.w, a.T, a.H, a.E, a.k, a.ids, a.vals, a);
+    router_body<EP, TOK, true>(a.x, a.w, a.T, a.H, a.E, a.k, a.lag, a.ids, a.vals, a);
 }
 
-// Sums of the workgroups' parts and the losses: one workgroup, a slice of
-// the parts per 1024 / EP threads, then the slices in order.
+// Sums of the workgroups' parts and the losses.  A workgroup takes 32 experts
+// (512 parts of 128 experts read by one workgroup cost 11 us, by four 5), 32
+// slices of the parts each, then the slices in order; it leaves its experts'
+// share of the balance loss where its first part was (which no other one
+// reads), and the last to finish adds the shares in order.  The count of
+// finished workgroups is kept in losses[0], zeroed by the kernel before.
 __global__ __launch_bounds__(1024) void router_losses_kernel(RouterTrainArgs a, int parts) {
     __shared__ double ps[1024], zsum[16];
     __shared__ int32_t cs[1024], nsum[16];
-    const int EP = (a.E + 31) / 32 * 32, slices = 1024 / EP, e = threadIdx.x % EP, sl = threadIdx.x / EP;
-    double p = 0.0;
-    int32_t c = 0;
-    if (e < a.E && sl < slices)
-#pragma unroll 32
-        for (int b = sl; b < parts; b += slices) {
+    __shared__ bool last;
+    const int tid = threadIdx.x, sl = tid >> 5, e = blockIdx.x * 32 + (tid & 31);
+    if (parts == 0) {
+        if (sl == 0 && e < a.E) a.counts[e] = 0;
+        if (e == 0 && sl == 0) {
+            a.counts[a.E] = 0;
+            a.losses[0] = a.losses[1] = 0.f;
+        }
+        return;
+    }
+    double p = 0.0, z = 0.0;
+    int32_t c = 0, n = 0;
+    if (e < a.E)
+#pragma unroll 16
+        for (int b = sl; b < parts; b += 32) {
             const RouterPart r = a.parts[(int64_t)b * a.E + e];
             p += r.sum;
             c += r.count;
         }
-    ps[threadIdx.x] = p;
-    cs[threadIdx.x] = c;
-    double z = 0.0;
-    int32_t n = 0;
-    for (int b = threadIdx.x; b < parts; b += 1024) {
+    for (int b = tid; b < parts; b += 1024) {
         const RouterPart r = a.tokens[b];
         z += r.sum;
         n += r.count;
@@ -338,49 +358,54 @@ __global__ __launch_bounds__(1024) void router_losses_kernel(RouterTrainArgs a, 
         z += __shfl_xor(z, d);
         n += __shfl_xor(n, d);
     }
-    if ((threadIdx.x & 63) == 0) {
-        zsum[threadIdx.x >> 6] = z;
-        nsum[threadIdx.x >> 6] = n;
+    ps[tid] = p;
+    cs[tid] = c;
+    if ((tid & 63) == 0) {
+        zsum[tid >> 6] = z;
+        nsum[tid >> 6] = n;
     }
     __syncthreads();
+    double *share = reinterpret_cast<double *>(a.parts + blockIdx.x * 32);
+    if (tid < 32) {
+        for (int i = 1; i < 32; ++i) {
+            p += ps[32 * i + tid];
+            c += cs[32 * i + tid];
+        }
+        if (e < a.E) a.counts[e] = c;
+        double term = p * c;
+        for (int d = 1; d < 32; d <<= 1) term += __shfl_xor(term, d, 32);
+        if (tid == 0) {
+            __hip_atomic_store(share, term, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            last = __hip_atomic_fetch_add(reinterpret_cast<int32_t *>(a.losses), 1, __ATOMIC_ACQ_REL,
+                                          __HIP_MEMORY_SCOPE_AGENT) == (int)gridDim.x - 1;
+        }
+    }
+    __syncthreads();
+    if (!last || tid != 0) return;
     z = 0.0;
     n = 0;
     for (int i = 0; i < 16; ++i) {
         z += zsum[i];
         n += nsum[i];
     }
-    double term = 0.0;
-    if (sl == 0 && e < a.E) {
-        for (int i = 1; i < slices; ++i) {
-            p += ps[i * EP + e];
-            c += cs[i * EP + e];
-        }
-        a.counts[e] = c;
-        term = p * c;
-    }
-    for (int d = 1; d < 64; d <<= 1) term += __shfl_xor(term, d);
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) ps[threadIdx.x >> 6] = term;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        double s = 0.0;
-        for (int i = 0; i < 4; ++i) s += ps[i];  // experts: the first 256 threads
-        a.counts[a.E] = n;
-        a.losses[0] = n > 0 ? (float)(s * a.E / ((double)a.k * n * n)) : 0.f;
-        a.losses[1] = n > 0 ? (float)(z / n) : 0.f;
-    }
+    double s = 0.0;
+    for (unsigned i = 0; i < gridDim.x; ++i)
+        s += __hip_atomic_load(reinterpret_cast<double *>(a.parts + i * 32), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    a.counts[a.E] = n;
+    a.losses[0] = n > 0 ? (float)(s * a.E / ((double)a.k * n * n)) : 0.f;
+    a.losses[1] = n > 0 ? (float)(z / n) : 0.f;
 }
 
 template <int EP, int TOK>
 hipError_t launch_ep(const _Float16 *x, const _Float16 *w, int64_t T, int64_t H, int32_t E,
-                     int32_t k, int32_t *ids, float *vals, hipStream_t s) {
+                     int32_t k, int32_t lag, int32_t *ids, float *vals, hipStream_t s) {
     using C = RouterCfg<EP, TOK>;
     static std::atomic<uint64_t> lds_set{0};
     hipError_t e = lds_opt_in_once((const void *)router_kernel<EP, TOK>, C::LDS_BYTES, lds_set);
     if (e != hipSuccess) return e;
     const unsigned grid = (unsigned)((T + TOK - 1) / TOK);
     hipLaunchKernelGGL((router_kernel<EP, TOK>), dim3(grid), dim3(320), C::LDS_BYTES, s, x, w, T, H,
-                       E, k, ids, vals);
+                       E, k, lag, ids, vals);
     return hipGetLastError();
 }
 
@@ -393,13 +418,6 @@ hipError_t launch_train_ep(const RouterTrainArgs &a, hipStream_t s) {
     hipLaunchKernelGGL((router_train_kernel<EP, TOK>), dim3((unsigned)((a.T + TOK - 1) / TOK)), dim3(320), C::LDS_BYTES,
                        s, a);
     return hipGetLastError();
-}
-
-template <int EP>
-hipError_t launch_tok(int tok, const _Float16 *x, const _Float16 *w, int64_t T, int64_t H,
-                      int32_t E, int32_t k, int32_t *ids, float *vals, hipStream_t s) {
-    if (tok == 64) return launch_ep<EP, 64>(x, w, T, H, E, k, ids, vals, s);
-    return launch_ep<EP, 32>(x, w, T, H, E, k, ids, vals, s);
 }
 
 // Compute units of the current device (cached per device).
@@ -418,21 +436,28 @@ hipError_t cu_count(int &n) {
     return hipSuccess;
 }
 
-// 64 once that still gives two workgroups per CU
-hipError_t tokens_per_workgroup(int64_t T, int &tok) {
+// Tokens per workgroup: 64 once that still gives two workgroups per CU; from
+// one per CU on, 64 as two lagging halves (16384 tokens, H = 7168, E = 128:
+// 94 -> 79 us) where workgroups of 32 do not split a chunk's K-steps, whose
+// sums are another order.
+hipError_t tokens_per_workgroup(int64_t T, int64_t H, int32_t E, int &tok, int32_t &lag) {
     int cus = 0;
-    hipError_t e = cu_count(cus);
-    tok = T >= (int64_t)64 * 2 * cus ? 64 : 32;
-    return e;
+    const hipError_t e = cu_count(cus);
+    if (e != hipSuccess) return e;
+    const bool halves = E > 64 && T >= (int64_t)64 * cus && T < (int64_t)64 * 2 * cus;
+    tok = halves || T >= (int64_t)64 * 2 * cus ? 64 : 32;
+    lag = halves ? (int32_t)(7 % (H / RT_CK)) : 0;
+    return hipSuccess;
 }
 
 }  // namespace
 
 int64_t router_train_parts(int64_t T) { return (T + 31) / 32; }
 
-hipError_t launch_router_train(const RouterTrainArgs &a, hipStream_t s) {
+hipError_t launch_router_train(const RouterTrainArgs &args, hipStream_t s) {
+    RouterTrainArgs a = args;
     int tok = 0;
-    hipError_t e = tokens_per_workgroup(a.T, tok);
+    hipError_t e = tokens_per_workgroup(a.T, a.H, a.E, tok, a.lag);
     if (e != hipSuccess) return e;
     if (a.T > 0) {
 #define RMOE_R(N) \
@@ -444,7 +469,8 @@ hipError_t launch_router_train(const RouterTrainArgs &a, hipStream_t s) {
 #undef RMOE_R
         if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL(router_losses_kernel, dim3(1), dim3(1024), 0, s, a, (int)((a.T + tok - 1) / tok));
+    hipLaunchKernelGGL(router_losses_kernel, dim3((unsigned)((a.E + 31) / 32)), dim3(1024), 0, s, a,
+                       (int)((a.T + tok - 1) / tok));
     return hipGetLastError();
 }
 
@@ -452,19 +478,18 @@ hipError_t launch_router(const _Float16 *x, const _Float16 *w, int64_t T, int64_
                          int32_t k, int32_t *ids, float *vals, hipStream_t s) {
     if (T == 0 || k == 0) return hipSuccess;
     int tok = 0;
-    hipError_t e = tokens_per_workgroup(T, tok);
+    int32_t lag = 0;
+    hipError_t e = tokens_per_workgroup(T, H, E, tok, lag);
     if (e != hipSuccess) return e;
+#define RMOE_R(N)                                                                        \
+    case N:                                                                              \
+        return tok == 64 ? launch_ep<32 * N, 64>(x, w, T, H, E, k, lag, ids, vals, s)    \
+                         : launch_ep<32 * N, 32>(x, w, T, H, E, k, 0, ids, vals, s);
     switch ((E + 31) / 32) {
-        case 1: return launch_tok<32>(tok, x, w, T, H, E, k, ids, vals, s);
-        case 2: return launch_tok<64>(tok, x, w, T, H, E, k, ids, vals, s);
-        case 3: return launch_tok<96>(tok, x, w, T, H, E, k, ids, vals, s);
-        case 4: return launch_tok<128>(tok, x, w, T, H, E, k, ids, vals, s);
-        case 5: return launch_tok<160>(tok, x, w, T, H, E, k, ids, vals, s);
-        case 6: return launch_tok<192>(tok, x, w, T, H, E, k, ids, vals, s);
-        case 7: return launch_tok<224>(tok, x, w, T, H, E, k, ids, vals, s);
-        case 8: return launch_tok<256>(tok, x, w, T, H, E, k, ids, vals, s);
+        RMOE_R(1) RMOE_R(2) RMOE_R(3) RMOE_R(4) RMOE_R(5) RMOE_R(6) RMOE_R(7) RMOE_R(8)
         default: return hipErrorInvalidValue;
     }
+#undef RMOE_R
 }
 
 }  // namespace rmoe

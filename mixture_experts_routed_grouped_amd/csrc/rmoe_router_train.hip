@@ -393,12 +393,15 @@ __global__ __launch_bounds__(512) void dw_kernel(RouterBackArgs a, Scratch s, in
     const _Float16 *xbase = uniform(a.x + (cx < a.H ? cx : a.H - 64));  // idle columns read valid ones
     const int tx = 16 * (wave & 1) + r8;
     const unsigned xstep = (unsigned)(16 * a.H), xoff = (unsigned)(tx * a.H * 2) + 16 * ((lane & 7) ^ swz_k(r8));
-    // step i; past the last one the last again, so that every wait counts the same
+    // step i; past the last one the last again, so that every wait counts the
+    // same.  The mask of the next step is requested here and used there.
+    uint64_t mask = n > 0 ? live[b0] : 0;
     auto fill = [&](int64_t i) {
         const unsigned d = lds + (unsigned)(i % C::D) * C::SLOT;
         const int64_t j = i < n ? i : n - 1, b = b0 + (j >> 1);
         const int half = (int)(j & 1);
-        const unsigned on = (unsigned)(live[b] >> (32 * half));
+        const unsigned on = (unsigned)(mask >> (32 * half));
+        mask = live[b0 + ((i + 1 < n ? i + 1 : n - 1) >> 1)];
         const _Float16 *src = xbase + (b * BT + 32 * half) * a.H;
         if (on == ~0u) {
             dma16_sb(src, xoff, d + (2 * wave) * FRAG);
