@@ -443,7 +443,8 @@ RMOE_API int rmoe_router_f16(const void *x, const void *router_w, int64_t num_to
  * irrelevant on entry.  Sums run in an order fixed by the sizes: equal calls
  * give equal bits.  Shapes: as rmoe_router_f16 with top_k >= 1, hidden at
  * most 2^20, num_tokens * top_k at most 2^31 - 1.  fp16 tensors 16-byte,
- * scratch 8-byte, the rest (but the mask) 4-byte aligned.  Two launches on `stream`.
+ * scratch 8-byte, the rest (but the mask) 4-byte aligned.  At most two launches
+ * on `stream`.
  */
 RMOE_API size_t rmoe_router_train_scratch_bytes(int64_t num_tokens, int32_t num_experts);
 RMOE_API int rmoe_router_train_f16(const void *x, const void *router_w, const uint8_t *token_mask,
@@ -471,7 +472,7 @@ RMOE_API int rmoe_router_train_f16(const void *x, const void *router_w, const ui
  * scratch: rmoe_router_backward_scratch_bytes(num_tokens, hidden, E) bytes,
  * 16-byte aligned, contents irrelevant on entry.  Sums run in a fixed order.
  * Shapes and alignment as rmoe_router_train_f16 (drouter_w and dx_add 16).
- * At most five launches on `stream`.
+ * At most six launches on `stream`.
  */
 RMOE_API size_t rmoe_router_backward_scratch_bytes(int64_t num_tokens, int64_t hidden, int32_t num_experts);
 RMOE_API int rmoe_router_backward_f16(const void *x, const void *router_w, const uint8_t *token_mask,

@@ -55,6 +55,13 @@ __device__ __forceinline__ bool better(float s, int e, float s2, int e2) {
     return s > s2 || (s == s2 && e < e2);
 }
 
+// The losses and the count of tokens from the sums over all tokens.
+__device__ __forceinline__ void router_losses(double sum_pc, double z, int n, const RouterTrainArgs &a) {
+    a.counts[a.E] = n;
+    a.losses[0] = n > 0 ? (float)(sum_pc * a.E / ((double)a.k * n * n)) : 0.f;
+    a.losses[1] = n > 0 ? (float)(z / n) : 0.f;
+}
+
 // TRAIN: the training forward, which also keeps the probabilities and each
 // token's logsumexp, leaves out masked tokens and sums what the losses need
 // over the workgroup's tokens.
@@ -231,7 +238,6 @@ __device__ __forceinline__ void router_body(const _Float16 *__restrict__ x, cons
     float *zs = reinterpret_cast<float *>(cnt + EP), *on = zs + TOK;
     bool counts = live;
     if constexpr (TRAIN) {
-        if (blockIdx.x == 0 && tid == 0) tr.losses[0] = 0.f;  // the next kernel counts there
         counts = live && (tr.mask == nullptr || tr.mask[t0 + tok] != 0);
         __syncthreads();  // idle threads (tok >= TOK) have read their rows there
         for (int e = tid; e < EP; e += 256) cnt[e] = 0;
@@ -287,22 +293,38 @@ __device__ __forceinline__ void router_body(const _Float16 *__restrict__ x, cons
         for (int t = wave; t < nt; t += 4)
             for (int e = lane; e < E; e += 64) tr.probs[(t0 + t) * E + e] = L[t * LD + e];
         // sums over the workgroup's tokens, in a fixed order
+        float sum_p = 0.f, z = 0.f, n = 0.f;
         if (tid < E) {
-            float s = 0.f;
 #pragma unroll 8
-            for (int t = 0; t < nt; ++t) s += L[t * LD + tid];
-            tr.parts[(int64_t)blockIdx.x * E + tid] = RouterPart{s, cnt[tid]};
+            for (int t = 0; t < nt; ++t) sum_p += L[t * LD + tid];
         }
         if (wave == 3) {  // zs and on hold TOK entries, zeros past the last token
-            float z = lane < TOK ? zs[lane] : 0.f, n = lane < TOK ? on[lane] : 0.f;
+            z = lane < TOK ? zs[lane] : 0.f;
+            n = lane < TOK ? on[lane] : 0.f;
 #pragma unroll
             for (int d = 1; d < 64; d <<= 1) {
                 z += __shfl_xor(z, d);
                 n += __shfl_xor(n, d);
             }
-            if (lane == 0) {
-                tr.tokens[blockIdx.x] = RouterPart{z, (int)n};
+        }
+        if (gridDim.x > 1) {
+            if (tid < E) tr.parts[(int64_t)blockIdx.x * E + tid] = RouterPart{sum_p, cnt[tid]};
+            if (tid == 192) tr.tokens[blockIdx.x] = RouterPart{z, (int)n};
+            if (blockIdx.x == 0 && tid == 0) tr.losses[0] = 0.f;  // the next kernel counts there
+        } else {  // the batch's only workgroup gives the losses itself
+            double term = tid < E ? (double)sum_p * cnt[tid] : 0.0;
+            if (tid < E) tr.counts[tid] = cnt[tid];
+            for (int d = 1; d < 64; d <<= 1) term += __shfl_xor(term, d);
+            __syncthreads();  // the rows are done with
+            double *part = reinterpret_cast<double *>(L);
+            if (lane == 0) part[wave] = term;
+            if (tid == 192) {
+                part[4] = z;
+                part[5] = n;
             }
+            __syncthreads();
+            if (tid == 0)
+                router_losses((part[0] + part[1]) + (part[2] + part[3]), part[4], (int)part[5], tr);
         }
     }
 }
@@ -391,9 +413,7 @@ __global__ __launch_bounds__(1024) void router_losses_kernel(RouterTrainArgs a, 
     double s = 0.0;
     for (unsigned i = 0; i < gridDim.x; ++i)
         s += __hip_atomic_load(reinterpret_cast<double *>(a.parts + i * 32), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    a.counts[a.E] = n;
-    a.losses[0] = n > 0 ? (float)(s * a.E / ((double)a.k * n * n)) : 0.f;
-    a.losses[1] = n > 0 ? (float)(z / n) : 0.f;
+    router_losses(s, z, n, a);
 }
 
 template <int EP, int TOK>
@@ -469,6 +489,7 @@ hipError_t launch_router_train(const RouterTrainArgs &args, hipStream_t s) {
 #undef RMOE_R
         if (e != hipSuccess) return e;
     }
+    if (a.T > 0 && a.T <= tok) return hipSuccess;
     hipLaunchKernelGGL(router_losses_kernel, dim3((unsigned)((a.E + 31) / 32)), dim3(1024), 0, s, a,
                        (int)((a.T + tok - 1) / tok));
     return hipGetLastError();

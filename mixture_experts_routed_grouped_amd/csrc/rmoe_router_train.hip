@@ -7,7 +7,8 @@
 //     dx    = dl . W             (a sum over the experts)
 //     dW[e] = sum_t dl[t, e] x[t]
 //
-// Three steps: dl, 64 tokens per workgroup; dx; dW.  The products run on fp16
+// Steps: dl, 64 tokens per workgroup; dx and dW, in one launch up to 128
+// experts; the parts of dW added up.  The products run on fp16
 // MFMA, so dl, which is fp32, becomes two fp16 operands, the value rounded
 // and what that rounding left (22 bits): once scaled by a power of two per
 // token (for dx), once by one per expert and 64 tokens (for dW), so that the
@@ -231,22 +232,26 @@ struct DxCfg {
     static constexpr int W = ET * 16 * FRAG;         // the gate matrix's 256 columns, before the loop
     static constexpr int LDS = W > D * SLOT ? W : D * SLOT;
 };
+// A value that is the same in every lane, in a scalar register (under two
+// nested branches the compiler kept LDS addresses in vector registers, which
+// the DMA's M0 cannot take).
+__device__ __forceinline__ unsigned scalar(unsigned x) { return __builtin_amdgcn_readfirstlane(x); }
 // 256-byte DMA: lane i stores the dword at g to LDS byte lds + 4 i (s_nop: as
 // in dma16)
 __device__ __forceinline__ void dma4(const void *g, unsigned lds) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(lds), "v"(g) : "memory", "m0");
 }
 template <int ET, bool ADD>
-__global__ __launch_bounds__(256) void dx_kernel(RouterBackArgs a, Scratch s, int chunks) {
+__device__ __forceinline__ void dx_body(const RouterBackArgs &a, const Scratch &s, int chunks, int block,
+                                        unsigned char *smem) {
     using C = DxCfg<ET>;
     constexpr int KS = C::KS;
-    extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
     const int lr = lane & 31, lh = lane >> 5;
     // an XCD's workgroups take neighbouring chunks of tokens, whose operands its L2 holds
     const int total = s.slices * chunks, per = (total + 7) / 8;
-    const int at = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
-    if ((int)(blockIdx.x >> 3) >= per || at >= total) return;
+    const int at = (block & 7) * per + (block >> 3);
+    if ((block >> 3) >= per || at >= total) return;
     const int chunk = at / s.slices, slice = at - chunk * s.slices;
     const int64_t c0 = (int64_t)slice * HS + 64 * wave;  // this wave's columns
     const bool mine = c0 < a.H;
@@ -358,29 +363,30 @@ __global__ __launch_bounds__(256) void dx_kernel(RouterBackArgs a, Scratch s, in
 // ---- dW: a workgroup takes 256 columns of H, up to 4 expert tiles and a
 // part of the blocks of tokens, which it runs through in steps of 32 tokens: x
 // as a k-major slot, the operands of dl as they are, and the experts' scales,
-// all by DMA three steps ahead.  8 waves, 4 groups of 64 columns x 2 halves of
-// the expert tiles: two per SIMD, one's scaling and addresses beside the
-// other's MFMAs.  A block's sums are scaled back and added up in fp32 after
-// its second step.
-template <int ET>
+// all by DMA D - 1 steps ahead.  NW = 8 waves, 4 groups of 64 columns x 2
+// halves of the expert tiles: two per SIMD, one's scaling and addresses beside
+// the other's MFMAs; or 4, each with every tile.  A block's sums are scaled
+// back and added up in fp32 after its second step.
+template <int ET, int NW, int D_>
 struct DwCfg {
-    static constexpr int XB = 32 * HS * 2, DB = ET * 4 * FRAG, SB = 8 * 256;  // bytes of a step: tokens, operands, scales
-    static constexpr int SLOT = XB + DB + SB, D = 4;
-    static constexpr int TPW = (ET + 1) / 2;     // expert tiles per wave
-    static constexpr int OPW = (4 * ET + 7) / 8;  // operands moved per wave
-    static constexpr int DMAS = 2 + OPW + 1;     // per wave and step
+    static constexpr int XB = 32 * HS * 2, DB = ET * 4 * FRAG, SB = NW * 256;  // bytes of a step: tokens, operands, scales
+    static constexpr int SLOT = XB + DB + SB, D = D_;
+    static constexpr int TPW = NW == 8 ? (ET + 1) / 2 : ET;  // expert tiles per wave
+    static constexpr int XPW = 16 / NW;                      // instructions of x per wave
+    static constexpr int OPW = (4 * ET + NW - 1) / NW;       // operands moved per wave
+    static constexpr int DMAS = XPW + OPW + 1;               // per wave and step
     static constexpr int LDS = D * SLOT;
 };
-template <int ET>
-__global__ __launch_bounds__(512) void dw_kernel(RouterBackArgs a, Scratch s, int tile0) {
-    using C = DwCfg<ET>;
-    extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
+template <int ET, int NW, int D>
+__device__ __forceinline__ void dw_body(const RouterBackArgs &a, const Scratch &s, int tile0, int block,
+                                        unsigned char *smem) {
+    using C = DwCfg<ET, NW, D>;
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
     const int lr = lane & 31, lh = lane >> 5, r8 = lane >> 3;
     const int cg = wave & 3, t0 = (wave >> 2) * C::TPW;  // this wave's columns, its first tile
     const int total = s.slices * s.splits, per = (total + 7) / 8;
-    const int at = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
-    if ((int)(blockIdx.x >> 3) >= per || at >= total) return;
+    const int at = (block & 7) * per + (block >> 3);
+    if ((block >> 3) >= per || at >= total) return;
     const int split = at / s.slices, slice = at - split * s.slices;
     const int64_t b0 = s.nb * split / s.splits, n = 2 * (s.nb * (split + 1) / s.splits - b0);  // first block, steps
     const unsigned lds = (unsigned)(uintptr_t)smem;
@@ -388,10 +394,10 @@ __global__ __launch_bounds__(512) void dw_kernel(RouterBackArgs a, Scratch s, in
     // vector memory instructions)
     typedef const __attribute__((address_space(4))) uint64_t *Words;
     const Words live = (Words)(uintptr_t)s.live;
-    // x: this wave moves 16 tokens of column group wave / 2, two instructions
-    const int64_t cx = (int64_t)slice * HS + 64 * (wave >> 1);
+    // x: this wave moves 8 XPW tokens of one column group
+    const int64_t cx = (int64_t)slice * HS + 64 * (wave * C::XPW >> 2);
     const _Float16 *xbase = uniform(a.x + (cx < a.H ? cx : a.H - 64));  // idle columns read valid ones
-    const int tx = 16 * (wave & 1) + r8;
+    const int tx = 8 * (wave * C::XPW & 3) + r8;
     const unsigned xstep = (unsigned)(16 * a.H), xoff = (unsigned)(tx * a.H * 2) + 16 * ((lane & 7) ^ swz_k(r8));
     // step i; past the last one the last again, so that every wait counts the
     // same.  The mask of the next step is requested here and used there.
@@ -404,13 +410,13 @@ __global__ __launch_bounds__(512) void dw_kernel(RouterBackArgs a, Scratch s, in
         mask = live[b0 + ((i + 1 < n ? i + 1 : n - 1) >> 1)];
         const _Float16 *src = xbase + (b * BT + 32 * half) * a.H;
         if (on == ~0u) {
-            dma16_sb(src, xoff, d + (2 * wave) * FRAG);
-            dma16_sb(src, xoff + xstep, d + (2 * wave + 1) * FRAG);
+#pragma unroll
+            for (int g = 0; g < C::XPW; ++g) dma16_sb(src, xoff + g * xstep, scalar(d + (wave * C::XPW + g) * FRAG));
         } else {
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {
+            for (int g = 0; g < C::XPW; ++g) {
                 const unsigned char *row = (const unsigned char *)src + xoff + g * xstep;
-                dma16(on >> (tx + 8 * g) & 1 ? row : s.zeros + 16 * (lane & 7), d + (2 * wave + g) * FRAG);
+                dma16(on >> (tx + 8 * g) & 1 ? row : s.zeros + 16 * (lane & 7), scalar(d + (wave * C::XPW + g) * FRAG));
             }
         }
         // the step's operands: tile o / 4, of its 8 the half's 4 (some moved twice)
@@ -418,9 +424,9 @@ __global__ __launch_bounds__(512) void dw_kernel(RouterBackArgs a, Scratch s, in
 #pragma unroll
         for (int g = 0; g < C::OPW; ++g) {
             const int o = (wave * C::OPW + g) % (4 * ET);
-            dma16_sb(uniform(f + ((o >> 2) * 8 + (o & 3)) * FRAG), 16 * lane, d + C::XB + o * FRAG);
+            dma16_sb(uniform(f + ((o >> 2) * 8 + (o & 3)) * FRAG), 16 * lane, scalar(d + C::XB + o * FRAG));
         }
-        dma4(s.sw + b * 32 * s.et + 32 * (tile0 + (wave < ET ? wave : 0)) + lr, d + C::XB + C::DB + wave * 256);
+        dma4(s.sw + b * 32 * s.et + 32 * (tile0 + (wave < ET ? wave : 0)) + lr, scalar(d + C::XB + C::DB + wave * 256));
     };
     f16x sum[C::TPW][2], acc[C::TPW][2];
 #pragma unroll
@@ -433,10 +439,10 @@ __global__ __launch_bounds__(512) void dw_kernel(RouterBackArgs a, Scratch s, in
 #pragma unroll
     for (int i = 0; i < 4; ++i) off[i >> 1][i & 1] = tr_off(lane, i >> 1, i & 1);
     auto step = [&](int64_t i, auto second) __attribute__((always_inline)) {
-        wait_vm<2 * C::DMAS>();              // all but the two steps after this one
+        wait_vm<(D - 2) * C::DMAS>();        // all but the steps after this one
         __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): this wave's reads of the step before
         bar();                               // step i is there; everyone is done with the slot of the one before
-        fill(i + 3);
+        fill(i + D - 1);
         const unsigned char *slot = smem + (i % C::D) * C::SLOT, *xs = slot + cg * 4 * FRAG;
         const unsigned char *ds = slot + C::XB + t0 * 4 * FRAG + lane * 16;
         h8 xa[2][2];
@@ -449,7 +455,7 @@ __global__ __launch_bounds__(512) void dw_kernel(RouterBackArgs a, Scratch s, in
             }
 #pragma unroll
         for (int et = 0; et < C::TPW; ++et) {
-            if (ET % 2 && t0 + et >= ET) continue;  // an odd count's idle tile
+            if (NW == 8 && ET % 2 && t0 + et >= ET) continue;  // an odd count's idle tile
             if constexpr (!second) {
 #pragma unroll
                 for (int ht = 0; ht < 2; ++ht)
@@ -475,7 +481,7 @@ __global__ __launch_bounds__(512) void dw_kernel(RouterBackArgs a, Scratch s, in
     };
     if (n > 0) {
 #pragma unroll
-        for (int i = 0; i < 3; ++i) fill(i);
+        for (int i = 0; i < D - 1; ++i) fill(i);
         for (int64_t i = 0; i < n; i += 2) {
             step(i, std::integral_constant<bool, false>{});
             step(i + 1, std::integral_constant<bool, true>{});
@@ -498,6 +504,30 @@ __global__ __launch_bounds__(512) void dw_kernel(RouterBackArgs a, Scratch s, in
     }
 }
 
+template <int ET>
+__global__ __launch_bounds__(512) void dw_kernel(RouterBackArgs a, Scratch s, int tile0) {
+    extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
+    dw_body<ET, 8, 4>(a, s, tile0, blockIdx.x, smem);
+}
+template <int ET, bool ADD>
+__global__ __launch_bounds__(256) void dx_kernel(RouterBackArgs a, Scratch s, int chunks) {
+    extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
+    dx_body<ET, ADD>(a, s, chunks, blockIdx.x, smem);
+}
+// Both in one launch, up to 4 expert tiles: workgroups 0 .. dws - 1 (a
+// multiple of 8) dW's, the others dx's, all of them at once, two per CU: dW
+// waits for its loads where dx stores.  Against a launch each: 16384 tokens of
+// 7168, 128 experts 217 -> 202 us for the whole pass, 4096 tokens of the same
+// 83 -> 73, 8191 tokens of 2048, 64 experts 39 -> 36, 9 tokens of 256 16 -> 12.
+template <int ET, bool ADD>
+__global__ __launch_bounds__(256) void grads_kernel(RouterBackArgs a, Scratch s, int chunks, int dws) {
+    extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
+    if ((int)blockIdx.x < dws)
+        dw_body<ET, 4, 2>(a, s, 0, blockIdx.x, smem);
+    else
+        dx_body<ET, ADD>(a, s, chunks, blockIdx.x - dws, smem);
+}
+
 // The parts' sum, in order.
 __global__ __launch_bounds__(64) void dw_sum_kernel(const f4 *__restrict__ parts, int splits, int64_t n, f4 *__restrict__ y) {
     for (int64_t i = (int64_t)blockIdx.x * 64 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 64) {
@@ -508,6 +538,12 @@ __global__ __launch_bounds__(64) void dw_sum_kernel(const f4 *__restrict__ parts
     }
 }
 
+// dx: parts of the tiles of tokens, for wgs workgroups in all
+int64_t dx_chunks(const RouterBackArgs &a, const Scratch &s, int64_t wgs) {
+    const int64_t tiles = (a.T + 31) / 32, n = wgs / s.slices;
+    return n > tiles ? tiles : n < 1 ? 1 : n;
+}
+
 template <int ET, bool ADD>
 hipError_t launch_dx(const RouterBackArgs &a, const Scratch &s, hipStream_t st) {
     constexpr int LDS = DxCfg<ET>::LDS;
@@ -515,23 +551,42 @@ hipError_t launch_dx(const RouterBackArgs &a, const Scratch &s, hipStream_t st) 
     static std::atomic<uint64_t> lds_set{0};
     hipError_t e = lds_opt_in_once((const void *)dx_kernel<ET, ADD>, LDS, lds_set);
     if (e != hipSuccess) return e;
-    const int64_t tiles = (a.T + 31) / 32;
-    int64_t chunks = s.slices >= 512 ? 1 : (512 + s.slices - 1) / s.slices;
-    if (chunks > tiles) chunks = tiles;
-    const int64_t total = (s.slices * chunks + 7) / 8 * 8;
+    const int64_t chunks = dx_chunks(a, s, 512 + s.slices - 1), total = (s.slices * chunks + 7) / 8 * 8;
     hipLaunchKernelGGL((dx_kernel<ET, ADD>), dim3((unsigned)total), dim3(256), LDS, st, a, s, (int)chunks);
     return hipGetLastError();
 }
 
 template <int ET>
 hipError_t launch_dw(const RouterBackArgs &a, const Scratch &s, int tile0, hipStream_t st) {
-    constexpr int LDS = DwCfg<ET>::LDS;
+    constexpr int LDS = DwCfg<ET, 8, 4>::LDS;
     static_assert(LDS <= 160 * 1024, "LDS");
     static std::atomic<uint64_t> lds_set{0};
     hipError_t e = lds_opt_in_once((const void *)dw_kernel<ET>, LDS, lds_set);
     if (e != hipSuccess) return e;
     const int total = (s.slices * s.splits + 7) / 8 * 8;
     hipLaunchKernelGGL(dw_kernel<ET>, dim3((unsigned)total), dim3(512), LDS, st, a, s, tile0);
+    return hipGetLastError();
+}
+
+template <int ET, bool ADD>
+hipError_t launch_grads(const RouterBackArgs &a, const Scratch &s, hipStream_t st) {
+    constexpr int LDS = DwCfg<ET, 4, 2>::LDS > DxCfg<ET>::LDS ? DwCfg<ET, 4, 2>::LDS : DxCfg<ET>::LDS;
+    static_assert(LDS <= 80 * 1024, "two workgroups per CU");
+    static std::atomic<uint64_t> lds_set{0};
+    hipError_t e = lds_opt_in_once((const void *)grads_kernel<ET, ADD>, LDS, lds_set);
+    if (e != hipSuccess) return e;
+    // all at once, two per CU
+    const int64_t dws = (s.slices * s.splits + 7) / 8 * 8, chunks = dx_chunks(a, s, 512 - dws), dxs = (s.slices * chunks + 7) / 8 * 8;
+    hipLaunchKernelGGL((grads_kernel<ET, ADD>), dim3((unsigned)(dws + dxs)), dim3(256), LDS, st, a, s, (int)chunks, (int)dws);
+    return hipGetLastError();
+}
+
+hipError_t launch_sum(const RouterBackArgs &a, const Scratch &s, hipStream_t st) {
+    if (s.splits <= 1) return hipSuccess;
+    const int64_t n = a.E * a.H / 4;
+    int64_t g = (n + 63) / 64;
+    if (g > 256 * 32) g = 256 * 32;  // strides beyond
+    hipLaunchKernelGGL(dw_sum_kernel, dim3((unsigned)g), dim3(64), 0, st, (const f4 *)s.parts, s.splits, n, (f4 *)a.dw);
     return hipGetLastError();
 }
 
@@ -549,9 +604,18 @@ hipError_t launch_router_backward(const RouterBackArgs &a, hipStream_t st) {
         hipLaunchKernelGGL(dlogits_kernel, dim3((unsigned)s.nb), dim3(1024), lds, st, a, s);
         e = hipGetLastError();
         if (e != hipSuccess) return e;
+        if (s.et <= GT) {
+#define RMOE_G(N) case N: e = a.add ? launch_grads<N, true>(a, s, st) : launch_grads<N, false>(a, s, st); break;
+            switch (s.et) {
+                RMOE_G(1) RMOE_G(2) RMOE_G(3)
+                default: e = a.add ? launch_grads<GT, true>(a, s, st) : launch_grads<GT, false>(a, s, st);
+            }
+#undef RMOE_G
+            return e != hipSuccess ? e : launch_sum(a, s, st);
+        }
 #define RMOE_X(N) case N: e = a.add ? launch_dx<N, true>(a, s, st) : launch_dx<N, false>(a, s, st); break;
         switch (s.et) {
-            RMOE_X(1) RMOE_X(2) RMOE_X(3) RMOE_X(4) RMOE_X(5) RMOE_X(6) RMOE_X(7) RMOE_X(8)
+            RMOE_X(5) RMOE_X(6) RMOE_X(7) RMOE_X(8)
             default: return hipErrorInvalidValue;
         }
 #undef RMOE_X
@@ -567,14 +631,7 @@ hipError_t launch_router_backward(const RouterBackArgs &a, hipStream_t st) {
         }
         if (e != hipSuccess) return e;
     }
-    if (s.splits > 1) {
-        const int64_t n = a.E * a.H / 4;
-        int64_t g = (n + 63) / 64;
-        if (g > 256 * 32) g = 256 * 32;  // strides beyond
-        hipLaunchKernelGGL(dw_sum_kernel, dim3((unsigned)g), dim3(64), 0, st, (const f4 *)s.parts, s.splits, n, (f4 *)a.dw);
-        return hipGetLastError();
-    }
-    return hipSuccess;
+    return launch_sum(a, s, st);
 }
 
 }  // namespace rmoe

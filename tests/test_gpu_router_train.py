@@ -102,6 +102,26 @@ def test_forward_is_the_serving_router_on_any_values(T, E, k, H):
         assert torch.equal(got[n], again[n]), n
 
 
+@pytest.mark.parametrize("E,H", [(100, 448), (128, 64), (256, 1024), (64, 128)])
+def test_serving_and_training_rows_do_not_depend_on_the_batch(E, H):
+    """A token's ids and scores are the same bits whatever follows it, up to
+    two workgroups of 64 tokens per compute unit: 64 tokens per workgroup from
+    one on are two halves that sum as workgroups of 32 do."""
+    cus = torch.cuda.get_device_properties(0).multi_processor_count
+    T = 128 * cus - 37
+    g = torch.Generator(device="cuda").manual_seed(E)
+    x, w = torch.randn((T, H), generator=g, device="cuda").half(), (torch.randn((E, H), generator=g, device="cuda") / H ** 0.5).half()
+    ids, vals = R.router(x, w, 4)
+    got = R.router_train(x, w, 4)
+    for few in (1, 95, 64 * cus - 1):
+        i, v = R.router(x[:few], w, 4)
+        t = R.router_train(x[:few], w, 4)
+        torch.cuda.synchronize()
+        assert torch.equal(i, ids[:few]) and torch.equal(v, vals[:few])
+        assert torch.equal(t["topk_ids"], i) and torch.equal(t["probs"], got["probs"][:few])
+    assert torch.equal(got["topk_ids"], ids) and torch.equal(got["topk_weights"], vals)
+
+
 def test_forward_of_nothing():
     """No tokens, and no token that counts."""
     w = torch.randn((8, 128), device="cuda").half()
