@@ -4,23 +4,31 @@
 // scores are the softmax probabilities).
 //
 // One workgroup = TOK tokens (64 or 32) x every expert (E padded to a
-// multiple of 32, at most 256).  Tokens and gate rows travel HBM/L2 -> LDS
-// by DMA in K-chunks of 64 (8 rows x 128 bytes per instruction) through a
-// 4-stage ring (one barrier per chunk); v_mfma_f32_32x32x16_f16 with gate
-// rows as A and a 32-token tile as B, fp32 logits.  TOK = 64: 4 waves = 2
-// token halves x 2 interleaved sets of 32-expert tiles; TOK = 32: one token
+// multiple of 32, at most 256), 4 computing waves and one that only requests
+// tokens.  Tokens and gate rows travel HBM/L2 -> LDS by DMA in K-chunks of 64
+// (8 rows x 128 bytes per instruction) through two rings of 4 stages (one
+// barrier per chunk): the fifth wave's requests of x never wait behind the
+// others' gate rows, which arrive sooner.  v_mfma_f32_32x32x16_f16 with gate
+// rows as A and a 32-token tile as B, fp32 logits.  TOK = 64: the 4 waves are
+// 2 token halves x 2 interleaved sets of 32-expert tiles; TOK = 32: one token
 // tile, 4 interleaved sets of expert tiles -- or, with fewer than four
 // expert tiles (E <= 64), the waves also split each chunk's four K-steps
 // (E <= 32: one K-step per wave; E <= 64: two), so that every wave has work
 // and a chunk costs one or two dependent MFMAs instead of four (64 tokens,
 // E = 8, H = 4096: two workgroups of 64 chunks); their partial logits are
-// added in a fixed order.  TOK = 32 gives twice the
-// workgroups, i.e. more memory streams per CU, for batches that would not
-// fill the chip twice over (16384 tokens, H = 7168, E = 128: 197 -> 100 us).
-// The logits go through LDS; 4 lanes per token then take the row maximum,
-// the exponential sum and k rounds of arg-max (equal scores: lower expert
-// index first), combining with lane shuffles.  The gate matrix ([E, H],
-// ~1.8 MB at E = 128, H = 7168) stays in L2; x is read once.
+// added in a fixed order.  TOK = 32 gives twice the workgroups, i.e. more
+// memory streams per CU, for batches that would not fill the chip.
+// The logits go through LDS, rows four banks apart; 4 lanes per token then
+// hold its scores in registers and take the row maximum, the exponential sum
+// and k rounds of arg-max (equal scores: lower expert index first), combining
+// with lane shuffles.  The gate matrix ([E, H], ~1.8 MB at E = 128, H = 7168)
+// stays in L2; x is read once, and HBM bounds large batches: 16384 tokens,
+// H = 7168, E = 128 take 67 us cold (3.5 TB/s), 4096 of them 35.  Small ones
+// are bound by the latency of their H / 64 chunks: 64 tokens, H = 4096, E = 8
+// take 10 us.
+// Measured and not kept: an 8-stage token ring with 3 stages of gate rows, so
+// fewer workgroups per CU (4096 tokens, H = 4096, E = 8: 15.7 against 12.2 us;
+// E = 64 up to 48 against 35; nothing gained elsewhere).
 #include "rmoe_device.h"
 #include "rmoe_internal.h"
 
@@ -28,8 +36,8 @@ namespace rmoe {
 namespace {
 
 constexpr int RT_CK = 64;   // K per chunk
-constexpr int RT_XST = 8;   // LDS ring stages of the tokens: from HBM, 7 chunks ahead
-constexpr int RT_WST = 3;   // and of the gate rows, from the L2
+constexpr int RT_XST = 4;   // LDS ring stages of the tokens: DMA runs 3 chunks ahead
+constexpr int RT_WST = 4;   // and of the gate rows
 
 template <int EP, int TOK>
 struct RouterCfg {
