@@ -37,7 +37,7 @@ __device__ __forceinline__ I8Row i8_row(float amax) {
 // the nearest integer n unless it lies that close to a border between two; a
 // fused add of 1.5 2^23 rounds it (half a unit in the last place there is one
 // half) and leaves n's low byte in the sum's.  Where |q - n| comes near one
-// half (one element in 10^4, one wave in 20 here), the remainder x - n s
+// half (one element in 5000, one wave's 512 in 10), the remainder x - n s
 // decides: the fused product is exact there (a multiple of the last place of s
 // or of x below s) and is compared with s / 2.
 constexpr float kI8Magic = 0x1.8p23f;

@@ -4,7 +4,7 @@
 // read once, held in registers while its largest magnitude is found, and its
 // codes are written once.
 //
-// A row is taken by W waves (1 or 4); a lane holds NV vectors of 8 elements
+// A row is taken by W waves (1, 4 or 16); a lane holds NV vectors of 8 elements
 // (16 bytes of fp16 and bf16, 32 of fp32), all loaded before the first is
 // used.  Rows longer than 64 W NV vectors are read twice, the second time
 // from the caches.
@@ -188,13 +188,13 @@ __global__ __launch_bounds__(256) void pack_kernel(const _Float16 *__restrict__ 
 
 // Hidden rows: the valid rows of every block, fp32 in, codes and scales out.
 template <int W, int NV>
-__global__ __launch_bounds__(256) void hidden_kernel(const float *__restrict__ rows, const int32_t *__restrict__ gs,
-                                                     const int32_t *__restrict__ gpo, const int32_t *__restrict__ gidx,
-                                                     int32_t E, int64_t vpr, unsigned char *__restrict__ codes,
-                                                     float *__restrict__ scales) {
-    __shared__ float part[4];
+__global__ __launch_bounds__(W == 16 ? 1024 : 256) void hidden_kernel(
+    const float *__restrict__ rows, const int32_t *__restrict__ gs, const int32_t *__restrict__ gpo,
+    const int32_t *__restrict__ gidx, int32_t E, int64_t vpr, unsigned char *__restrict__ codes,
+    float *__restrict__ scales) {
+    __shared__ float part[W];
     const BlockInfo bi = block_info(gs, gpo, gidx, E, blockIdx.y);
-    constexpr int RPW = 4 / W;
+    constexpr int RPW = W == 1 ? 4 : 1;
     for (int i0 = blockIdx.x * RPW; i0 < bi.rows; i0 += gridDim.x * RPW) {
         const int i = i0 + (W == 1 ? threadIdx.x >> 6 : 0);
         if (W == 1 && i >= bi.rows) continue;
@@ -280,14 +280,16 @@ hipError_t launch_pack_i8(const _Float16 *x, const float *topk_w, const int32_t 
 
 hipError_t launch_quantize_hidden_i8(const I8Args &a, int64_t pairs, hipStream_t s) {
     const int64_t vpr = a.N / 8;
-    const int w = waves(pairs, vpr), nv = vectors(vpr, w);
-    const dim3 grid(w == 1 ? kBlockM / 4 : kBlockM, (unsigned)a.M), wg(256);
+    // few long rows: 16 waves each, as one row's latency is the launch's (128 rows of 14336: 8.5 -> 5.6 us)
+    const int w = pairs <= 1024 && vpr > 256 ? 16 : waves(pairs, vpr), nv = vectors(vpr, w);
+    const dim3 grid(32, (unsigned)a.M), wg(w == 16 ? 1024 : 256);
 #define RMOE_H(W, NV)                                                                                          \
     if (w == W && nv == NV) {                                                                                  \
         hipLaunchKernelGGL((hidden_kernel<W, NV>), grid, wg, 0, s, a.rows, a.gs, a.gpo, a.gidx, a.E, vpr,      \
                            a.yc, a.ys);                                                                        \
         return hipGetLastError();                                                                              \
     }
+    RMOE_H(16, 1) RMOE_H(16, 2) RMOE_H(16, 4) RMOE_H(16, 8)
     RMOE_H(1, 1) RMOE_H(1, 2) RMOE_H(1, 4) RMOE_H(4, 1) RMOE_H(4, 2) RMOE_H(4, 4) RMOE_H(4, 8)
 #undef RMOE_H
     return hipErrorInvalidValue;

@@ -264,6 +264,18 @@ def test_stages(counts, H, I, variant):
     _check(d)
 
 
+@pytest.mark.parametrize("counts,I", [([3, 0, 40], 2048), ([3, 0, 40], 2176), ([3, 0, 40], 8320), ([3, 0, 40], 24576),
+                                      ([1, 33], 33024), ([1024], 2176), ([5, 1020], 2176)])
+def test_few_and_many_long_hidden_rows(counts, I):
+    """Hidden rows shared by 4 and by 16 waves, of one to eight vectors a lane and of more."""
+    print(f"[int8] counts={counts} I={I}", flush=True)
+    d = _case(counts, 128, I, seed=I)
+    _gate_up(d, "auto")
+    _down(d, "auto")
+    torch.cuda.synchronize()
+    _check(d)
+
+
 @pytest.mark.parametrize("H,I", [(133120, 128), (128, 133120)])
 @pytest.mark.parametrize("variant", ["stream", "tile"])
 def test_maximum_hidden_and_intermediate(H, I, variant):
