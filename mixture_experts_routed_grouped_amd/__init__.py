@@ -519,7 +519,8 @@ def _mask(dev, token_mask, T):
     if token_mask is None:
         return None
     torch = _torch()
-    return _arg(dev, "token_mask", token_mask, torch.bool if token_mask.dtype is torch.bool else torch.uint8, T)
+    dtype = torch.bool if getattr(token_mask, "dtype", None) is torch.bool else torch.uint8
+    return _arg(dev, "token_mask", token_mask, dtype, T)
 
 
 def router_backward_scratch_bytes(num_tokens: int, hidden: int, num_experts: int) -> int:

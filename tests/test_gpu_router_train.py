@@ -368,6 +368,15 @@ def test_binding_refusals():
                 R.router_backward(**{**good, name: bad})
 
 
+def test_mask_types():
+    T, E, k, H = 20, 8, 2, 128
+    _, _, _, xg, wg, mg = _inputs(T, E, H, 2, 0.3)
+    a, b = R.router_train(xg, wg, k, token_mask=mg), R.router_train(xg, wg, k, token_mask=mg.bool())
+    assert all(torch.equal(a[n], b[n]) for n in ("topk_ids", "topk_weights", "probs", "lse", "counts", "losses"))
+    with pytest.raises(TypeError):
+        R.router_train(xg, wg, k, token_mask=mg.tolist())
+
+
 def test_training_step_of_a_whole_layer():
     """Router, contract, pack, expert FFN, combine, and all of it backwards, as
     a program runs them, with padding tokens: the gradients of the tokens, the
