@@ -23,7 +23,7 @@
 // and k rounds of arg-max (equal scores: lower expert index first), combining
 // with lane shuffles.  The gate matrix ([E, H], ~1.8 MB at E = 128, H = 7168)
 // stays in L2; x is read once, and HBM bounds large batches: 16384 tokens,
-// H = 7168, E = 128 take 67 us cold (3.5 TB/s), 4096 of them 35.  Small ones
+// H = 7168, E = 128 take 67 us cold (3.5 TB/s), 4096 of them 33.  Small ones
 // are bound by the latency of their H / 64 chunks: 64 tokens, H = 4096, E = 8
 // take 10 us.
 // Measured and not kept: an 8-stage token ring with 3 stages of gate rows, so
@@ -51,6 +51,12 @@ struct RouterCfg {
     static constexpr int TPW = (NT + EW - 1) / EW;  // tiles per wave
     // waves per expert tile that split a chunk's 4 K-steps (TOK = 32 only)
     static constexpr int KSW = TOK == 32 && NT == 1 ? 4 : TOK == 32 && NT == 2 ? 2 : 1;
+    // Two sets of operands: a chunk's MFMAs run while the next one's operands
+    // come from LDS (64 tokens, H = 7168, E = 128: 33 -> 28 us; 8192 of 4096,
+    // E = 96: 22 -> 19).  With 64 tokens the registers cost more than that
+    // (16384 of 7168, E = 128: 68 -> 73 us; 20000 of 2048, E = 256: 71 -> 339,
+    // spilled), and where the waves split the K-steps nothing changes.
+    static constexpr bool TWO = TOK == 32 && KSW == 1;
     static constexpr int LD = EP + 4;             // words per row of logits
     static constexpr int LDS_BYTES = W_OFF + RT_WST * WSTAGE;  // >= the TROWS x LD fp32 logits
     static_assert(TOK == 64 || TOK == 32, "tokens per workgroup: whole 32-token tiles");
@@ -152,35 +158,60 @@ __device__ __forceinline__ void router_body(const _Float16 *__restrict__ x, cons
 
 #pragma unroll
     for (int p = 0; p < RT_WST - 1; ++p) dma(p);
-    for (int kc = 0; kc < sweep; ++kc) {
+    constexpr int NS = 4 / C::KSW;  // K-steps of this wave: s = KSW i + ks
+    struct Ops {
+        h8 b[NS], a[C::TPW][NS];
+    } ops[C::TWO ? 2 : 1];
+    auto mul = [&](const Ops &o) {
+#pragma unroll
+        for (int i = 0; i < NS; ++i)
+#pragma unroll
+            for (int t = 0; t < C::TPW; ++t)
+                acc[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(o.a[t][i], o.b[i], acc[t], 0, 0, 0);
+    };
+    // requests the operands of chunk kc and multiplies those of `ready`
+    auto step = [&](int kc, Ops &o, const Ops &ready) {
         wait_vm<(RT_WST - 2) * C::NIW>();    // chunk kc landed (own DMAs) ...
         __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): this wave's reads of chunk kc-1
         bar();  // ... and everyone's; and every wave is done with chunk kc-1's stages
         if (lag && (th ? kc < lag : kc >= nk)) {  // the other half's part of the sweep
             dma(kc + RT_WST - 1);
-            continue;
+            return;
         }
         // the wave's operands of the chunk, all requested before the first MFMA
         const unsigned char *bx = smem + (kc % RT_XST) * C::XSTAGE;
         const unsigned char *bw = smem + C::W_OFF + (kc % RT_WST) * C::WSTAGE;
-        constexpr int NS = 4 / C::KSW;  // K-steps of this wave: s = KSW i + ks
-        h8 b[NS], a[C::TPW][NS];
 #pragma unroll
         for (int i = 0; i < NS; ++i) {
             const int ch = 2 * (C::KSW * i + ks) + lh;
-            b[i] = *(const h8 *)(bx + lds_off(32 * th + lr, ch));
+            o.b[i] = *(const h8 *)(bx + lds_off(32 * th + lr, ch));
 #pragma unroll
             for (int t = 0; t < C::TPW; ++t) {
                 // an idle last tile reads the tile before it
                 const int et = whole || eh + C::EW * t < C::NT ? eh + C::EW * t : C::NT - 1;
-                a[t][i] = *(const h8 *)(bw + lds_off(32 * et + lr, ch));
+                o.a[t][i] = *(const h8 *)(bw + lds_off(32 * et + lr, ch));
             }
         }
+        if constexpr (C::TWO) __builtin_amdgcn_sched_barrier(0);
         dma(kc + RT_WST - 1);
+        mul(ready);
+    };
+    if constexpr (C::TWO) {
 #pragma unroll
-        for (int i = 0; i < NS; ++i)
+        for (int i = 0; i < NS; ++i) {  // before the first chunk: adds zeros
+            ops[1].b[i] = h8{};
 #pragma unroll
-            for (int t = 0; t < C::TPW; ++t) acc[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a[t][i], b[i], acc[t], 0, 0, 0);
+            for (int t = 0; t < C::TPW; ++t) ops[1].a[t][i] = h8{};
+        }
+        int kc = 0;
+        for (; kc + 1 < sweep; kc += 2) {
+            step(kc, ops[0], ops[1]);
+            step(kc + 1, ops[1], ops[0]);
+        }
+        if (kc < sweep) step(kc, ops[0], ops[1]);
+        mul(kc < sweep ? ops[0] : ops[1]);
+    } else {
+        for (int kc = 0; kc < sweep; ++kc) step(kc, ops[0], ops[0]);
     }
     wait_vm<0>();
     bar();
