@@ -466,7 +466,8 @@ RMOE_API int rmoe_router_train_f16(const void *x, const void *router_w, const ui
  *   dx = fp16( dl . router_w + dx_add )         [num_tokens, hidden]
  *   drouter_w[e] = sum_t dl[t, e] x[t]          [E, hidden] fp32
  * dx_add [num_tokens, hidden] fp16 or NULL: the gradient that reached the
- * tokens through the experts (rmoe_combine_f16); it may be dx itself.  dl is
+ * tokens through the experts (rmoe_combine_f16); it may be dx itself, else dx
+ * and drouter_w overlap no other argument.  dl is
  * fp32; for the products it is split into two fp16 values (22 bits).  Every
  * row of dx is written; rows of x that are left out are not read.
  * scratch: rmoe_router_backward_scratch_bytes(num_tokens, hidden, E) bytes,

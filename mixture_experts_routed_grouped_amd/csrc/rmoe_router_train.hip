@@ -106,9 +106,9 @@ __global__ __launch_bounds__(1024) void dlogits_kernel(RouterBackArgs a, Scratch
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
     const int EP = 32 * s.et, ld = EP + 4;  // row stride: 16 tokens x 4 lanes on 64 banks
     float *L = reinterpret_cast<float *>(smem);            // [64][ld] dl
-    float *pg = L + BT * ld;                               // [64 k] a routed weight's gradient times its probability
+    float *pg = L + BT * ld;                               // [64 k] a routed weight's gradient
     int *pid = reinterpret_cast<int *>(pg + BT * a.k);     // [64 k] its expert, -1: none
-    __shared__ float red[4][BT], up_x[BT], up_w[256];
+    __shared__ float red[4][BT], big[4][BT], up_x[BT], up_w[256];
     __shared__ uint16_t on[4];
     const int tid = threadIdx.x, sub = tid & 3, tok = (tid >> 2) & 63, part = tid >> 8;
     const int64_t b = blockIdx.x, t0 = b * BT, t = t0 + tok;
@@ -129,20 +129,12 @@ __global__ __launch_bounds__(1024) void dlogits_kernel(RouterBackArgs a, Scratch
         const int tk = i / a.k, id = a.ids[t0 * a.k + i];
         const bool use = id >= 0 && id < a.E && (a.mask == nullptr || a.mask[t0 + tk] != 0);
         const int64_t q = a.cpos ? (int64_t)a.cpos[t0 * a.k + i] : t0 * a.k + i;
-        const float g = use && q >= 0 && q < a.T * a.k ? a.drw[q] : 0.f;
-        pg[i] = use ? g * a.probs[(t0 + tk) * a.E + id] : 0.f;
+        pg[i] = use && q >= 0 && q < a.T * a.k ? a.drw[q] : 0.f;
         pid[i] = use ? id : -1;
     }
-    float dot = 0.f;
-    float dv[16];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        dv[i] = i < ne && e0 + 4 * i < a.E ? pv[i] * (ca * (float)a.counts[e0 + 4 * i]) : 0.f;
-        dot += dv[i];
-    }
-    dot += __shfl_xor(dot, 1);
-    dot += __shfl_xor(dot, 2);
-    if (sub == 0) red[part][tok] = dot;
+    for (int i = 0; i < 16; ++i)
+        if (i < ne) row[e0 + 4 * i] = e0 + 4 * i < a.E ? ca * (float)a.counts[e0 + 4 * i] : 0.f;
     if (tid < 256) {  // 16 tokens per wave, 4 equal bits each
         const uint64_t bits = __ballot(live);
         if ((tid & 63) == 0) {
@@ -155,28 +147,39 @@ __global__ __launch_bounds__(1024) void dlogits_kernel(RouterBackArgs a, Scratch
     if (tid == 0)
         s.live[b] = (uint64_t)on[0] | (uint64_t)on[1] << 16 | (uint64_t)on[2] << 32 | (uint64_t)on[3] << 48;
     if (b == 0 && tid < 8) ((h8 *)s.zeros)[tid] = h8{0, 0, 0, 0, 0, 0, 0, 0};
-    dot = (red[0][tok] + red[1][tok]) + (red[2][tok] + red[3][tok]);
-    if (live)
-        for (int j = 0; j < a.k; ++j) dot += pg[tok * a.k + j];
-    const float z = live ? cz * a.lse[t] - dot : 0.f;
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-        if (i < ne) row[e0 + 4 * i] = dv[i] + pv[i] * z;
-    __syncthreads();
     if (live && tid < 256 && sub == 0)
         for (int j = 0; j < a.k; ++j) {
             const int id = pid[tok * a.k + j];
             if (id >= 0) row[id] += pg[tok * a.k + j];
         }
     __syncthreads();
-    // scales: of a token, over its lanes and parts; of an expert
+    // dl from dp - sum p dp: what is large in both cancels before the rest is
+    // added (exactly where one expert has all the probability)
+    float dv[16], dot = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        dv[i] = i < ne ? row[e0 + 4 * i] : 0.f;
+        dot += pv[i] * dv[i];
+    }
+    dot += __shfl_xor(dot, 1);
+    dot += __shfl_xor(dot, 2);
+    if (sub == 0) red[part][tok] = dot;
+    __syncthreads();
+    dot = (red[0][tok] + red[1][tok]) + (red[2][tok] + red[3][tok]);
+    const float z = live ? cz * a.lse[t] : 0.f;
+    // and the scales: of a token, over its lanes and parts; of an expert
     float m = 0.f;
 #pragma unroll
     for (int i = 0; i < 16; ++i)
-        if (i < ne) m = __builtin_elementwise_maximum(m, __builtin_fabsf(row[e0 + 4 * i]));
+        if (i < ne) {
+            const float dl = live && e0 + 4 * i < a.E ? pv[i] * ((dv[i] - dot) + z) : 0.f;
+            row[e0 + 4 * i] = dl;
+            m = __builtin_elementwise_maximum(m, __builtin_fabsf(dl));
+        }
     m = __builtin_elementwise_maximum(m, __shfl_xor(m, 1));
     m = __builtin_elementwise_maximum(m, __shfl_xor(m, 2));
-    if (sub == 0) red[part][tok] = m;
+    if (sub == 0) big[part][tok] = m;
+    __syncthreads();
     if (tid < EP) {
         float w = 0.f;
 #pragma unroll 16
@@ -184,15 +187,14 @@ __global__ __launch_bounds__(1024) void dlogits_kernel(RouterBackArgs a, Scratch
         const Scale c = scale_of(w);
         up_w[tid] = c.up;
         s.sw[b * EP + tid] = c.down;
-    }
-    __syncthreads();
-    if (tid < BT) {
-        m = red[0][tid];
+    } else if (tid >= 1024 - BT) {
+        const int tk = tid - (1024 - BT);
+        m = big[0][tk];
 #pragma unroll
-        for (int i = 1; i < 4; ++i) m = __builtin_elementwise_maximum(m, red[i][tid]);
+        for (int i = 1; i < 4; ++i) m = __builtin_elementwise_maximum(m, big[i][tk]);
         const Scale c = scale_of(m);
-        up_x[tid] = c.up;
-        s.sx[t0 + tid] = c.down;
+        up_x[tk] = c.up;
+        s.sx[t0 + tk] = c.down;
     }
     __syncthreads();
     // operands of dx: lane = token % 32 + 32 (octet of experts % 2)

@@ -270,6 +270,27 @@ def test_backward_of_ids_twice_and_out_of_range():
     _check_backward(dx, dw, f, x, w, None, g, (3.0, 1.0))
 
 
+@pytest.mark.parametrize("E", [1, 40])
+def test_backward_where_one_expert_has_all_the_probability(E):
+    """p = 1: the routed weights' gradients cancel exactly, however large, and
+    leave the z loss's, with the roundings of its own products only (a fp32
+    constant, lse, p, n: 4; two fp16 parts 2^-22; the sums of dW)."""
+    T, H = 130, 128
+    x, w, _, xg, wg, _ = _inputs(T, E, H, 9)
+    f = RB.forward(x, w, 1)
+    f["ids"][:] = E - 1
+    f["probs"][:] = 0
+    f["probs"][:, E - 1] = 1
+    g = np.random.default_rng(3).standard_normal((T, 1)) * 1e4
+    dx, dw = _backward(f, xg, wg, None, g, (0.0, 0.01))
+    dl = np.zeros((T, E))
+    dl[:, E - 1] = 2 * 0.01 * f["lse"].astype(np.float32).astype(np.float64) / T
+    top = np.abs(dl).max()
+    size = np.abs(dl).T @ np.abs(x)
+    assert (np.abs(_np(dw) - dl.T @ x) <= size * (6 * U + 2.0 ** -22 + 431 * 2.0 ** -23) + T * top * 2.0 ** -36).all()
+    assert (np.abs(_np(dx) - dl @ w) <= (np.abs(dl) @ np.abs(w)) * (2.0 ** -10) + 2.0 ** -24).all()
+
+
 def test_backward_counts_may_come_from_elsewhere():
     """Counts summed over several ranks: constants of the loss."""
     x, w, mask, xg, wg, mg = _inputs(90, 12, 192, 8, 0.1)
