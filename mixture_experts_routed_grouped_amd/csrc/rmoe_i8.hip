@@ -160,25 +160,30 @@ __global__ __launch_bounds__(256) void dequantize_kernel(const unsigned char *__
     }
 }
 
-// A token's row is read and quantised once, by one workgroup, and its codes
-// and scale are written to its k padded rows.  Pairs whose table entry is out
-// of range move nothing.
-template <int NV>
+// A token's row is read and quantised once, by W waves, and its codes and
+// scale are written to its k padded rows.  Pairs whose table entry is out of
+// range move nothing.  The first 64 entries are read beside the row.
+template <int W, int NV>
 __global__ __launch_bounds__(256) void pack_kernel(const _Float16 *__restrict__ x, const float *__restrict__ topk_w,
                                                    const int32_t *__restrict__ prow, const int32_t *__restrict__ cpos,
                                                    int64_t T, int32_t k, int64_t vpr, int64_t Tp,
                                                    unsigned char *__restrict__ codes, float *__restrict__ scales,
                                                    float *__restrict__ w_compact) {
     __shared__ float part[4];
+    constexpr int TPG = 4 / W;  // tokens per workgroup
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t pairs = T * k;
-    for (int64_t t = blockIdx.x; t < T; t += gridDim.x) {
-        const float s = quantize_row<_Float16, 4, NV>(x + t * vpr * 8, vpr, part, [&](int64_t v, u2 c) {
+    for (int64_t t0 = (int64_t)blockIdx.x * TPG; t0 < T; t0 += (int64_t)gridDim.x * TPG) {
+        const int64_t t = t0 + (W == 1 ? wave : 0);
+        if (W == 1 && t >= T) continue;
+        const int first = lane < k ? prow[t * k + lane] : -1;
+        const float s = quantize_row<_Float16, W, NV>(x + t * vpr * 8, vpr, part, [&](int64_t v, u2 c) {
             for (int j = 0; j < k; ++j) {
-                const int64_t r = prow[t * k + j];
+                const int64_t r = j < 64 ? __builtin_amdgcn_readlane(first, j) : prow[t * k + j];
                 if (r >= 0 && r < Tp) ((u2 *)codes)[r * vpr + v] = c;
             }
         });
-        for (int j = threadIdx.x; j < k; j += 256) {
+        for (int j = W == 1 ? lane : threadIdx.x; j < k; j += 64 * W) {
             const int64_t p = t * k + j, q = cpos[p], r = prow[p];
             if (q >= 0 && q < pairs) w_compact[q] = topk_w[p];
             if (r >= 0 && r < Tp) scales[r] = s;
@@ -265,17 +270,17 @@ hipError_t launch_pack_i8(const _Float16 *x, const float *topk_w, const int32_t 
                           int32_t k, int64_t H, int64_t Tp, unsigned char *codes, float *scales, float *w_compact,
                           hipStream_t s) {
     const int64_t vpr = H / 8;
-    const dim3 grid(grid_of(T)), wg(256);
-#define RMOE_P(NV)                                                                                                \
-    case NV:                                                                                                      \
-        hipLaunchKernelGGL(pack_kernel<NV>, grid, wg, 0, s, x, topk_w, prow, cpos, T, k, vpr, Tp, codes, scales,  \
-                           w_compact);                                                                            \
-        break;
-    switch (vectors(vpr, 4)) {
-        RMOE_P(1) RMOE_P(2) RMOE_P(4) RMOE_P(8)
+    const int w = waves(T, vpr), nv = vectors(vpr, w);
+    const dim3 grid(grid_of(w == 1 ? (T + 3) / 4 : T)), wg(256);
+#define RMOE_P(W, NV)                                                                                            \
+    if (w == W && nv == NV) {                                                                                    \
+        hipLaunchKernelGGL((pack_kernel<W, NV>), grid, wg, 0, s, x, topk_w, prow, cpos, T, k, vpr, Tp, codes,    \
+                           scales, w_compact);                                                                   \
+        return hipGetLastError();                                                                                \
     }
+    RMOE_P(1, 1) RMOE_P(1, 2) RMOE_P(1, 4) RMOE_P(4, 1) RMOE_P(4, 2) RMOE_P(4, 4) RMOE_P(4, 8)
 #undef RMOE_P
-    return hipGetLastError();
+    return hipErrorInvalidValue;
 }
 
 hipError_t launch_quantize_hidden_i8(const I8Args &a, int64_t pairs, hipStream_t s) {
