@@ -7,7 +7,14 @@
 // A row is taken by W waves (1, 4 or 16); a lane holds NV vectors of 8 elements
 // (16 bytes of fp16 and bf16, 32 of fp32), all loaded before the first is
 // used.  Rows longer than 64 W NV vectors are read twice, the second time
-// from the caches.
+// from the caches.  One wave per row needs no barrier and is taken once there
+// are several rows per CU; more waves shorten the one row that a small call
+// waits for.
+//
+// 8 x 14336 x 4096 bf16: 257 us there (5.5 TB/s), 229 back (6.2); 49152 hidden
+// rows of 1408 fp32 60 us (5.8 TB/s); the pack of 8192 tokens of 2048 to 6 rows
+// each 34 us.  Calls of some hundred rows take 3 to 7 us, a launch's latency
+// and one trip to memory.
 #include <type_traits>
 
 #include "rmoe_i8.h"

@@ -8,6 +8,11 @@
 // barriers, and operands travel by DMA into per-wave rings: 32 weight rows x
 // 128 bytes per tile and chunk, and the pass's token rows.  The partial sums
 // are integers, so their order does not matter; scales enter at the end.
+//
+// 64 tokens, 2 of 8 experts, 4096 x 14336: gate/up 160 us for 940 MB of
+// weights, down 76 us for 470 (5.9 and 6.2 TB/s; a contiguous read-only sweep
+// reaches 7.07).  One wave per workgroup with two ring slots where that gives
+// enough workgroups: the more independent sweeps, the fuller the channels.
 #include <atomic>
 
 #include "rmoe_i8.h"
