@@ -647,11 +647,12 @@ RMOE_API int rmoe_pack_int8_f16(const void *x, const float *topk_weights, const 
  * rmoe_forward_f16_variant; H and I at most 133120, so that the sums fit
  * (RMOE_ERR_UNSUPPORTED_SHAPE).  workspace: rmoe_int8_workspace_bytes(Tp, I)
  * bytes: the hidden rows' codes [Tp, I], the rows in fp32 [Tp, I], their
- * scales [Tp]; contents irrelevant on entry.  Only valid rows of out and of
- * the workspace are written.  variant: RMOE_VARIANT_STREAM or _TILE (equal
+ * scales [Tp]; contents irrelevant on entry.  Only valid rows of out, the codes
+ * and the scales are written; the fp32 rows' space is scratch.  variant: RMOE_VARIANT_STREAM or _TILE (equal
  * results, bit for bit), or _AUTO for the choice of rmoe_pick_variant_int8.
  * Codes, the weights' scales, workspace and out 16-byte aligned, the rest 4.
- * Three launches on `stream`.
+ * At most four launches on `stream` (with few experts and rows the down
+ * product is cut into parts along I, which a launch of its own adds up).
  */
 RMOE_API size_t rmoe_int8_workspace_bytes(int64_t total_padded_tokens, int64_t intermediate);
 RMOE_API int rmoe_pick_variant_int8(int32_t variant, int64_t num_pairs, int32_t num_experts);

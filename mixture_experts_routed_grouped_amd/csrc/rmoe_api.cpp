@@ -856,16 +856,23 @@ int check_i8_sizes(int32_t type, int64_t rows, int64_t cols, bool *empty) {
 
 // Streaming reads an expert's weights once per 64 rows of each of its blocks.
 // Forward times of both families (one MI355X, the tiled one's over the
-// streaming one's; equal groups, then Zipf 1.2): E=1 (4096, 14336) 1.74 at 64
-// rows per expert, 1.23 at 128; E=2 1.90 and 1.03; E=8 (4096, 14336) 1.22 and
-// 0.91 at 48, 1.17 and 0.77 at 64; E=8 (2048, 5632) 1.48 and 1.19, 1.34 and
-// 1.03; E=16 (4096, 14336) 1.04 and 0.88 at 32, 0.98 and 0.81 at 40; E=32
-// (4096, 2048) 1.23 and 1.34 at 40, 1.17 and 1.05 at 64; E=64 (2048, 1408)
-// 1.10 and 1.12, 1.09 and 1.04; E=128 (7168, 2048) 1.00 and 0.97, 0.96 and
-// 0.81.
+// streaming one's).  Equal groups of 64 and 96 rows: E=1 (4096, 14336) 1.06 and
+// 0.69, (1024, 4096) 1.30 and 1.17, (7168, 2048) 1.91 and 1.36; E=2 (4096,
+// 14336) 1.22 and 0.72, (2048, 8192) 1.07 and 0.75, (7168, 2048) 1.80 and 1.23;
+// E=4 (4096, 14336) 1.22 and 0.70, (1024, 4096) 1.13 and 0.87, (4096, 2048)
+// 1.61 and 1.13; E=8 (4096, 14336) 1.04 and 0.60.  Equal groups, then Zipf 1.2:
+// E=8 (4096, 14336) 1.22 and 0.91 at 48 rows; E=8 (2048, 5632) 1.48 and 1.19,
+// 1.34 and 1.03 at 64; E=16 (4096, 14336) 1.04 and 0.88 at 32, 0.98 and 0.81 at
+// 40; E=32 (4096, 2048) 1.23 and 1.34 at 40, 1.17 and 1.05 at 64; E=64 (2048,
+// 1408) 1.10 and 1.12, 1.09 and 1.04; E=128 (7168, 2048) 1.00 and 0.97, 0.96
+// and 0.81.
 int pick_variant_i8(int32_t variant, int64_t pairs, int32_t num_experts) {
     if (variant == RMOE_VARIANT_STREAM || variant == RMOE_VARIANT_TILE) return variant;
-    const int64_t rows = num_experts <= 4 ? 128 : num_experts <= 8 ? 56 : num_experts < 32 ? 32 : 40;
+    const int64_t rows = num_experts == 1   ? 128
+                         : num_experts <= 4 ? 64
+                         : num_experts <= 8 ? 56
+                         : num_experts < 32 ? 32
+                                            : 40;
     return pairs <= rows * num_experts ? RMOE_VARIANT_STREAM : RMOE_VARIANT_TILE;
 }
 
@@ -883,7 +890,7 @@ int i8_down_impl(const rmoe::I8Args &a, int32_t variant, int64_t pairs, void *st
     hipStream_t s = static_cast<hipStream_t>(stream);
     if (pick_variant_i8(variant, pairs, a.E) == RMOE_VARIANT_STREAM)
         return to_status(rmoe::launch_i8_stream_down(a, pairs, s));
-    return to_status(rmoe::launch_i8_tile_down(a, s));
+    return to_status(rmoe::launch_i8_tile_down(a, pairs, s));
 }
 
 int check_i8_dims(int64_t hidden, int64_t intermediate, int32_t E, int64_t Tp, int64_t pairs, int32_t M,
@@ -1028,6 +1035,9 @@ int rmoe_forward_int8(const void *xc, const float *xs, const void *gc, const flo
     st = i8_down_args(&dn, hc, hs, dc, ds, rw, gs, go, gpo, gidx, out, hidden, intermediate, num_experts,
                       total_valid_tokens, num_blocks_m);
     if (st != RMOE_OK) return st;
+    // the rows' room is free again once they are quantised
+    dn.part = reinterpret_cast<int32_t *>(rows);
+    dn.Tp = total_padded_tokens;
     st = i8_gate_up_impl(gu, variant, total_valid_tokens, stream);
     return st != RMOE_OK ? st : i8_down_impl(dn, variant, total_valid_tokens, stream);
 }

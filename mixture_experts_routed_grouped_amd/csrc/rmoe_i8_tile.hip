@@ -88,15 +88,23 @@ struct I8Ops {
     __device__ __forceinline__ void publish(int) {}
 };
 
-__device__ __forceinline__ float sum_of(float c) { return (float)__builtin_bit_cast(int, c); }
+// (by value: the cast of a vector's element takes its first one)
+__device__ __forceinline__ int bits_of(float c) { return __builtin_bit_cast(int, c); }
+__device__ __forceinline__ float sum_of(float c) { return (float)bits_of(c); }
+
+// The down product whole, or a part of its K per item: out rows' sums, which
+// another launch adds up (exact integers: the same results).
+enum Stage { GATE_UP, DOWN, DOWN_PART };
 
 // What a lane and a wave hold for the whole launch, and the item's bases.
-template <bool DUAL>
+template <int STAGE>
 struct Tile {
+    static constexpr bool DUAL = STAGE == GATE_UP, PART = STAGE == DOWN_PART;
     const I8Args &a;
     unsigned char *smem;
     int wave, lane, ww, wt;  // ww: weight half, wt: token half (= block bx + wt)
     int64_t N, K;
+    int cols;  // parts: column tiles, an item's slice being part * cols + column tile
     I8Ops p;
     // The scales of the item whose products run: of the wave's 128 weight rows
     // (gate/up: 64 gate, 64 up rows) and of its 128 tokens (down: times the
@@ -112,6 +120,7 @@ struct Tile {
         wt = wave >> 1;
         N = a.N;
         K = a.K;
+        cols = PART ? (int)((N + 255) / 256) : 0;
         p.smem = smem;
         p.nk = (int)(K / BK);
         p.lane = lane;
@@ -128,14 +137,25 @@ struct Tile {
         }
         p.dwave = (unsigned)(uintptr_t)smem + 64 * wave * BK;
     }
+    __device__ __forceinline__ int part(const TileItem &it) const { return PART ? it.nt / cols : 0; }
+    __device__ __forceinline__ int64_t first(const TileItem &it) const {  // its first column
+        return (int64_t)(PART ? it.nt % cols : it.nt) * (DUAL ? 128 : 256);
+    }
     __device__ __forceinline__ void set(const TileItem &it) {
-        const int64_t n0 = (int64_t)it.nt * (DUAL ? 128 : 256);
+        const int64_t n0 = first(it);
         // weight rows 64 w .. of the slot: gate rows for waves 0, 1, up rows for 2, 3
         int64_t wrow0 = n0 + (DUAL ? (64 * wave) & 127 : 64 * wave);
         wrow0 = wrow0 < N ? wrow0 : N - 64;  // a narrow last slice: idle rows read valid rows
         p.wbase = uniform((DUAL && wave >= 2 ? a.w1 : a.w0) + ((int64_t)it.e * N + wrow0) * K);
         // an absent second block: its half reads the first block's rows
         p.tbase = uniform(a.x + ((int64_t)it.bx * kBlockM + (it.rows1 > 0 ? 64 * wave : (64 * wave) & 127)) * K);
+        if constexpr (PART) {
+            const int nk = (int)(K / BK), k0 = nk * part(it) / a.splits;
+            p.nk = nk * (part(it) + 1) / a.splits - k0;
+            p.wbase += k0 * BK;
+            p.tbase += k0 * BK;
+            return;
+        }
         // an idle wave (a narrow last slice, an absent second block) reads valid ones
         const int64_t c0 = n0 + (DUAL ? 64 : 128) * ww, f = (int64_t)it.e * N + (c0 < N ? c0 : N - 128) + lane;
         const int64_t row = ((int64_t)it.bx + (rows(it) > 0 ? wt : 0)) * kBlockM + lane;
@@ -153,7 +173,7 @@ struct Tile {
     // valid rows and live token tiles of this wave
     __device__ __forceinline__ int rows(const TileItem &it) const { return wt ? it.rows1 : it.rows0; }
     __device__ __forceinline__ int tiles(const TileItem &it) const {
-        return DUAL || (int64_t)it.nt * 256 + 128 * ww < N ? (rows(it) + 31) / 32 : 0;
+        return DUAL || first(it) + 128 * ww < N ? (rows(it) + 31) / 32 : 0;
     }
     // Two pieces of 8 KB of this wave's LDS: in A's slot 2 and B's slot 1,
     // which only its own DMAs fill (all landed after the K loop; no wave reads
@@ -221,7 +241,7 @@ struct Tile {
     template <int NTT, class F>
     __device__ __forceinline__ void out(const TileItem &it, f16x (&acc)[4][4], F &&fill) {
         const int ln = fresh(lane), lr = ln & 31, lh = ln >> 5, c = ln & 15;
-        const int64_t row0 = (int64_t)(it.bx + wt) * kBlockM, n0 = (int64_t)it.nt * 256 + 128 * ww;
+        const int64_t row0 = (int64_t)(it.bx + wt) * kBlockM, n0 = first(it) + 128 * ww;
         const int myrows = rows(it);
         keep_scales();
         fill();
@@ -256,38 +276,129 @@ struct Tile {
         }
     }
 
+    // a part's sums, 32 tokens of 64 columns at a time, staged as hidden rows
+    template <int NTT, class F>
+    __device__ __forceinline__ void sums(const TileItem &it, f16x (&acc)[4][4], F &&fill) {
+        const int ln = fresh(lane), lr = ln & 31, lh = ln >> 5, c = ln & 15;
+        const int64_t row0 = (int64_t)(it.bx + wt) * kBlockM, n0 = first(it) + 128 * ww;
+        const int myrows = rows(it);
+        int32_t *ybase = a.part + ((int64_t)part(it) * a.Tp + row0) * N + n0 + 4 * c;
+        fill();
+        unsigned char *st = piece(0);
+#pragma unroll
+        for (int u = 0; u < NTT; ++u)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                __builtin_amdgcn_sched_barrier(0);  // no accumulator is copied out early: registers
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        i32x4 v;
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) v[r] = bits_of(acc[2 * h + t][u][4 * q + r]);
+                        *(i32x4 *)(st + lr * 256 + (((8 * t + 2 * q + lh) ^ (lr & 15)) << 4)) = v;
+                    }
+                i32x4 v[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int r = 4 * j + (ln >> 4);
+                    v[j] = *(const i32x4 *)(st + r * 256 + ((c ^ (r & 15)) << 4));
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int row = 32 * u + 4 * j + (ln >> 4);
+                    if (row < myrows) *(i32x4 *)(ybase + (int64_t)row * N + 64 * h) = v[j];
+                }
+            }
+    }
+
     template <int NTT, class F>
     __device__ __forceinline__ bool finish(const TileItem &it, f16x (&acc)[4][4], F &&fill) {
         if constexpr (DUAL)
             hidden<NTT>(it, acc, fill);
+        else if constexpr (PART)
+            sums<NTT>(it, acc, fill);
         else
             out<NTT>(it, acc, fill);
-        return NTT == 4 && rows(it) == kBlockM;  // a whole block of rows: 32 stores
+        return NTT == 4 && rows(it) == kBlockM;  // a whole block of rows: 32 stores and more
     }
 };
 
-template <bool DUAL>
+template <int STAGE>
 __global__ __launch_bounds__(256) void i8_tile_kernel(I8Args a, int NT) {
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
-    Tile<DUAL> tile(a, smem);
+    Tile<STAGE> tile(a, smem);
     run_items(tile, a.gs, a.gpo, a.gidx, a.E, NT);
 }
 
-template <bool DUAL>
+// out from the parts' sums: 4 columns per thread, every gridDim.z'th row of
+// block y.
+__global__ __launch_bounds__(256) void i8_join_kernel(I8Args a) {
+    const BlockInfo bi = block_info(a.gs, a.gpo, a.gidx, a.E, blockIdx.y);
+    const int64_t c = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+    if (bi.rows == 0 || c >= a.N) return;
+    const f4 d = *(const f4 *)(a.w0s + (int64_t)bi.e * a.N + c);
+    const float *rw = a.rw + a.go[bi.e] + bi.token_offset;
+    for (int i = blockIdx.z; i < bi.rows; i += gridDim.z) {
+        const int64_t row = (int64_t)blockIdx.y * kBlockM + i;
+        const int32_t *p = a.part + row * a.N + c;
+        i32x4 v = *(const i32x4 *)p;
+#pragma unroll 4
+        for (int s = 1; s < a.splits; ++s) v += *(const i32x4 *)(p + s * a.Tp * a.N);
+        const float w = a.xs[row] * rw[i];
+        *(h4 *)(a.y + row * a.N + c) = to_h4((float)v[0] * (w * d[0]), (float)v[1] * (w * d[1]),
+                                             (float)v[2] * (w * d[2]), (float)v[3] * (w * d[3]));
+    }
+}
+
+template <int STAGE>
 hipError_t launch(const I8Args &a, int NT, hipStream_t s) {
     unsigned grid = 0;
     hipError_t e = cu_grid(grid);
     if (e != hipSuccess) return e;
     static std::atomic<uint64_t> lds_set{0};
-    e = lds_opt_in_once((const void *)i8_tile_kernel<DUAL>, LDS_BYTES, lds_set);
+    e = lds_opt_in_once((const void *)i8_tile_kernel<STAGE>, LDS_BYTES, lds_set);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(i8_tile_kernel<DUAL>, dim3(grid), dim3(256), LDS_BYTES, s, a, NT);
+    hipLaunchKernelGGL(i8_tile_kernel<STAGE>, dim3(grid), dim3(256), LDS_BYTES, s, a, NT);
     return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_i8_tile_gate_up(const I8Args &a, hipStream_t s) { return launch<true>(a, (int)(a.N / 128), s); }
-hipError_t launch_i8_tile_down(const I8Args &a, hipStream_t s) { return launch<false>(a, (int)((a.N + 255) / 256), s); }
+hipError_t launch_i8_tile_gate_up(const I8Args &a, hipStream_t s) { return launch<GATE_UP>(a, (int)(a.N / 128), s); }
+
+// Few experts and rows make few tiles of out, each a long sum, at 1 us or more
+// per step of 128 elements on its own CU.  K is cut into n parts where those
+// find free CUs, have 8 steps each and fit the room for their sums, and gain
+// more than the sums cost: a launch and the way out and back (8 us and 8 TB/s,
+// mostly in the caches).  One expert, 4096 x 14336, 256 rows: forward 176 ->
+// 112 us (n = 3); 1024 rows: 248 -> 213; one of 1024 x 4096, 1024 rows: 75 ->
+// 65 (n = 4); 4 of those, 2048 rows each, which stay whole: 48 us for the down
+// product, 55 in two parts.
+hipError_t launch_i8_tile_down(const I8Args &args, int64_t pairs, hipStream_t s) {
+    I8Args a = args;
+    unsigned cus = 0;
+    hipError_t e = cu_grid(cus);
+    if (e != hipSuccess) return e;
+    const int cols = (int)((a.N + 255) / 256);
+    const int64_t live = pairs < a.E ? pairs : a.E, full = (pairs + 255) / 256;  // items per column: at least
+    const int64_t items = (live > full ? live : full) * cols;
+    int n = 1;
+    double gain = 0.0;
+    for (int64_t i = 2; a.part != nullptr && i * items <= cus && i * a.N <= a.K && i * 8 * BK <= a.K; ++i) {
+        const double g = (double)(a.K / BK) * (1.0 - 1.0 / (double)i) - 8.0 - 1e-6 * (double)(i * pairs * a.N);
+        if (g > gain) {
+            gain = g;
+            n = (int)i;
+        }
+    }
+    if (n < 2) return launch<DOWN>(a, cols, s);
+    a.splits = n;
+    e = launch<DOWN_PART>(a, cols * n, s);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(i8_join_kernel, dim3((unsigned)((a.N + 1023) / 1024), (unsigned)a.M, 32), dim3(256), 0, s, a);
+    return hipGetLastError();
+}
 
 }  // namespace rmoe

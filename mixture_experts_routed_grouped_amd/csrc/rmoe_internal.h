@@ -191,12 +191,13 @@ struct I8Args {
     unsigned char *yc;                         // gate/up: their codes [Tp, N]
     float *ys;                                 // and scales [Tp]
     _Float16 *y;                               // down: out [Tp, N]
-    int64_t K, N;
-    int32_t E, M;
+    int32_t *part;                             // down, tiled: room for K / N parts of sums [Tp, N], or null
+    int64_t K, N, Tp;
+    int32_t E, M, splits;                      // splits: parts of K (set by the launch)
 };
 // The products of the gate/up stage write rows, the quantisation yc and ys.
 hipError_t launch_i8_tile_gate_up(const I8Args &a, hipStream_t s);
-hipError_t launch_i8_tile_down(const I8Args &a, hipStream_t s);
+hipError_t launch_i8_tile_down(const I8Args &a, int64_t pairs, hipStream_t s);
 hipError_t launch_i8_stream_gate_up(const I8Args &a, int64_t pairs, hipStream_t s);
 hipError_t launch_i8_stream_down(const I8Args &a, int64_t pairs, hipStream_t s);
 hipError_t launch_quantize_hidden_i8(const I8Args &a, int64_t pairs, hipStream_t s);

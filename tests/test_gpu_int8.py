@@ -322,6 +322,23 @@ def test_forward_is_its_stages(variant):
     assert torch.equal(ws[5 * n:].view(torch.float32)[rows], d["hs"][rows])
 
 
+@pytest.mark.parametrize("counts,H,I", [([40, 0, 130, 3], 128, 4096), ([256], 256, 2176), ([700], 384, 8320), ([1], 128, 16384),
+                                        ([300, 129], 1152, 2432), ([5, 0, 260], 640, 2048), ([128] * 9, 512, 3968)])
+def test_forward_in_parts_of_k(counts, H, I):
+    """Few tiles of out and a long K: the forward cuts the sums into parts,
+    whose results are those of the stage alone, which has no room for them."""
+    print(f"[int8] parts counts={counts} H={H} I={I}", flush=True)
+    d = _case(counts, H, I, seed=I)
+    _gate_up(d, "tile")
+    _down(d, "tile")
+    ws, out = _workspace(d), torch.full_like(d["out"].view(torch.int16), 0x7E5A).view(torch.float16)
+    for _ in range(2):
+        _forward(d, ws, out, "tile")
+    torch.cuda.synchronize()
+    assert torch.equal(out.view(torch.int16), d["out"].view(torch.int16))
+    _check(d)
+
+
 def test_families_agree_bit_for_bit():
     d = _case([60, 200, 9, 0, 128], 512, 384, seed=6)
     got = []
