@@ -137,6 +137,28 @@ def test_quantize_many_short_rows():
 
 
 # -------------------------------------------------------------------- pack
+@pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("cols", [8, 16, 24, 64, 72, 128, 136, 248, 256, 264, 504, 512, 520])
+def test_quantize_rows_that_share_a_wave(cols, dtype):
+    """One to 64 lanes per row; the last workgroup partly filled; rows of NaN,
+    zeros and the largest values beside others."""
+    kind = {"f16": torch.float16, "bf16": torch.bfloat16, "f32": torch.float32}[dtype]
+    g = torch.Generator(device="cuda").manual_seed(cols)
+    x = (torch.randn((515, cols), generator=g, device="cuda") * torch.exp(3 * torch.randn((515, 1), generator=g, device="cuda"))).to(kind)
+    x[3], x[8], x[9] = 0, torch.finfo(kind).max, -torch.finfo(kind).max
+    x[5, cols - 1], x[514, 0] = float("nan"), float("inf")
+    codes, scales = R.quantize_int8(x)
+    alone = [R.quantize_int8(x[r:r + 1]) for r in (0, 4, 6, 256, 513)]
+    torch.cuda.synchronize()
+    bad = torch.tensor([5, 514], device="cuda")
+    good = torch.ones(515, dtype=torch.bool, device="cuda")
+    good[bad] = False
+    _same(x[good], codes[good], scales[good])
+    assert scales[bad].isnan().all() and not codes[bad].any()
+    for r, (c, s) in zip((0, 4, 6, 256, 513), alone):
+        assert torch.equal(c[0], codes[r]) and torch.equal(s[0], scales[r])
+
+
 @pytest.mark.parametrize("T,k,H", [(1, 1, 8), (5, 3, 264), (130, 2, 512), (700, 8, 1408), (3, 40, 7168), (4, 2, 20000)])
 def test_pack(T, k, H):
     rng = np.random.default_rng(T)
