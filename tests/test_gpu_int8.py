@@ -390,6 +390,22 @@ def test_nan_and_zero_rows_stay_by_themselves(variant):
     assert not out[20].any()
 
 
+def test_corrupted_block_table_in_parts_of_k():
+    d = _case([300, 129], 256, 4096, seed=12)
+    _gate_up(d, "tile")
+    _down(d, "tile")
+    torch.cuda.synchronize()
+    want, blocks = d["out"].view(torch.int16).clone(), d["gidx"].clone()
+    for bad in (1, -1, 7, 2 ** 31 - 1):              # block 1 belongs to expert 0
+        d["gidx"].copy_(blocks)
+        d["gidx"][1] = bad
+        ws, out = _workspace(d), torch.full_like(want, 0x7E5A)
+        _forward(d, ws, out.view(torch.float16), "tile")
+        torch.cuda.synchronize()
+        assert (out[128:256] == 0x7E5A).all()
+        assert torch.equal(out[:128], want[:128]) and torch.equal(out[256:], want[256:])
+
+
 @pytest.mark.parametrize("variant", ["stream", "tile"])
 def test_corrupted_block_table_leaves_rows_unwritten(variant):
     d = _case([140, 20], 256, 128, seed=2)
@@ -436,6 +452,24 @@ def test_graph_replays_on_another_stream(variant):
         assert torch.equal(d["out"][rows].view(torch.int16), want.view(torch.int16)), i
         assert torch.equal(eager[rows].view(torch.int16), want.view(torch.int16)), i
         assert torch.equal(qc, wq[0]) and torch.equal(qs, wq[1]), i
+
+
+def test_graph_replays_in_parts_of_k():
+    d = _case([200, 64], 128, 4096, seed=13)
+    ws, out = _workspace(d), torch.full_like(d["out"].view(torch.int16), 0x7E5A).view(torch.float16)
+    _forward(d, ws, out, "tile")
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        _forward(d, ws, out, "tile")
+    for i in range(3):
+        d["codes"].copy_(d["codes"].roll(i + 1, 1))
+        graph.replay()
+        _gate_up(d, "stream")
+        _down(d, "stream")
+        torch.cuda.synchronize()
+        assert torch.equal(out.view(torch.int16), d["out"].view(torch.int16))
+        ws.fill_(0x11)
 
 
 def test_two_streams_at_once():
