@@ -85,7 +85,9 @@ __device__ __forceinline__ void router_body(const _Float16 *__restrict__ x, cons
                                             float *__restrict__ vals, const RouterTrainArgs &tr) {
     using C = RouterCfg<EP, TOK>;
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
-    const int64_t t0 = (int64_t)blockIdx.x * TOK;
+    const unsigned block = blockIdx.y * gridDim.x + blockIdx.x;  // grid_rows
+    const int64_t t0 = (int64_t)block * TOK;
+    if (t0 >= T) return;
     const int tid = threadIdx.x;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int lane = tid & 63, lr = lane & 31, lh = lane >> 5;
@@ -104,7 +106,7 @@ __device__ __forceinline__ void router_body(const _Float16 *__restrict__ x, cons
     // end (the same sums, the gate rows read once for both).
     const int nk = (int)(H / RT_CK);
     const int lag = TOK == 64 ? lag_ : 0, sweep = nk + lag;
-    const int kofs = (int)((blockIdx.x * (TOK == 64 && lag ? 14u : 7u)) % (unsigned)nk);
+    const int kofs = (int)((block * (TOK == 64 && lag ? 14u : 7u)) % (unsigned)nk);
     auto chunk = [&](int kc) -> int64_t {  // element offset; clamped at the end: repeats land in stages no later chunk reads
         kc = (kc < sweep ? kc : sweep - 1) + kofs;
         kc = kc < nk ? kc : kc - nk;
@@ -346,10 +348,10 @@ __device__ __forceinline__ void router_body(const _Float16 *__restrict__ x, cons
                 n += __shfl_xor(n, d);
             }
         }
-        if (gridDim.x > 1) {
-            if (tid < E) tr.parts[(int64_t)blockIdx.x * E + tid] = RouterPart{sum_p, cnt[tid]};
-            if (tid == 192) tr.tokens[blockIdx.x] = RouterPart{z, (int)n};
-            if (blockIdx.x == 0 && tid == 0) tr.losses[0] = 0.f;  // the next kernel counts there
+        if (T > TOK) {
+            if (tid < E) tr.parts[(int64_t)block * E + tid] = RouterPart{sum_p, cnt[tid]};
+            if (tid == 192) tr.tokens[block] = RouterPart{z, (int)n};
+            if (block == 0 && tid == 0) tr.losses[0] = 0.f;  // the next kernel counts there
         } else {  // the batch's only workgroup gives the losses itself
             double term = tid < E ? (double)sum_p * cnt[tid] : 0.0;
             if (tid < E) tr.counts[tid] = cnt[tid];
@@ -462,8 +464,8 @@ hipError_t launch_ep(const _Float16 *x, const _Float16 *w, int64_t T, int64_t H,
     static std::atomic<uint64_t> lds_set{0};
     hipError_t e = lds_opt_in_once((const void *)router_kernel<EP, TOK>, C::LDS_BYTES, lds_set);
     if (e != hipSuccess) return e;
-    const unsigned grid = (unsigned)((T + TOK - 1) / TOK);
-    hipLaunchKernelGGL((router_kernel<EP, TOK>), dim3(grid), dim3(320), C::LDS_BYTES, s, x, w, T, H,
+    const GridRows grid = grid_rows((T + TOK - 1) / TOK);
+    hipLaunchKernelGGL((router_kernel<EP, TOK>), dim3(grid.x, grid.y), dim3(320), C::LDS_BYTES, s, x, w, T, H,
                        E, k, lag, ids, vals);
     return hipGetLastError();
 }
@@ -474,8 +476,8 @@ hipError_t launch_train_ep(const RouterTrainArgs &a, hipStream_t s) {
     static std::atomic<uint64_t> lds_set{0};
     hipError_t e = lds_opt_in_once((const void *)router_train_kernel<EP, TOK>, C::LDS_BYTES, lds_set);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((router_train_kernel<EP, TOK>), dim3((unsigned)((a.T + TOK - 1) / TOK)), dim3(320), C::LDS_BYTES,
-                       s, a);
+    const GridRows grid = grid_rows((a.T + TOK - 1) / TOK);
+    hipLaunchKernelGGL((router_train_kernel<EP, TOK>), dim3(grid.x, grid.y), dim3(320), C::LDS_BYTES, s, a);
     return hipGetLastError();
 }
 

@@ -115,7 +115,8 @@ __global__ __launch_bounds__(1024) void dlogits_kernel(RouterBackArgs a, Scratch
     __shared__ float red[4][BT], big[4][BT], up_x[BT], up_w[256];
     __shared__ uint16_t on[4];
     const int tid = threadIdx.x, sub = tid & 3, tok = (tid >> 2) & 63, part = tid >> 8;
-    const int64_t b = blockIdx.x, t0 = b * BT, t = t0 + tok;
+    const int64_t b = (int64_t)blockIdx.y * gridDim.x + blockIdx.x, t0 = b * BT, t = t0 + tok;  // grid_rows
+    if (b >= s.nb) return;
     const bool live = t < a.T && (a.mask == nullptr || a.mask[t] != 0);
     const float n = (float)a.counts[a.E];
     const float ca = a.dlosses && n > 0.f ? a.dlosses[0] * (float)a.E / ((float)a.k * n * n) : 0.f;
@@ -607,7 +608,8 @@ hipError_t launch_router_backward(const RouterBackArgs &a, hipStream_t st) {
         static std::atomic<uint64_t> lds_set{0};
         hipError_t e = lds_opt_in_once((const void *)dlogits_kernel, BT * (256 + 4 + 2 * 32) * 4, lds_set);
         if (e != hipSuccess) return e;
-        hipLaunchKernelGGL(dlogits_kernel, dim3((unsigned)s.nb), dim3(1024), lds, st, a, s);
+        const GridRows grid = grid_rows(s.nb);
+        hipLaunchKernelGGL(dlogits_kernel, dim3(grid.x, grid.y), dim3(1024), lds, st, a, s);
         e = hipGetLastError();
         if (e != hipSuccess) return e;
         if (s.et <= GT) {

@@ -32,6 +32,19 @@ namespace rmoe {
 constexpr int kItemRows = 128;  // rows per contract block
 constexpr int kXcd = 8;         // MI355X: workgroups go round-robin over 8 XCDs
 
+// A launch of one workgroup per piece of its input (at most 1024 threads
+// each): rows of a two-dimensional grid.  A dimension holds fewer than 2^32
+// threads, and the host takes a larger one modulo 2^32 without an error.
+// Workgroup y gridDim.x + x takes that piece, those past the last one none.
+constexpr int64_t kGridRow = 1 << 21;
+struct GridRows {
+    unsigned x, y;
+};
+inline GridRows grid_rows(int64_t pieces) {
+    const int64_t x = pieces < kGridRow ? pieces : kGridRow;
+    return GridRows{(unsigned)x, (unsigned)((pieces + x - 1) / x)};
+}
+
 struct TileItem {
     int nt;     // weight slice
     int e;      // expert
