@@ -76,6 +76,139 @@ __device__ __forceinline__ void router_losses(double sum_pc, double z, int n, co
     a.losses[1] = n > 0 ? (float)(z / n) : 0.f;
 }
 
+// ---- softmax and top-k of the logits L: 4 consecutive lanes per token, lane
+// `sub` owns experts sub, sub + 4, ..., NE scores in registers.  NE is EP / 4,
+// but 2 for at most 8 experts, whose lanes would spend the time on scores that
+// do not exist (8 experts, inputs from HBM: 300000 tokens of H = 64 25.2 ->
+// 22.7 us, 300000 of 256 42.5 -> 40.6, 131072 of 1024 52.1 -> 50.7; 64 of
+// 4096 10.0 -> 9.5).
+template <int EP, int TOK, int NE, bool TRAIN>
+__device__ __forceinline__ void router_scores(float *L, unsigned block, int64_t t0, int64_t T, int32_t E, int32_t k,
+                                              int32_t *__restrict__ ids, float *__restrict__ vals,
+                                              const RouterTrainArgs &tr) {
+    using C = RouterCfg<EP, TOK>;
+    constexpr int LD = C::LD;
+    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
+    const int tok = tid >> 2, sub = tid & 3;
+    float *row = L + tok * LD;
+    float v[NE], m = -__builtin_inff();
+#pragma unroll
+    for (int i = 0; i < NE; ++i) {
+        v[i] = sub + 4 * i < E ? row[sub + 4 * i] : -__builtin_inff();
+        m = fmaxf(m, v[i]);
+    }
+    m = fmaxf(m, __shfl_xor(m, 1));
+    m = fmaxf(m, __shfl_xor(m, 2));
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < NE; ++i) {
+        v[i] = __builtin_amdgcn_exp2f((v[i] - m) * 1.4426950408889634f);
+        sum += v[i];
+    }
+    sum += __shfl_xor(sum, 1);
+    sum += __shfl_xor(sum, 2);
+    const float inv = 1.0f / sum;
+#pragma unroll
+    for (int i = 0; i < NE; ++i) v[i] *= inv;
+    const bool live = tok < TOK && t0 + tok < T;
+    // behind the logits: the workgroup's pairs per expert, and of each token
+    // lse^2 and whether it counts
+    static_assert(!TRAIN || C::LDS_BYTES >= (C::TROWS * LD + EP + 2 * TOK) * 4, "LDS behind the logits");
+    int32_t *cnt = reinterpret_cast<int32_t *>(L + C::TROWS * LD);
+    float *zs = reinterpret_cast<float *>(cnt + EP), *on = zs + TOK;
+    bool counts = live;
+    if constexpr (TRAIN) {
+        counts = live && (tr.mask == nullptr || tr.mask[t0 + tok] != 0);
+        __syncthreads();  // idle threads (tok >= TOK) have read their rows there
+        for (int e = tid; e < EP; e += 256) cnt[e] = 0;
+        if (tok < TOK) {
+#pragma unroll
+            for (int i = 0; i < NE; ++i) row[sub + 4 * i] = counts ? v[i] : 0.f;
+            if (sub == 0) {
+                const float lse = counts ? m + __builtin_amdgcn_logf(sum) * 0.6931471805599453f : 0.f;
+                zs[tok] = lse * lse;
+                on[tok] = counts ? 1.f : 0.f;
+                if (live) tr.lse[t0 + tok] = lse;
+            }
+        }
+        __syncthreads();
+    }
+#pragma unroll
+    for (int i = 0; i < NE; ++i) v[i] = sub + 4 * i < E ? v[i] : -2.f;
+    for (int j = 0; j < k; ++j) {
+        float bs = -1.f;
+        int be = 0x7fffffff;
+#pragma unroll
+        for (int i = 0; i < NE; ++i)
+            if (v[i] > bs) {  // in ascending order: the first of equal scores stays
+                bs = v[i];
+                be = sub + 4 * i;
+            }
+#pragma unroll
+        for (int d = 1; d <= 2; d <<= 1) {
+            const float os = __shfl_xor(bs, d);
+            const int oe = __shfl_xor(be, d);
+            if (better(os, oe, bs, be)) {
+                bs = os;
+                be = oe;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < NE; ++i) v[i] = be == sub + 4 * i ? -2.f : v[i];  // taken
+        if (live && sub == 0) {
+            if constexpr (TRAIN) {
+                ids[(t0 + tok) * k + j] = counts ? be : -1;
+                vals[(t0 + tok) * k + j] = counts ? bs : 0.f;
+                // a row of NaN picks no expert (be past E)
+                if (counts && be < E) atomicAdd(&cnt[be], 1);
+            } else {
+                ids[(t0 + tok) * k + j] = be;
+                vals[(t0 + tok) * k + j] = bs;
+            }
+        }
+    }
+    if constexpr (TRAIN) {
+        __syncthreads();
+        const int nt = T - t0 < TOK ? (int)(T - t0) : TOK;
+        for (int t = wave; t < nt; t += 4)
+            for (int e = lane; e < E; e += 64) tr.probs[(t0 + t) * E + e] = L[t * LD + e];
+        // sums over the workgroup's tokens, in a fixed order
+        float sum_p = 0.f, z = 0.f, n = 0.f;
+        if (tid < E) {
+#pragma unroll 8
+            for (int t = 0; t < nt; ++t) sum_p += L[t * LD + tid];
+        }
+        if (wave == 3) {  // zs and on hold TOK entries, zeros past the last token
+            z = lane < TOK ? zs[lane] : 0.f;
+            n = lane < TOK ? on[lane] : 0.f;
+#pragma unroll
+            for (int d = 1; d < 64; d <<= 1) {
+                z += __shfl_xor(z, d);
+                n += __shfl_xor(n, d);
+            }
+        }
+        if (T > TOK) {
+            if (tid < E) tr.parts[(int64_t)block * E + tid] = RouterPart{sum_p, cnt[tid]};
+            if (tid == 192) tr.tokens[block] = RouterPart{z, (int)n};
+            if (block == 0 && tid == 0) tr.losses[0] = 0.f;  // the next kernel counts there
+        } else {  // the batch's only workgroup gives the losses itself
+            double term = tid < E ? (double)sum_p * cnt[tid] : 0.0;
+            if (tid < E) tr.counts[tid] = cnt[tid];
+            for (int d = 1; d < 64; d <<= 1) term += __shfl_xor(term, d);
+            __syncthreads();  // the rows are done with
+            double *part = reinterpret_cast<double *>(L);
+            if (lane == 0) part[wave] = term;
+            if (tid == 192) {
+                part[4] = z;
+                part[5] = n;
+            }
+            __syncthreads();
+            if (tid == 0)
+                router_losses((part[0] + part[1]) + (part[2] + part[3]), part[4], (int)part[5], tr);
+        }
+    }
+}
+
 // TRAIN: the training forward, which also keeps the probabilities and each
 // token's logsumexp, leaves out masked tokens and sums what the losses need
 // over the workgroup's tokens.
@@ -247,127 +380,13 @@ __device__ __forceinline__ void router_body(const _Float16 *__restrict__ x, cons
         __syncthreads();
     }
 
-    // ---- softmax and top-k: 4 consecutive lanes per token, lane `sub` owns
-    //      experts sub, sub + 4, ..., in registers
-    constexpr int NE = EP / 4;
-    const int tok = tid >> 2, sub = tid & 3;
-    float *row = L + tok * LD;
-    float v[NE], m = -__builtin_inff();
-#pragma unroll
-    for (int i = 0; i < NE; ++i) {
-        v[i] = sub + 4 * i < E ? row[sub + 4 * i] : -__builtin_inff();
-        m = fmaxf(m, v[i]);
-    }
-    m = fmaxf(m, __shfl_xor(m, 1));
-    m = fmaxf(m, __shfl_xor(m, 2));
-    float sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < NE; ++i) {
-        v[i] = __builtin_amdgcn_exp2f((v[i] - m) * 1.4426950408889634f);
-        sum += v[i];
-    }
-    sum += __shfl_xor(sum, 1);
-    sum += __shfl_xor(sum, 2);
-    const float inv = 1.0f / sum;
-#pragma unroll
-    for (int i = 0; i < NE; ++i) v[i] *= inv;
-    const bool live = tok < TOK && t0 + tok < T;
-    // behind the logits: the workgroup's pairs per expert, and of each token
-    // lse^2 and whether it counts
-    static_assert(!TRAIN || C::LDS_BYTES >= (C::TROWS * LD + EP + 2 * TOK) * 4, "LDS behind the logits");
-    int32_t *cnt = reinterpret_cast<int32_t *>(L + C::TROWS * LD);
-    float *zs = reinterpret_cast<float *>(cnt + EP), *on = zs + TOK;
-    bool counts = live;
-    if constexpr (TRAIN) {
-        counts = live && (tr.mask == nullptr || tr.mask[t0 + tok] != 0);
-        __syncthreads();  // idle threads (tok >= TOK) have read their rows there
-        for (int e = tid; e < EP; e += 256) cnt[e] = 0;
-        if (tok < TOK) {
-#pragma unroll
-            for (int i = 0; i < NE; ++i) row[sub + 4 * i] = counts ? v[i] : 0.f;
-            if (sub == 0) {
-                const float lse = counts ? m + __builtin_amdgcn_logf(sum) * 0.6931471805599453f : 0.f;
-                zs[tok] = lse * lse;
-                on[tok] = counts ? 1.f : 0.f;
-                if (live) tr.lse[t0 + tok] = lse;
-            }
-        }
-        __syncthreads();
-    }
-#pragma unroll
-    for (int i = 0; i < NE; ++i) v[i] = sub + 4 * i < E ? v[i] : -2.f;
-    for (int j = 0; j < k; ++j) {
-        float bs = -1.f;
-        int be = 0x7fffffff;
-#pragma unroll
-        for (int i = 0; i < NE; ++i)
-            if (v[i] > bs) {  // in ascending order: the first of equal scores stays
-                bs = v[i];
-                be = sub + 4 * i;
-            }
-#pragma unroll
-        for (int d = 1; d <= 2; d <<= 1) {
-            const float os = __shfl_xor(bs, d);
-            const int oe = __shfl_xor(be, d);
-            if (better(os, oe, bs, be)) {
-                bs = os;
-                be = oe;
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < NE; ++i) v[i] = be == sub + 4 * i ? -2.f : v[i];  // taken
-        if (live && sub == 0) {
-            if constexpr (TRAIN) {
-                ids[(t0 + tok) * k + j] = counts ? be : -1;
-                vals[(t0 + tok) * k + j] = counts ? bs : 0.f;
-                // a row of NaN picks no expert (be past E)
-                if (counts && be < E) atomicAdd(&cnt[be], 1);
-            } else {
-                ids[(t0 + tok) * k + j] = be;
-                vals[(t0 + tok) * k + j] = bs;
-            }
+    if constexpr (EP == 32) {
+        if (E <= 8) {
+            router_scores<EP, TOK, 2, TRAIN>(L, block, t0, T, E, k, ids, vals, tr);
+            return;
         }
     }
-    if constexpr (TRAIN) {
-        __syncthreads();
-        const int nt = T - t0 < TOK ? (int)(T - t0) : TOK;
-        for (int t = wave; t < nt; t += 4)
-            for (int e = lane; e < E; e += 64) tr.probs[(t0 + t) * E + e] = L[t * LD + e];
-        // sums over the workgroup's tokens, in a fixed order
-        float sum_p = 0.f, z = 0.f, n = 0.f;
-        if (tid < E) {
-#pragma unroll 8
-            for (int t = 0; t < nt; ++t) sum_p += L[t * LD + tid];
-        }
-        if (wave == 3) {  // zs and on hold TOK entries, zeros past the last token
-            z = lane < TOK ? zs[lane] : 0.f;
-            n = lane < TOK ? on[lane] : 0.f;
-#pragma unroll
-            for (int d = 1; d < 64; d <<= 1) {
-                z += __shfl_xor(z, d);
-                n += __shfl_xor(n, d);
-            }
-        }
-        if (T > TOK) {
-            if (tid < E) tr.parts[(int64_t)block * E + tid] = RouterPart{sum_p, cnt[tid]};
-            if (tid == 192) tr.tokens[block] = RouterPart{z, (int)n};
-            if (block == 0 && tid == 0) tr.losses[0] = 0.f;  // the next kernel counts there
-        } else {  // the batch's only workgroup gives the losses itself
-            double term = tid < E ? (double)sum_p * cnt[tid] : 0.0;
-            if (tid < E) tr.counts[tid] = cnt[tid];
-            for (int d = 1; d < 64; d <<= 1) term += __shfl_xor(term, d);
-            __syncthreads();  // the rows are done with
-            double *part = reinterpret_cast<double *>(L);
-            if (lane == 0) part[wave] = term;
-            if (tid == 192) {
-                part[4] = z;
-                part[5] = n;
-            }
-            __syncthreads();
-            if (tid == 0)
-                router_losses((part[0] + part[1]) + (part[2] + part[3]), part[4], (int)part[5], tr);
-        }
-    }
+    router_scores<EP, TOK, EP / 4, TRAIN>(L, block, t0, T, E, k, ids, vals, tr);
 }
 
 template <int EP, int TOK>

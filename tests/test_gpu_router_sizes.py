@@ -1,9 +1,9 @@
-"""GPU tests of the router, its training forward and its backward pass at the
-token counts whose workgroups pass 2^32 threads in one dimension of a grid (the
+"""GPU tests of the router, its training forward and its backward pass at its
+fewest experts and at the token counts whose workgroups pass 2^32 threads in one dimension of a grid (the
 host takes such a launch modulo 2^32: rows were left unwritten and nothing was
 reported).
 
-Nearly all token rows are zero, so that every logit of theirs is 0: probability
+In the latter nearly all token rows are zero, so that every logit of theirs is 0: probability
 1 / E each, the first expert, lse = ln E.  Rows with values stand at the start,
 at the edge between two rows of the grid and at the end.
 
@@ -18,6 +18,7 @@ import pytest
 import torch
 
 import mixture_experts_routed_grouped_amd as R
+from test_gpu_router_train import _check_forward, _inputs
 
 pytestmark = pytest.mark.gpu
 ROW = 1 << 21                     # workgroups in a row of the grid
@@ -117,3 +118,20 @@ def test_backward_past_2_32_threads():
     # only the rows with values add to the gate matrix's gradient: at most 128 + 300 + 410 additions
     want, size = dl.T @ x[at].double(), dl.abs().T @ x[at].double().abs()
     assert ((dw.double() - want).abs() <= size * 2.0 ** -13).all()
+
+
+@pytest.mark.parametrize("H", [64, 576])
+@pytest.mark.parametrize("E", [1, 2, 5, 8, 9])
+@pytest.mark.parametrize("T", [77, 40003])
+def test_forward_of_few_experts(T, E, H):
+    """Up to 8 experts the lanes hold two scores each; every expert chosen."""
+    x, w, mask, xg, wg, mg = _inputs(T, E, H, T + E, 0.1)
+    got = R.router_train(xg, wg, E, token_mask=mg)
+    torch.cuda.synchronize()
+    _check_forward(got, x, w, E, mask)
+    x, w, _, xg, wg, _ = _inputs(T, E, H, T + E)
+    got = R.router_train(xg, wg, E)
+    ids, vals = R.router(xg, wg, E)
+    torch.cuda.synchronize()
+    _check_forward(got, x, w, E, None)
+    assert torch.equal(ids, got["topk_ids"]) and torch.equal(vals, got["topk_weights"])
