@@ -437,8 +437,9 @@ RMOE_API int rmoe_router_f16(const void *x, const void *router_w, int64_t num_to
  * token_mask [num_tokens] uint8 or NULL: tokens whose byte is 0 are left out
  * (the padding of a batch; their rows may hold anything): ids -1, weights,
  * probs and lse 0, in no count and no loss.  The contract builder leaves
- * pairs with id -1 out of its tables.  A token with a NaN logit gets the id
- * 2^31 - 1 (left out likewise), NaN probabilities and NaN losses.
+ * pairs with id -1 out of its tables.  A token with a NaN or +infinite logit
+ * gets the id 2^31 - 1 (left out likewise) with the weight -1, NaN probabilities
+ * and NaN losses.
  * scratch: rmoe_router_train_scratch_bytes(num_tokens, E) bytes, contents
  * irrelevant on entry.  Sums run in an order fixed by the sizes: equal calls
  * give equal bits.  Shapes: as rmoe_router_f16 with top_k >= 1, hidden at
@@ -650,9 +651,13 @@ RMOE_API int rmoe_pack_int8_f16(const void *x, const float *topk_weights, const 
  * scales [Tp]; contents irrelevant on entry.  Only valid rows of out, the codes
  * and the scales are written; the fp32 rows' space is scratch.  variant: RMOE_VARIANT_STREAM or _TILE (equal
  * results, bit for bit), or _AUTO for the choice of rmoe_pick_variant_int8.
+ * The scales' (and the routed weight's) product is taken first, in fp32, then
+ * multiplied with the sum: it must not overflow.
  * Codes, the weights' scales, workspace and out 16-byte aligned, the rest 4.
  * At most four launches on `stream` (with few experts and rows the down
  * product is cut into parts along I, which a launch of its own adds up).
+ * AUTO goes by the experts and the rows per expert, not by H and I: a caller
+ * who measures its shape may name the family.
  */
 RMOE_API size_t rmoe_int8_workspace_bytes(int64_t total_padded_tokens, int64_t intermediate);
 RMOE_API int rmoe_pick_variant_int8(int32_t variant, int64_t num_pairs, int32_t num_experts);
@@ -667,7 +672,9 @@ RMOE_API int rmoe_forward_int8(const void *token_codes, const float *token_scale
 
 /* Its stages alone.  rmoe_gate_up_int8 writes the hidden rows in fp32 into
  * hidden_rows [Tp, I] (scratch; 16-byte aligned), then their codes and scales
- * (two launches); rmoe_down_int8 reads those. */
+ * (two launches); rmoe_down_int8 reads those.  It has no room for sums of parts
+ * and never cuts the product along I: with few experts and rows it takes longer
+ * than the same stage inside rmoe_forward_int8 (the same bits). */
 RMOE_API int rmoe_gate_up_int8(const void *token_codes, const float *token_scales, const void *gate_codes,
                                const float *gate_scales, const void *up_codes, const float *up_scales,
                                const int32_t *group_sizes, const int32_t *group_padded_offsets,

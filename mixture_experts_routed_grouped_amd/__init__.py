@@ -1027,7 +1027,8 @@ def gate_up_int8(token_codes, token_scales, gate_codes, gate_scales, up_codes, u
 def down_int8(hidden_codes, hidden_scales, down_codes, down_scales, routed_expert_weights, group_sizes, group_offsets,
               group_padded_offsets, group_idx_for_bx, out, variant="auto", stream=None):
     """Stage 2 of ``forward_int8`` alone: out = fp16((hidden Wd^T) * w) on
-    valid rows."""
+    valid rows.  The same bits as inside it, but with few experts and rows more
+    time: it has no room for the sums of a product cut along I."""
     torch = _torch()
     i8, f32 = torch.int8, torch.float32
     dev = _gpu(out, "out")

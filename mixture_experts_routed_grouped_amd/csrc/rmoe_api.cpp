@@ -854,18 +854,30 @@ int check_i8_sizes(int32_t type, int64_t rows, int64_t cols, bool *empty) {
     return RMOE_OK;
 }
 
-// Streaming reads an expert's weights once per 64 rows of each of its blocks.
-// Forward times of both families (one MI355X, the tiled one's over the
-// streaming one's).  Equal groups of 64 and 96 rows: E=1 (4096, 14336) 1.06 and
-// 0.69, (1024, 4096) 1.30 and 1.17, (7168, 2048) 1.91 and 1.36; E=2 (4096,
-// 14336) 1.22 and 0.72, (2048, 8192) 1.07 and 0.75, (7168, 2048) 1.80 and 1.23;
-// E=4 (4096, 14336) 1.22 and 0.70, (1024, 4096) 1.13 and 0.87, (4096, 2048)
-// 1.61 and 1.13; E=8 (4096, 14336) 1.04 and 0.60.  Equal groups, then Zipf 1.2:
-// E=8 (4096, 14336) 1.22 and 0.91 at 48 rows; E=8 (2048, 5632) 1.48 and 1.19,
-// 1.34 and 1.03 at 64; E=16 (4096, 14336) 1.04 and 0.88 at 32, 0.98 and 0.81 at
-// 40; E=32 (4096, 2048) 1.23 and 1.34 at 40, 1.17 and 1.05 at 64; E=64 (2048,
-// 1408) 1.10 and 1.12, 1.09 and 1.04; E=128 (7168, 2048) 1.00 and 0.97, 0.96
-// and 0.81.
+// Streaming reads an expert's weights once per 64 rows of each of its blocks,
+// so its time jumps where groups pass 64 rows; the tiles leave CUs idle where
+// they are few.  The borders go by the experts and the rows per expert alone,
+// although shapes differ, and so weigh losses against each other.  Forward
+// times, the tiled family's over the streaming one's (one MI355X, weights from
+// HBM; above 1 streaming is faster).  Equal groups of 64, 80 and 128 rows:
+//   E=1  (4096, 14336) 1.41 0.95 0.85, (2048, 8192) 1.42 1.05 1.00,
+//        (1024, 4096) 1.25 1.04 1.10, (7168, 2048) 2.53 1.77 1.60
+//   E=2  (4096, 14336) 1.21 0.74 0.69, (2048, 8192) 1.24 0.91 0.86,
+//        (7168, 2048) 2.38 1.65 1.50
+//   E=4  (4096, 14336) 1.23 0.72 0.61, (1024, 4096) 1.24 0.99 0.85,
+//        (4096, 2048) 2.12 1.45 0.96
+// Equal groups of 40, 56 and 64 rows; Zipf 1.2 of 40, 56 and 64 on average:
+//   E=8  (4096, 14336) 1.09 1.03 1.05; 0.83 0.77 0.71
+//        (2048, 5632) 1.26 1.18 1.18; 1.06 0.97 0.89
+// Equal groups of 32, 40 and 64 rows; Zipf 1.2 of 32, 40 and 64:
+//   E=16  (4096, 14336) 1.04 0.99 0.94; 0.90 0.82 0.86
+//   E=32  (4096, 2048) 1.17 1.14 1.09; 1.24 1.22 0.94
+//   E=64  (2048, 1408) 1.14 1.09 1.08; 1.18 1.12 1.05
+//   E=128 (7168, 2048) 1.07 1.01 0.96; 1.03 0.96 0.81
+// What a border costs at most there: one expert of 4096 x 14336 with 128 rows
+// streams in 139 us (tiles 118); two of 7168 x 2048 with 80 rows take the tiles
+// in 104 us (streaming 63); 8 of 4096 x 14336 with 56 skewed rows stream in
+// 429 us (tiles 331).  A caller who knows its shape may name the family.
 int pick_variant_i8(int32_t variant, int64_t pairs, int32_t num_experts) {
     if (variant == RMOE_VARIANT_STREAM || variant == RMOE_VARIANT_TILE) return variant;
     const int64_t rows = num_experts == 1   ? 128

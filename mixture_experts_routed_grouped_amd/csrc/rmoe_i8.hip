@@ -9,7 +9,8 @@
 // used.  Rows longer than 64 W NV vectors are read twice, the second time
 // from the caches.  One wave per row needs no barrier and is taken once there
 // are several rows per CU; more waves shorten the one row that a small call
-// waits for.  Rows of at most 64 vectors are quantised several to a wave.
+// waits for.  Rows of at most 64 vectors go without these loops: up to 32
+// vectors several rows share a wave, from 33 on each has one.
 //
 // 8 x 14336 x 4096 bf16: 257 us there (5.5 TB/s), 229 back (6.2); 49152 hidden
 // rows of 1408 fp32 60 us (5.8 TB/s); the pack of 8192 tokens of 2048 to 6 rows
@@ -138,10 +139,11 @@ __global__ __launch_bounds__(256) void quantize_kernel(const void *__restrict__ 
     }
 }
 
-// Rows of up to 64 vectors: 1 << sh lanes each, the fewest that hold one, so
-// that a wave takes several; a wave for each row spends its time on starting
-// waves (54320 rows of 16 fp32 21.5 -> 2.6 us, 100000 of 64 fp16 39 -> 6,
-// 100000 of 512 46 -> 30).
+// Rows of up to 64 vectors: 1 << sh lanes each, the fewest that hold one.  Up
+// to 32 vectors a wave takes several rows, where a wave for each spent its time
+// on starting waves (54320 rows of 16 fp32 21.5 -> 2.6 us, 100000 of 64 fp16
+// 39 -> 6); from 33 on a row still has its wave, and what it gains it gains by
+// the straight body without quantize_row's loops (100000 of 512 46 -> 30).
 template <typename T>
 __global__ __launch_bounds__(256) void quantize_short_kernel(const void *__restrict__ x, int64_t rows, int vpr, int sh,
                                                              unsigned char *__restrict__ codes,

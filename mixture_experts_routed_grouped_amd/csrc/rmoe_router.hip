@@ -22,10 +22,12 @@
 // hold its scores in registers and take the row maximum, the exponential sum
 // and k rounds of arg-max (equal scores: lower expert index first), combining
 // with lane shuffles.  The gate matrix ([E, H], ~1.8 MB at E = 128, H = 7168)
-// stays in L2; x is read once, and HBM bounds large batches: 16384 tokens,
-// H = 7168, E = 128 take 67 us cold (3.5 TB/s), 4096 of them 33.  Small ones
-// are bound by the latency of their H / 64 chunks: 64 tokens, H = 4096, E = 8
-// take 10 us.
+// stays in L2; x is read once (counters: 265 MB for 235 and the gate rows; the
+// matrix cores busy 15% of the time), and HBM bounds large batches: 16384
+// tokens, H = 7168, E = 128 take 73 us with x from HBM (3.2 TB/s), 4096 of them
+// 45.  Small ones are bound by the latency of their H / 64 chunks: 64 tokens,
+// H = 4096, E = 8 take 11 us.  (Figures of the form a -> b in this file are
+// those of the step that they explain, on its own box.)
 // Measured and not kept: an 8-stage token ring with 3 stages of gate rows, so
 // fewer workgroups per CU (4096 tokens, H = 4096, E = 8: 15.7 against 12.2 us;
 // E = 64 up to 48 against 35; nothing gained elsewhere).
@@ -517,8 +519,8 @@ hipError_t cu_count(int &n) {
 }
 
 // Tokens per workgroup: 64 once that still gives two workgroups per CU; from
-// one per CU on, 64 as two lagging halves (16384 tokens, H = 7168, E = 128:
-// 94 -> 79 us) where workgroups of 32 do not split a chunk's K-steps, whose
+// one per CU on, 64 as two lagging halves (16384 tokens, H = 7168, E = 128,
+// training forward: 94 -> 79 us) where workgroups of 32 do not split a chunk's K-steps, whose
 // sums are another order.
 hipError_t tokens_per_workgroup(int64_t T, int64_t H, int32_t E, int &tok, int32_t &lag) {
     int cus = 0;

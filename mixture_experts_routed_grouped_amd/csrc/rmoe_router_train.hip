@@ -18,8 +18,8 @@
 //
 // Bound by memory: x is read once for dW, dx written once (and added to what
 // came through the experts, read once).  16384 tokens of 7168, 128 experts, an
-// eighth left out: 200 us, 188 of them dx and dW (720 MB: 3.8 TB/s, 150 us at a
-// copy's rate), dl 15, the sum of the parts 9.  8191 tokens of 2048, 64
+// eighth left out: 200 us, 188 of them dx and dW (752 MB by the counters: 4.0
+// TB/s, the matrix cores busy 28%), dl 15, the sum of the parts 9.  8191 tokens of 2048, 64
 // experts: 35 us (9 + 21 + 5), three launches of which each waits for its first
 // loads; 9 tokens of 256: 13 us, most of it the host's.
 #include <atomic>
@@ -522,10 +522,14 @@ __global__ __launch_bounds__(256) void dx_kernel(RouterBackArgs a, Scratch s, in
     dx_body<ET, ADD>(a, s, chunks, blockIdx.x, smem);
 }
 // Both in one launch, up to 4 expert tiles: workgroups 0 .. dws - 1 (a
-// multiple of 8) dW's, the others dx's, all of them at once, two per CU: dW
-// waits for its loads where dx stores.  Against a launch each: 16384 tokens of
-// 7168, 128 experts 217 -> 202 us for the whole pass, 4096 tokens of the same
-// 83 -> 73, 8191 tokens of 2048, 64 experts 39 -> 36, 9 tokens of 256 16 -> 12.
+// multiple of 8) dW's, the others dx's.  Up to 3 expert tiles two workgroups
+// fit a CU, all are there at once, and dW waits for its loads where dx stores.
+// With 4 (186 vector and 128 accumulation registers: one wave per SIMD) a CU
+// holds one: dW's go first and dx's follow as CUs fall free, which saves a
+// launch and the drain between the two, no more.  Against a launch each: 16384
+// tokens of 7168, 128 experts 217 -> 202 us for the whole pass, 4096 tokens of
+// the same 83 -> 73, 8191 tokens of 2048, 64 experts 39 -> 36, 9 tokens of 256
+// 16 -> 12.
 template <int ET, bool ADD>
 __global__ __launch_bounds__(256) void grads_kernel(RouterBackArgs a, Scratch s, int chunks, int dws) {
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
@@ -578,11 +582,11 @@ hipError_t launch_dw(const RouterBackArgs &a, const Scratch &s, int tile0, hipSt
 template <int ET, bool ADD>
 hipError_t launch_grads(const RouterBackArgs &a, const Scratch &s, hipStream_t st) {
     constexpr int LDS = DwCfg<ET, 4, 2>::LDS > DxCfg<ET>::LDS ? DwCfg<ET, 4, 2>::LDS : DxCfg<ET>::LDS;
-    static_assert(LDS <= 80 * 1024, "two workgroups per CU");
+    static_assert(LDS <= 80 * 1024, "LDS of two workgroups per CU");
     static std::atomic<uint64_t> lds_set{0};
     hipError_t e = lds_opt_in_once((const void *)grads_kernel<ET, ADD>, LDS, lds_set);
     if (e != hipSuccess) return e;
-    // all at once, two per CU
+    // 512 workgroups in all: two per CU (with 4 expert tiles one after the other)
     const int64_t dws = (s.slices * s.splits + 7) / 8 * 8, chunks = dx_chunks(a, s, 512 - dws), dxs = (s.slices * chunks + 7) / 8 * 8;
     hipLaunchKernelGGL((grads_kernel<ET, ADD>), dim3((unsigned)(dws + dxs)), dim3(256), LDS, st, a, s, (int)chunks, (int)dws);
     return hipGetLastError();

@@ -61,3 +61,21 @@ def test_forward_of_64_tokens_per_workgroup(per_cu, E, H):
     torch.cuda.synchronize()
     on = mg > 0
     assert torch.equal(ids[on], got["topk_ids"][on]) and torch.equal(vals[on], got["topk_weights"][on])
+
+
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+def test_forward_of_a_token_without_a_choice(value):
+    """A NaN or +infinite logit: no expert, the weight -1, NaN probabilities;
+    the other tokens as without it."""
+    _, _, _, xg, wg, _ = _inputs(70, 12, 128, 3)
+    wg[:, 3] = 0.5
+    plain = R.router_train(xg, wg, 3)
+    bad = xg.clone()
+    bad[5, 3] = value
+    got = R.router_train(bad, wg, 3)
+    torch.cuda.synchronize()
+    rest = [t for t in range(70) if t != 5]
+    assert (got["topk_ids"][5] == 2 ** 31 - 1).all() and (got["topk_weights"][5] == -1).all()
+    assert torch.isnan(got["probs"][5]).all() and torch.isnan(got["losses"]).all()
+    for n in ("topk_ids", "topk_weights", "probs", "lse"):
+        assert torch.equal(got[n][rest], plain[n][rest]), n
