@@ -1,11 +1,11 @@
 """GPU tests of the router, its training forward and its backward pass at its
-fewest experts and at the token counts whose workgroups pass 2^32 threads in one dimension of a grid (the
-host takes such a launch modulo 2^32: rows were left unwritten and nothing was
-reported).
+fewest experts and at the token counts whose workgroups pass 2^32 threads in
+one dimension of a grid (the host takes such a launch modulo 2^32: rows were
+left unwritten and nothing was reported).
 
-In the latter nearly all token rows are zero, so that every logit of theirs is 0: probability
-1 / E each, the first expert, lse = ln E.  Rows with values stand at the start,
-at the edge between two rows of the grid and at the end.
+In the latter nearly all token rows are zero, so that every logit of theirs is
+0: probability 1 / E each, the first expert, lse = ln E.  Rows with values
+stand at the start, at the edge between two rows of the grid and at the end.
 
 Tolerances, u = 2^-24: logits are whole multiples of 2^-15 below 2^9, exact in
 fp32; with D a row's largest distance of a logit from its maximum a
